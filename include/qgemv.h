@@ -57,9 +57,11 @@
  *     and mins, 128 bytes of 4-bit quants; weight = d*sc*q - dmin*m.
  *   Q8_0, 34 B per 32 weights: fp16 d, 32 int8 q; weight = d*q.
  *
- * Workspaces: only the LM-head entry points (lmhead_argmax, lmhead_argmax_verify,
+ * Workspaces: the LM-head entry points (lmhead_argmax, lmhead_argmax_verify,
  * lmhead_argmax_verify_q8_1, lmhead_topk) and logits_topk take one; each reports
- * the bytes it needs through its *_workspace_bytes query. A workspace must be
+ * the bytes it needs through its *_workspace_bytes query (so do
+ * qgemm_q4k_smalln_batch_ws, qgemm_i8 and logits_beam_select, whose rules stand at
+ * their declarations). A workspace of those LM-head and top-k calls must be
  * all-zero when first used (qg_workspace_clear, or any zero-filled allocation)
  * and every call leaves it all-zero again, so one workspace can serve every entry
  * point in turn. A call that fails on the device may leave it dirty: clear it
@@ -422,6 +424,147 @@ size_t lmhead_topk_workspace_bytes(int64_t M, int64_t K);
 qg_status lmhead_topk(const void* w_packed, const float* x, int64_t M, int64_t K, int k, float* logits,
                       const qg_sampler* sampler /* host, or NULL */, void* workspace, size_t workspace_bytes,
                       const qg_topk_out* out /* host */, qg_stream_t stream);
+
+/*
+ * Int8 products with one scale per weight row (channel) and one per activation row
+ * (token). The dotLLM README names integer activations (its news entries on Q8_1 /
+ * Q8_K input quantization) and the GPU backend's separate path for many columns;
+ * the pages give no format for either, so this one is the library's own:
+ *   y[n, m] = x_scale[n] * w_scale[m] * sum_k xq[n, k] * wq[m, k]  (+ bias[m])
+ * with int8 xq, wq and float32 scales. The sums are exact int32 (hence
+ * K <= QG_I8_MAX_K); each is converted to float32, multiplied by the rounded
+ * product of the two scales, the bias is added, all in float32, and the result is
+ * rounded once more when Y is fp16 or bf16. Any number of columns N >= 1: decode
+ * and verification columns, beams, prefill tokens. Matrices that share their
+ * activations (Q, K and V; gate and up) are one product over their rows stacked.
+ *
+ * qg_pack_i8 lays the weights out once, at load time: wq is row-major int8, M rows
+ * of K at stride ldw >= K bytes. The packed buffer has qg_i8_bytes(M, K) bytes: rows
+ * padded to 16 and K to 64 with zeros, and the 16 bytes k = 64 b + 16 g .. + 15 of
+ * row 16 t + i at ((t * ceil(K / 64) + b) * 64 + 16 g + i) * 16, which is the order
+ * of one wavefront's matrix-core operand. 1 <= M <= QG_I8_MAX_ROWS,
+ * 1 <= K <= QG_I8_MAX_K. wq needs no alignment; wq and dst must not overlap.
+ *
+ * qg_quantize_i8_rows quantizes N rows of K (row n at x + n * ldx elements) of
+ * fp32, fp16 or bf16, weights (per channel) or activations (per token) alike:
+ * scale[n] = max_k |x| / 127 rounded to float32; q[n, k] = x / scale[n] rounded to
+ * the nearest integer, ties to even, decided on the exact quotient and clamped to
+ * +-127 (0 where the scale is 0). Bytes K .. round_up(K, 64) - 1 of each row of q
+ * are set to 0; ldq >= round_up(K, 64), a multiple of 16, and bytes beyond are left
+ * as they are. A row that holds an infinity or NaN gets scale NaN and zeros, so that
+ * its products are NaN. ldx >= K; x needs the alignment of its elements only.
+ * 1 <= N <= QG_I8_MAX_ROWS; N * ldx and N * ldq at most 2^40.
+ *
+ * qgemm_i8: xq has rows of ldx >= round_up(K, 64) bytes, ldx a multiple of 16 (what
+ * lies between K and round_up(K, 64) may be anything: it meets zeros), Y rows of
+ * ldy >= M elements of type y_type, ldy a multiple of 4. Only Y[n, 0..M) is written.
+ * bias may be NULL. Results do not depend on how the work is split (the sums are
+ * integers). 1 <= N <= QG_I8_MAX_ROWS, M * N <= 2^32. Workspace:
+ * qgemm_i8_workspace_bytes(M, K, N) bytes (0: none needed; 0 too for an invalid
+ * shape), for the partial sums of products split along K; its contents need no
+ * preparation and are undefined afterwards. Calls that overlap must not share it.
+ */
+#define QG_F32 0
+#define QG_F16 1
+#define QG_BF16 2
+#define QG_I8_MAX_K 131071
+#define QG_I8_MAX_ROWS 4194303
+size_t qg_i8_bytes(int64_t M, int64_t K);
+qg_status qg_pack_i8(const void* wq, int64_t ldw, void* dst, int64_t M, int64_t K, qg_stream_t stream);
+qg_status qg_quantize_i8_rows(const void* x, int x_type, int64_t ldx, int64_t N, int64_t K, void* q, int64_t ldq,
+                              float* scale, qg_stream_t stream);
+size_t qgemm_i8_workspace_bytes(int64_t M, int64_t K, int64_t N);
+qg_status qgemm_i8(const void* w_packed, const float* w_scale, const void* xq, int64_t ldx, const float* x_scale,
+                   const float* bias, void* Y, int y_type, int64_t ldy, int64_t M, int64_t K, int64_t N,
+                   void* workspace, size_t workspace_bytes, qg_stream_t stream);
+
+/*
+ * Beam search's selection over beams and vocabulary, on the device, beside
+ * logits_topk (dotLLM README: log-softmax and top_logprobs; the pages decode greedily
+ * or by sampling only, and a beam step is the same ranking over several hypotheses).
+ * Logits: batch * beams rows of `vocab` values of logits_type at stride ld elements,
+ * row b * beams + w for beam w of item b. score[b * beams + w] is the beam's running
+ * log-probability. Candidates of item b:
+ *   a live beam: every token v, with
+ *     s = score + ((z_v - z_max) - log(sum_u exp(z_u - z_max)));
+ *   a finished beam (finished != NULL and nonzero): the token `eos` alone, s = score.
+ * s is computed in double precision. The n best candidates by s / max(len, 1)^length_penalty
+ * are written, best first, len being the hypothesis' length after the step
+ * (length + 1, of a finished beam length; length is needed only where length_penalty
+ * is not 0, and may be given otherwise). Equal ranks: the lower beam first, and in
+ * one beam the higher logit, then the lower token. No candidates: tokens whose
+ * logit is -inf or NaN (masked), and any of a beam whose score is -inf or NaN. A logit
+ * of +inf counts as the largest finite float. Outputs, batch * n each:
+ *   token, parent   the token and the beam (0 .. beams - 1) it extends (required)
+ *   score           s rounded to float32 (required)
+ *   finished        1 if the parent was finished or the token is eos, else 0 (or NULL)
+ *   length          len (NULL allowed; needs `length`)
+ * Where an item has fewer than n candidates, the remaining entries are token -1,
+ * parent -1, score -inf, finished 0, length 0. With n == beams, out->score,
+ * out->finished and out->length may be the input arrays themselves (a step in
+ * place); otherwise outputs must not overlap inputs.
+ * 1 <= n <= QG_BEAM_MAX_SELECT, 1 <= beams <= QG_BEAM_MAX, batch * beams <= 2^20,
+ * 1 <= vocab <= QG_TOPK_MAX_ROWS, ld >= vocab; eos in [0, vocab), or -1 for none
+ * (then finished must be NULL); length_penalty in [-16, 16]. The logits must be 16-byte
+ * aligned, rows need not be; the other arrays 4-byte (finished: 1). Workspace:
+ * logits_beam_select_workspace_bytes(...) bytes, no preparation needed, contents
+ * undefined afterwards; calls that overlap must not share it.
+ */
+#define QG_BEAM_MAX 32
+#define QG_BEAM_MAX_SELECT 64
+typedef struct {
+    const void* logits;
+    int logits_type;
+    int64_t ld;
+    int64_t batch;
+    int beams;
+    int64_t vocab;
+    const float* score;
+    const uint8_t* finished; /* or NULL */
+    const int32_t* length;   /* or NULL */
+    double length_penalty;
+    int32_t eos;
+} qg_beam_in;
+typedef struct {
+    int32_t* token;
+    int32_t* parent;
+    float* score;
+    uint8_t* finished;
+    int32_t* length;
+} qg_beam_out;
+size_t logits_beam_select_workspace_bytes(int logits_type, int64_t batch, int beams, int64_t vocab, int n);
+qg_status logits_beam_select(const qg_beam_in* in /* host */, int n, void* workspace, size_t workspace_bytes,
+                             const qg_beam_out* out /* host */, qg_stream_t stream);
+
+/*
+ * Reordering of the beams' states after a selection (keys and values, block tables,
+ * token histories), many tensors in one launch; the pages keep one KV cache per
+ * sequence (dotLLM README, paged KV cache), and a beam step needs its rows to follow
+ * their parents. For each state, item b and entry j:
+ *   dst row b * beams_out + j = src row b * beams_in + parent[b * beams_out + j].
+ * A row is `outer` pieces of `span` bytes at stride src_outer / dst_outer bytes; rows
+ * are src_row / dst_row bytes apart. dst == src moves in place (then beams_in ==
+ * beams_out and equal strides): rows whose parent is themselves are not touched, and
+ * every row is read before any is overwritten. Otherwise src and dst must not
+ * overlap. A parent outside [0, beams_in) leaves its dst row as it was. States of one
+ * call must not overlap each other's. A state's bytes are moved 16 at a time where its
+ * pointers, strides and span allow it, else 4, else singly; states need no alignment.
+ * 1 <= count <= QG_BEAM_MAX_STATES, 1 <= beams_in, beams_out <= QG_BEAM_MAX, 1 <= batch
+ * <= 65535; outer * span < 2^40, and less than 2^32 such units over one row of every
+ * state; strides in [0, 2^40], dst rows and pieces apart (the smaller stride at least
+ * a span, the larger at least all that the smaller steps over) and apart from parent.
+ * Work is split by alignment into at most three launches. No workspace.
+ */
+#define QG_BEAM_MAX_STATES 56
+typedef struct {
+    const void* src;
+    void* dst;
+    int64_t src_row, dst_row;
+    int64_t src_outer, dst_outer;
+    int64_t outer, span;
+} qg_beam_state;
+qg_status qg_beam_reorder(const qg_beam_state* states /* host */, int count, const int32_t* parent, int64_t batch,
+                          int beams_in, int beams_out, qg_stream_t stream);
 
 /*
  * Launch override, for tests and measurements only (not needed for correct

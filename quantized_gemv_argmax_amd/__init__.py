@@ -6,6 +6,7 @@ raises if the compiled library is missing: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -18,6 +19,10 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "qgemv.h")
 
 MAX_BATCH = 8
 SMALLN_MAX = 32
+I8_MAX_K = 131071
+BEAM_MAX = 32
+BEAM_MAX_SELECT = 64
+BEAM_MAX_STATES = 56
 
 _lib = None
 
@@ -66,6 +71,23 @@ class _Sampler(ctypes.Structure):
                 ("u", ctypes.c_void_p)]
 
 
+class _BeamIn(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_type", ctypes.c_int), ("ld", ctypes.c_int64),
+                ("batch", ctypes.c_int64), ("beams", ctypes.c_int), ("vocab", ctypes.c_int64),
+                ("score", ctypes.c_void_p), ("finished", ctypes.c_void_p), ("length", ctypes.c_void_p),
+                ("length_penalty", ctypes.c_double), ("eos", ctypes.c_int32)]
+
+
+class _BeamOut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("token", "parent", "score", "finished", "length")]
+
+
+class _BeamState(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_row", ctypes.c_int64),
+                ("dst_row", ctypes.c_int64), ("src_outer", ctypes.c_int64), ("dst_outer", ctypes.c_int64),
+                ("outer", ctypes.c_int64), ("span", ctypes.c_int64)]
+
+
 _P, _I64, _SZ, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
 
 _SIGS = {
@@ -108,6 +130,14 @@ _SIGS = {
                          _P]),
     "lmhead_argmax": (_I, [_P, _P, _I64, _I64, _P, _SZ, _P, _P, _P]),
     "lmhead_argmax_noalloc": (_I, [_P, _P, _I64, _I64, _P, _P, _P]),
+    "qg_i8_bytes": (_SZ, [_I64, _I64]),
+    "qg_pack_i8": (_I, [_P, _I64, _P, _I64, _I64, _P]),
+    "qg_quantize_i8_rows": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P]),
+    "qgemm_i8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "qgemm_i8": (_I, [_P, _P, _P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P, _SZ, _P]),
+    "logits_beam_select_workspace_bytes": (_SZ, [_I, _I64, _I, _I64, _I]),
+    "logits_beam_select": (_I, [ctypes.POINTER(_BeamIn), _I, _P, _SZ, ctypes.POINTER(_BeamOut), _P]),
+    "qg_beam_reorder": (_I, [ctypes.POINTER(_BeamState), _I, _P, _I64, _I, _I, _P]),
 }
 
 
@@ -576,3 +606,249 @@ def lmhead_topk(w: torch.Tensor, x: torch.Tensor, M: int, K: int, k: int, logits
     _check("lmhead_topk", lib().lmhead_topk(_ptr(w), _ptr(x), M, K, k, _ptr(logits), _sampler(sampler), ws.ptr(),
                                             ws.nbytes(), ctypes.byref(oc), _stream(x.device)))
     return out, logits
+
+
+# ------------------------------------------------------------------ int8 rows and products
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(device):
+    """Context in which `device` is the current one (kernels launch there)."""
+    return _HERE_ALREADY if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _check_tensor(name, t, dtypes, device=None, shape=None):
+    """A GPU tensor of one of `dtypes` on `device` with the given shape (None: any extent)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a tensor on the GPU")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    if shape is not None and (t.dim() != len(shape) or any(e is not None and e != g for e, g in zip(shape, t.shape))):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('any' if e is None else e for e in shape)}")
+
+
+def _row_stride(name, t):
+    """Row stride in elements of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _scratch(ws, need, device):
+    """(address, bytes) of a call's workspace: the caller's, grown if need be, or one of
+    the call's own, so that calls on several streams and captured graphs never share."""
+    if not need:
+        return None, 0, None
+    if ws is not None:
+        ws.ensure(need)
+        return ws.ptr(), ws.nbytes(), ws.buf
+    buf = torch.empty(need, dtype=torch.uint8, device=device)
+    return buf.data_ptr(), need, buf
+
+
+def i8_bytes(M: int, K: int) -> int:
+    return int(lib().qg_i8_bytes(M, K))
+
+
+def pack_i8(w: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Lay out row-major int8 weights (M, K), rows at any stride, for qgemm_i8
+    (uint8 buffer of i8_bytes(M, K) bytes)."""
+    _check_tensor("w", w, (torch.int8,))
+    ldw = _row_stride("w", w)
+    M, K = w.shape
+    n = i8_bytes(M, K)
+    if n == 0:
+        raise ValueError(f"no int8 layout for a {M} x {K} matrix")
+    if out is None:
+        out = torch.empty(n, dtype=torch.uint8, device=w.device)
+    _check_tensor("out", out, (torch.uint8,), w.device)
+    if out.numel() != n or not out.is_contiguous():
+        raise ValueError(f"out must be {n} contiguous bytes")
+    with _on(w.device):
+        _check("qg_pack_i8", lib().qg_pack_i8(_ptr(w), ldw, _ptr(out), M, K, _stream(w.device)))
+    return out
+
+
+def quantize_i8_rows(x: torch.Tensor, out: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """Int8 rows of x (N, K) in fp32, fp16 or bf16, a scale each (max|x| / 127):
+    tokens for qgemm_i8, or the rows of a weight matrix before pack_i8. Returns
+    (q int8 (N, ldq), scale float32 (N)), ldq = K rounded up to 64, zeros beyond K."""
+    _check_tensor("x", x, tuple(_TYPES))
+    ldx = _row_stride("x", x)
+    N, K = x.shape
+    kp = (K + 63) // 64 * 64
+    if out is None:
+        out = torch.empty((N, kp), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(N, dtype=torch.float32, device=x.device)
+    _check_tensor("out", out, (torch.int8,), x.device, (N, None))
+    _check_tensor("scale", scale, (torch.float32,), x.device, (N,))
+    if out.shape[1] < kp or not scale.is_contiguous():
+        raise ValueError(f"out needs rows of {kp} bytes, scale {N} contiguous numbers")
+    ldq = _row_stride("out", out)
+    with _on(x.device):
+        _check("qg_quantize_i8_rows", lib().qg_quantize_i8_rows(_ptr(x), _TYPES[x.dtype], ldx, N, K, _ptr(out), ldq,
+                                                                _ptr(scale), _stream(x.device)))
+    return out, scale
+
+
+def qgemm_i8_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().qgemm_i8_workspace_bytes(M, K, N))
+
+
+def qgemm_i8(w: torch.Tensor, w_scale: torch.Tensor, xq: torch.Tensor, x_scale: torch.Tensor, M: int, K: int,
+             bias: torch.Tensor | None = None, Y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+             ws: Workspace | None = None) -> torch.Tensor:
+    """Y[n, m] = x_scale[n] w_scale[m] sum_k xq[n, k] wq[m, k] (+ bias[m]) for weights
+    packed by pack_i8 and rows quantized by quantize_i8_rows. Returns Y (N, ldy) of
+    `dtype` (fp32, fp16 or bf16) with Y[:, :M] written. Without ws, a call that needs
+    a workspace (products split along K) allocates its own."""
+    _check_tensor("w", w, (torch.uint8,))
+    dev = w.device
+    _check_tensor("w_scale", w_scale, (torch.float32,), dev, (M,))
+    _check_tensor("xq", xq, (torch.int8,), dev, (None, None))
+    ldx = _row_stride("xq", xq)
+    N = xq.shape[0]
+    _check_tensor("x_scale", x_scale, (torch.float32,), dev, (N,))
+    if bias is not None:
+        _check_tensor("bias", bias, (torch.float32,), dev, (M,))
+    if w.numel() != i8_bytes(M, K) or not w.is_contiguous():
+        raise ValueError(f"w is not a packed {M} x {K} matrix")
+    if xq.shape[1] < (K + 63) // 64 * 64:
+        raise ValueError(f"xq needs rows of {(K + 63) // 64 * 64} bytes for K = {K}")
+    if not all(t is None or t.is_contiguous() for t in (w_scale, x_scale, bias)):
+        raise ValueError("w_scale, x_scale and bias must be contiguous")
+    if Y is None:
+        if dtype not in _TYPES:
+            raise ValueError(f"no output of type {dtype}")
+        Y = torch.empty((N, (M + 3) // 4 * 4), dtype=dtype, device=dev)
+    _check_tensor("Y", Y, tuple(_TYPES), dev, (N, None))
+    if Y.shape[1] < M:
+        raise ValueError(f"Y needs rows of {M} numbers")
+    ldy = _row_stride("Y", Y)
+    wp, wb, keep = _scratch(ws, qgemm_i8_workspace_bytes(M, K, N), dev)
+    with _on(dev):
+        _check("qgemm_i8", lib().qgemm_i8(_ptr(w), _ptr(w_scale), _ptr(xq), ldx, _ptr(x_scale), _ptr(bias), _ptr(Y),
+                                          _TYPES[Y.dtype], ldy, M, K, N, wp, wb, _stream(dev)))
+    return Y
+
+
+# ------------------------------------------------------------------ beam search
+class BeamSelection:
+    """Device outputs of logits_beam_select, (batch, n) each: token and parent (int32),
+    score (float32), finished (bool) and, if lengths were given, length (int32)."""
+
+    def __init__(self, batch: int, n: int, device, length: bool):
+        self.token = torch.empty((batch, n), dtype=torch.int32, device=device)
+        self.parent = torch.empty((batch, n), dtype=torch.int32, device=device)
+        self.score = torch.empty((batch, n), dtype=torch.float32, device=device)
+        self.finished = torch.empty((batch, n), dtype=torch.bool, device=device)
+        self.length = torch.empty((batch, n), dtype=torch.int32, device=device) if length else None
+
+
+def logits_beam_select(logits: torch.Tensor, score: torch.Tensor, n: int, finished: torch.Tensor | None = None,
+                       length: torch.Tensor | None = None, eos: int = -1, length_penalty: float = 0.0,
+                       out: BeamSelection | None = None, ws: Workspace | None = None) -> BeamSelection:
+    """The n best continuations of each batch item over its beams and the vocabulary.
+    logits (batch * beams, vocab), rows at any stride, fp32, fp16 or bf16; score (batch,
+    beams) float32; finished (batch, beams) bool; length (batch, beams) int32. `out` may
+    hold score, finished and length themselves when n is the number of beams (a step
+    in place). Ranking and special values as include/qgemv.h states."""
+    _check_tensor("logits", logits, tuple(_TYPES), shape=(None, None))
+    dev = logits.device
+    _check_tensor("score", score, (torch.float32,), dev, (None, None))
+    B, W = score.shape
+    V = logits.shape[1]
+    if logits.shape[0] != B * W:
+        raise ValueError(f"logits has {logits.shape[0]} rows for {B} x {W} scores")
+    ld = _row_stride("logits", logits)
+    out = out if out is not None else BeamSelection(B, n, dev, length is not None)
+    named = [("score", score, (torch.float32,), (B, W)), ("finished", finished, (torch.bool, torch.uint8), (B, W)),
+             ("length", length, (torch.int32,), (B, W)), ("out.token", out.token, (torch.int32,), (B, n)),
+             ("out.parent", out.parent, (torch.int32,), (B, n)), ("out.score", out.score, (torch.float32,), (B, n)),
+             ("out.finished", out.finished, (torch.bool, torch.uint8), (B, n)),
+             ("out.length", out.length, (torch.int32,), (B, n))]
+    for name, t, types, shape in named:
+        if t is not None:
+            _check_tensor(name, t, types, dev, shape)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    xt = _TYPES[logits.dtype]
+    need = int(lib().logits_beam_select_workspace_bytes(xt, B, W, V, n))
+    wp, wb, keep = _scratch(ws, need, dev)
+    ci = _BeamIn(_ptr(logits), xt, ld, B, W, V, _ptr(score), _ptr(finished), _ptr(length), length_penalty, eos)
+    co = _BeamOut(_ptr(out.token), _ptr(out.parent), _ptr(out.score), _ptr(out.finished), _ptr(out.length))
+    with _on(dev):
+        _check("logits_beam_select", lib().logits_beam_select(ctypes.byref(ci), n, wp, wb, ctypes.byref(co),
+                                                              _stream(dev)))
+    return out
+
+
+def _row_pieces(name, t):
+    """(row stride, piece stride, pieces, bytes of a piece) of a tensor whose rows (first
+    dimension) are equally spaced contiguous pieces."""
+    eb = t.element_size()
+    span, dims = 1, [(n, st) for n, st in zip(t.shape[1:], t.stride()[1:]) if n != 1]
+    while dims and dims[-1][1] == span:
+        span *= dims.pop()[0]
+    outer, step = 1, 0
+    while dims:
+        n, st = dims.pop()
+        if outer > 1 and st != outer * step:
+            raise ValueError(f"{name}: a row must be equally spaced contiguous pieces, got strides {t.stride()}")
+        step = step if outer > 1 else st
+        outer *= n
+    return t.stride(0) * eb, step * eb, outer, span * eb
+
+
+def beam_reorder(states, parent: torch.Tensor, out=None):
+    """Rows of every state follow their parents: row b * n + j of each result is row
+    b * beams + parent[b, j] of the state (first dimension batch * beams; parent int32
+    (batch, n); a parent outside [0, beams) leaves the result's row as it was). In place
+    without `out` (then n == beams), else into the tensors of `out`. States may be
+    views (a cache's filled part); returns the list of results."""
+    states = list(states)
+    results = states if out is None else list(out)
+    if not states:
+        raise ValueError("no states given")
+    _check_tensor("parent", parent, (torch.int32,), None, (None, None))
+    dev = parent.device
+    if not parent.is_contiguous() or len(results) != len(states):
+        raise ValueError("parent must be contiguous, and out as long as states")
+    B, n = parent.shape
+    if not B or not n or states[0].dim() < 1 or states[0].shape[0] % B:
+        raise ValueError(f"{tuple(parent.shape)} parents do not fit a state of shape {tuple(states[0].shape)}")
+    W = states[0].shape[0] // B
+    arr = (_BeamState * len(states))()
+    count = 0
+    for i, (s, d) in enumerate(zip(states, results)):
+        _check_tensor(f"states[{i}]", s, (getattr(s, "dtype", None),), dev)
+        _check_tensor(f"out[{i}]", d, (s.dtype,), dev)
+        if s.dim() < 1 or s.shape[0] != B * W or d.dim() != s.dim() or d.shape[0] != B * n or d.shape[1:] != s.shape[1:]:
+            raise ValueError(f"state {i}: shapes {tuple(s.shape)} and {tuple(d.shape)} for {B} x {W} beams and {n} parents")
+        if s.numel() == 0:  # nothing cached yet
+            continue
+        sr, so, outer, span = _row_pieces(f"states[{i}]", s)
+        dr, do, outer_d, span_d = (sr, so, outer, span) if d is s else _row_pieces(f"out[{i}]", d)
+        if (outer, span) != (outer_d, span_d):
+            # pieces of the finer of the two cuts
+            fine = min(span, span_d)
+            if max(span, span_d) % fine or (outer != 1 and outer_d != 1):
+                raise ValueError(f"state {i}: rows of state and result are cut into pieces that do not match")
+            if span > fine:
+                so, outer, span = fine, outer_d, fine
+            else:
+                do = fine
+        arr[count] = _BeamState(_ptr(s), _ptr(d), sr, dr, so, do, outer, span)
+        count += 1
+    with _on(dev):
+        for k in range(0, count, BEAM_MAX_STATES):
+            m = min(BEAM_MAX_STATES, count - k)
+            part = ctypes.cast(ctypes.addressof(arr) + k * ctypes.sizeof(_BeamState), ctypes.POINTER(_BeamState))
+            _check("qg_beam_reorder", lib().qg_beam_reorder(part, m, _ptr(parent), B, W, n, _stream(dev)))
+    return results
