@@ -455,9 +455,9 @@ qg_status lmhead_topk(const void* w_packed, const float* x, int64_t M, int64_t K
  * its products are NaN. ldx >= K; x needs the alignment of its elements only.
  * 1 <= N <= QG_I8_MAX_ROWS; N * ldx and N * ldq at most 2^40.
  *
- * qgemm_i8: xq has rows of ldx >= round_up(K, 64) bytes, ldx a multiple of 16 (what
- * lies between K and round_up(K, 64) may be anything: it meets zeros), Y rows of
- * ldy >= M elements of type y_type, ldy a multiple of 4. Only Y[n, 0..M) is written.
+ * qgemm_i8: xq has rows of ldx bytes, round_up(K, 64) <= ldx <= 2^22, a multiple of
+ * 16 (what lies between K and round_up(K, 64) may be anything: it meets zeros), Y rows
+ * of ldy >= M elements of type y_type, ldy a multiple of 4. Only Y[n, 0..M) is written.
  * bias may be NULL. Results do not depend on how the work is split (the sums are
  * integers). 1 <= N <= QG_I8_MAX_ROWS, M * N <= 2^32. Workspace:
  * qgemm_i8_workspace_bytes(M, K, N) bytes (0: none needed; 0 too for an invalid

@@ -8,6 +8,8 @@
 // (16 x 16 x 64, twice the fp16 rate) with the scales applied once, in the
 // epilogue. Integer sums are exact, so every split of K gives the same bits.
 #include <algorithm>
+#include <atomic>
+#include <climits>
 
 #include "qg_device.h"
 #include "qg_host.h"
@@ -210,48 +212,67 @@ struct GArgs {
     const float* bias;
     void* Y;
     int64_t ldy;
-    int32_t M, N, nb;  // nb: k blocks of 64
-    int32_t mtiles;
+    qi4* part;           // partial sums of a product split along K
+    int32_t M, N, nb;    // nb: k blocks of 64
+    int32_t mtiles;      // 16-row tiles of W
+    int32_t kper;        // K tiles (two blocks) of a split
 };
 
 QG_DEV float scaled(int acc, float xs, float ws, float b) { return (float)acc * (xs * ws) + b; }
 
-// Four consecutive outputs m .. m + 3 of column n.
 template <int YT>
-QG_DEV void store4(const GArgs& a, int64_t n, int m, qi4 acc) {
-    if (m >= a.M) return;
-    const float xs = a.xs[n];
-    float y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int r = min(m + e, a.M - 1);
-        y[e] = scaled(acc[e], xs, a.ws[r], a.bias ? a.bias[r] : 0.f);
-    }
+QG_DEV uint32_t pack2(float lo, float hi) {
+    if constexpr (YT == QG_F16)
+        return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) |
+               (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
+    else
+        return (uint32_t)f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
+}
+
+// C (4 or 8) consecutive outputs from element `at` of Y on, `count` of them inside
+// the row (rows are at least four elements aligned).
+template <int YT, int C>
+QG_DEV void store_row(void* Y, int64_t at, const float (&y)[C], int count) {
     if constexpr (YT == QG_F32) {
-        float* p = reinterpret_cast<float*>(a.Y) + n * a.ldy + m;
-        if (m + 4 <= a.M) {
-            *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
+        float* p = reinterpret_cast<float*>(Y) + at;
+        if (count >= C) {
+#pragma unroll
+            for (int c = 0; c < C / 4; ++c)
+                reinterpret_cast<float4*>(p)[c] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (m + e < a.M) p[e] = y[e];
+            for (int e = 0; e < C; ++e)
+                if (e < count) p[e] = y[e];
         }
     } else {
-        uint16_t h[4];
+        uint16_t* p = reinterpret_cast<uint16_t*>(Y) + at;
+        uint32_t h[C / 2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            h[e] = YT == QG_F16 ? __builtin_bit_cast(uint16_t, (_Float16)y[e]) : f32_to_bf16(y[e]);
-        uint16_t* p = reinterpret_cast<uint16_t*>(a.Y) + n * a.ldy + m;
-        if (m + 4 <= a.M) {
-            *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+        for (int e = 0; e < C / 2; ++e) h[e] = pack2<YT>(y[2 * e], y[2 * e + 1]);
+        if (count >= C) {
+#pragma unroll
+            for (int c = 0; c < C / 4; ++c) reinterpret_cast<uint2*>(p)[c] = make_uint2(h[2 * c], h[2 * c + 1]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (m + e < a.M) p[e] = h[e];
+            for (int e = 0; e < C; ++e)
+                if (e < count) p[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
         }
     }
 }
 
+// The scales (and biases) of C consecutive weight rows from m on, rows beyond M
+// repeating the last one.
+template <int C>
+QG_DEV void row_scales(const GArgs& a, int m, float (&sw)[C], float (&sb)[C]) {
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+        const int r = min(m + e, a.M - 1);
+        sw[e] = a.ws[r];
+        sb[e] = a.bias ? a.bias[r] : 0.f;
+    }
+}
+
+// ---------------------------------------------------------------- few columns
 // One 16-row tile and NB blocks of 16 columns per workgroup; its KW wavefronts take
 // the k blocks in turn, and their integer sums meet in LDS. The weights go from
 // memory straight to the operand registers, in the packed order.
@@ -259,13 +280,12 @@ template <int YT, int NB, int KW>
 __global__ __launch_bounds__(64 * KW) void gemm_i8_stream_kernel(GArgs a) {
     __shared__ qi4 part[KW][NB][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int t = blockIdx.x % a.mtiles;
-    const int n0 = blockIdx.x / a.mtiles * (NB * 16);
+    const int t = blockIdx.x;
     const uint8_t* w = a.w + ((size_t)t * a.nb) * kTileB + lane * 16;
     const int8_t* xr[NB];
 #pragma unroll
     for (int c = 0; c < NB; ++c)  // columns beyond N read the last one; their sums are not stored
-        xr[c] = a.x + (int64_t)min(n0 + 16 * c + (lane & 15), a.N - 1) * a.ldx + (lane >> 4) * 16;
+        xr[c] = a.x + (int64_t)min(16 * c + (lane & 15), a.N - 1) * a.ldx + (lane >> 4) * 16;
     qi4 acc[NB];
 #pragma unroll
     for (int c = 0; c < NB; ++c) acc[c] = qi4{0, 0, 0, 0};
@@ -281,26 +301,315 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_stream_kernel(GArgs a) {
 #pragma unroll
     for (int c = 0; c < NB; ++c) part[wave][c][lane] = acc[c];
     __syncthreads();
-    for (int c = wave; c < NB; c += KW) {
+    if (wave < NB) {
+        const int c = wave;
         qi4 s = part[0][c][lane];
 #pragma unroll
         for (int k = 1; k < KW; ++k) s += part[k][c][lane];
-        const int n = n0 + 16 * c + (lane & 15);
-        if (n < a.N) store4<YT>(a, n, t * T + (lane >> 4) * 4, s);
+        const int n = 16 * c + (lane & 15), m = t * T + (lane >> 4) * 4;
+        if (n < a.N && m < a.M) {
+            float sw[4], sb[4], y[4];
+            row_scales(a, m, sw, sb);
+            const float xs = a.xs[n];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = scaled(s[e], xs, sw[e], sb[e]);
+            store_row<YT>(a.Y, n * a.ldy + m, y, a.M - m);
+        }
     }
 }
 
-template <int YT>
-qg_status launch_gemm(const GArgs& a, hipStream_t s) {
-    const int nblk = (int)qg::ceil_div(a.N, 16);
-    if (nblk <= 1) {
-        hipLaunchKernelGGL((gemm_i8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
-    } else if (nblk <= 2) {
-        hipLaunchKernelGGL((gemm_i8_stream_kernel<YT, 2, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
-    } else {
-        const int64_t g = (int64_t)a.mtiles * qg::ceil_div(nblk, 4);
-        hipLaunchKernelGGL((gemm_i8_stream_kernel<YT, 4, 8>), dim3((unsigned)g), dim3(512), 0, s, a);
+// ---------------------------------------------------------------- many columns
+// Y in tiles of BM weight rows x BN columns, one per workgroup of WM x WN
+// wavefronts, K in tiles of 128 bytes through two LDS buffers.
+template <int BM, int BN, int WM, int WN>
+struct Tile {
+    static constexpr int W = WM * WN;
+    static constexpr int MT = BM / WM / 16, CT = BN / WN / 16;    // 16 x 16 products of a wavefront
+    static constexpr int AB = BM * 128, XB = BN * 128, STAGE = AB + XB, LDS = 2 * STAGE;
+    static constexpr int AU = AB / 1024 / W, XU = XB / 1024 / W;  // 1 KB loads of a wavefront
+    static_assert(MT % 2 == 0 && AU * 1024 * W == AB && XU * 1024 * W == XB, "tile does not split evenly");
+};
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// 1 KB from memory to LDS, 16 bytes a lane, lanes in order from dst on.
+QG_DEV void lds_load(const __amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff, int soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, voff, soff, 0, 0);
+}
+
+// Every wavefront's loads have arrived and its LDS reads are done, for all of them.
+QG_DEV void tile_sync() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Outputs of a wavefront's accumulators. Product i of a pair (2c, 2c + 1) holds in its
+// row 4 q + e the weight row 32 c + 8 q + 4 (i % 2) + e, so a lane's pair is eight
+// consecutive outputs and four lanes' pairs are 32.
+template <int YT, int CT>
+QG_DEV void store_pair(const GArgs& a, const qi4 (&lo)[CT], const qi4 (&hi)[CT], int m, int n0) {
+    const int count = a.M - m;
+    if (count <= 0) return;
+    float sw[8], sb[8];
+    row_scales(a, m, sw, sb);
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+        const int n = n0 + 16 * j;
+        if (n < a.N) {
+            const float xs = a.xs[n];
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[e] = scaled(lo[j][e], xs, sw[e], sb[e]);
+                y[4 + e] = scaled(hi[j][e], xs, sw[4 + e], sb[4 + e]);
+            }
+            store_row<YT>(a.Y, n * a.ldy + m, y, count);
+        }
     }
+}
+
+// Tile of workgroup id: eight XCDs take the tiles in eight contiguous runs, and in a
+// run groups of eight tile rows walk the columns together, so that the tiles an XCD
+// works on at a time share their weights and activations in its L2.
+struct TileAt {
+    int t0, n0;  // first 16-row tile, first column
+};
+template <int BM, int BN>
+QG_DEV TileAt tile_at(const GArgs& a, int id) {
+    const int mts = (a.mtiles * 16 + BM - 1) / BM, nts = (a.N + BN - 1) / BN;
+    const int total = mts * nts, q = total / 8, r = total % 8, x = id % 8;
+    id = x * q + min(x, r) + id / 8;
+    constexpr int GM = 8;
+    const int per = GM * nts, grp = id / per, rem = id - grp * per;
+    const int gm = min(GM, mts - grp * GM);
+    return {(grp * GM + rem % gm) * (BM / 16), rem / gm * BN};
+}
+
+template <int YT, int BM, int BN, int WM, int WN, bool SPLIT>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
+    typedef Tile<BM, BN, WM, WN> G;
+    extern __shared__ __align__(1024) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const TileAt at = tile_at<BM, BN>(a, blockIdx.x);
+    const int t0 = at.t0, n0 = at.n0;
+    const int k0 = SPLIT ? blockIdx.y * a.kper : 0;
+    const int k1 = SPLIT ? min((a.nb + 1) / 2, k0 + a.kper) : (a.nb + 1) / 2;
+
+    // Loads: rows and tiles beyond the operands repeat the last ones (their sums are
+    // not stored). Weights arrive in the packed order. Activations: eight lanes per row
+    // of 128 bytes, the 16-byte chunk c of row r at place c ^ (r % 8), which spreads
+    // the operand reads over the banks.
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(a.w + (size_t)t0 * a.nb * kTileB), (short)0,
+        (int)min((int64_t)(a.mtiles - t0) * a.nb * kTileB, (int64_t)INT32_MAX), kQgRawBufferFlags);
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(a.x + n0 * a.ldx), (short)0,
+        (int)min((int64_t)(a.N - 1 - n0) * a.ldx + a.nb * kKB, (int64_t)INT32_MAX), kQgRawBufferFlags);
+    uint32_t woff[G::AU], xoff[G::XU];
+#pragma unroll
+    for (int u = 0; u < G::AU; ++u)
+        woff[u] = (uint32_t)min((wave * G::AU + u) >> 1, a.mtiles - 1 - t0) * (uint32_t)a.nb * kTileB + lane * 16u;
+    const int chunk = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+    for (int u = 0; u < G::XU; ++u)
+        xoff[u] = (uint32_t)min((wave * G::XU + u) * 8 + (lane >> 3), a.N - 1 - n0) * (uint32_t)a.ldx + chunk * 16u;
+    // an odd last block: its row ends after half of the 128 bytes, the lanes of the
+    // other half read the first one again (and no product uses what they read)
+    const uint32_t back = chunk >= 4 ? 64u : 0u;
+    auto fetch = [&](int t, int buf) {
+        uint8_t* A = lds + buf * G::STAGE;
+        uint8_t* X = A + G::AB;
+#pragma unroll
+        for (int u = 0; u < G::AU; ++u) {
+            const int unit = wave * G::AU + u;
+            lds_load(wr, A + unit * 1024, woff[u], min(2 * t + (unit & 1), a.nb - 1) * kTileB);
+        }
+        const uint32_t sub = 2 * t + 1 < a.nb ? 0u : back;
+#pragma unroll
+        for (int u = 0; u < G::XU; ++u) lds_load(xr, X + (wave * G::XU + u) * 1024, xoff[u] - sub, t * 128);
+    };
+
+    const int wm = wave % WM, wn = wave / WM;
+    const int r = lane & 15, q = lane >> 4;
+    qi4 acc[G::MT][G::CT];
+#pragma unroll
+    for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+        for (int j = 0; j < G::CT; ++j) acc[i][j] = qi4{0, 0, 0, 0};
+    const int arow = (wm * G::MT + (r >> 3)) * 2048 + (q * 16 + ((r >> 2) & 1) * 8 + (r & 3)) * 16;
+    const int xrow = (wn * G::CT * 16 + r) * 128;
+    auto frags = [&](int buf, int h, qi4(&fa)[G::MT], qi4(&fx)[G::CT]) {
+        const uint8_t* A = lds + buf * G::STAGE + arow + h * 1024;
+        const uint8_t* X = lds + buf * G::STAGE + G::AB + xrow + (((h * 4 + q) ^ (r & 7)) * 16);
+#pragma unroll
+        for (int j = 0; j < G::CT; ++j) fx[j] = *reinterpret_cast<const qi4*>(X + j * 2048);
+#pragma unroll
+        for (int i = 0; i < G::MT; ++i) fa[i] = *reinterpret_cast<const qi4*>(A + (i >> 1) * 4096 + (i & 1) * 64);
+    };
+    auto mma = [&](const qi4(&fa)[G::MT], const qi4(&fx)[G::CT]) {
+#pragma unroll
+        for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[i], fx[j], acc[i][j], 0, 0, 0);
+    };
+
+    // One barrier per K tile, between its two halves: the second half's operands are in
+    // registers then, so its buffer can be refilled, and the next tile's loads, sent a
+    // whole tile earlier, have arrived.
+    qi4 a0[G::MT], x0[G::CT], a1[G::MT], x1[G::CT];
+    fetch(k0, 0);
+    tile_sync();
+    if (k0 + 1 < k1) fetch(k0 + 1, 1);
+    frags(0, 0, a0, x0);
+    int t = k0, buf = 0;
+    for (; t + 2 < k1; ++t, buf ^= 1) {
+        frags(buf, 1, a1, x1);
+        mma(a0, x0);
+        tile_sync();
+        frags(buf ^ 1, 0, a0, x0);
+        fetch(t + 2, buf);
+        mma(a1, x1);
+    }
+    if (t + 1 < k1) {
+        frags(buf, 1, a1, x1);
+        mma(a0, x0);
+        tile_sync();
+        frags(buf ^ 1, 0, a0, x0);
+        mma(a1, x1);
+        ++t;
+        buf ^= 1;
+    }
+    frags(buf, 1, a1, x1);
+    mma(a0, x0);
+    if (2 * t + 1 < a.nb) mma(a1, x1);
+
+    if constexpr (SPLIT) {
+        qi4* p = a.part + ((((size_t)blockIdx.y * gridDim.x + blockIdx.x) * G::W + wave) * (G::MT * G::CT)) * 64 + lane;
+#pragma unroll
+        for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j) p[(i * G::CT + j) * 64] = acc[i][j];
+    } else {
+#pragma unroll
+        for (int c = 0; c < G::MT / 2; ++c)
+            store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], (t0 + wm * G::MT + 2 * c) * 16 + q * 8,
+                                  n0 + wn * G::CT * 16 + r);
+    }
+}
+
+// The partial sums of a split product added and stored: one wavefront per pair of
+// a tile wavefront's products.
+template <int YT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64) void gemm_i8_join_kernel(GArgs a, int tiles, int splits) {
+    typedef Tile<BM, BN, WM, WN> G;
+    const int lane = threadIdx.x;
+    const int c = blockIdx.x % (G::MT / 2), wave = blockIdx.x / (G::MT / 2) % G::W;
+    const int id = blockIdx.x / (G::MT / 2 * G::W);
+    const TileAt at = tile_at<BM, BN>(a, id);
+    const int wm = wave % WM, wn = wave / WM, r = lane & 15, q = lane >> 4;
+    const qi4* p = a.part + (((size_t)id * G::W + wave) * (G::MT * G::CT) + 2 * c * G::CT) * 64 + lane;
+    const size_t step = (size_t)tiles * G::W * (G::MT * G::CT) * 64;
+    qi4 lo[G::CT], hi[G::CT];
+#pragma unroll
+    for (int j = 0; j < G::CT; ++j) lo[j] = hi[j] = qi4{0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s, p += step)
+#pragma unroll
+        for (int j = 0; j < G::CT; ++j) {
+            lo[j] += p[j * 64];
+            hi[j] += p[(G::CT + j) * 64];
+        }
+    store_pair<YT, G::CT>(a, lo, hi, (at.t0 + wm * G::MT + 2 * c) * 16 + q * 8, at.n0 + wn * G::CT * 16 + r);
+}
+
+// ---------------------------------------------------------------- launches
+// How a product runs: N <= 32 streams the weights past the columns; else a tile form,
+// perhaps split along K.
+enum { FORM_STREAM, FORM_64, FORM_128, FORM_256 };
+struct Plan {
+    int form, tiles, splits, kper;
+    size_t ws;
+};
+
+// The largest tile that still gives most compute units one, larger tiles reading the
+// operands less often: 37888 x 3584 by 4096 columns takes 534 us in tiles of 256 and
+// 1094 in tiles of 64; 18944 x 3584 by 256 takes 36.0 us in 296 tiles of 128 and 45.3
+// in 74 of 256 split three ways. With fewer tiles K is split until about 448
+// workgroups share it, each keeping at least 7 K tiles (14 of the larger ones) to repay
+// the second launch:
+// 3584 x 18944 by 64 columns takes 24.7 us in 8 splits and 33.9 in 4; 4608 x 3584 by
+// 64 12.2 in 4 and 13.4 in 7. Tiles of 128 are split where K is long (3584 x 18944 by
+// 256: 42.4 us, tiles of 64 46.4), tiles of 64 where it is not (4608 x 3584 by 512:
+// 19.8 us in 576 tiles, 23.4 in 144 of 128 split three ways).
+Plan plan(int64_t M, int64_t K, int64_t N) {
+    Plan p{};
+    const int kt = (int)qg::ceil_div(K, 2 * kKB);
+    p.splits = 1;
+    p.kper = kt;
+    if (N <= 32) {
+        p.form = FORM_STREAM;
+        p.tiles = (int)qg::ceil_div(M, T);
+        return p;
+    }
+    auto tiles = [&](int b) { return qg::ceil_div(M, b) * qg::ceil_div(N, b); };
+    int side = 64;
+    if (N > 64 && tiles(256) >= 192)
+        side = 256;
+    else if (N > 64 && (tiles(128) >= 192 || kt >= 64))
+        side = 128;
+    p.form = side == 256 ? FORM_256 : side == 128 ? FORM_128 : FORM_64;
+    p.tiles = (int)tiles(side);
+    const int s = side == 256 ? 1 : (int)std::min<int64_t>({448 / tiles(side), kt / (side == 128 ? 14 : 7), 16});
+    if (s > 1) {
+        p.kper = (int)qg::ceil_div(kt, s);
+        p.splits = (int)qg::ceil_div(kt, p.kper);
+    }
+    if (p.splits > 1) p.ws = (size_t)p.splits * p.tiles * side * side * 4;
+    return p;
+}
+
+// Allows a kernel more than 64 KB of LDS, once per device.
+qg_status allow_lds(const void* f, int bytes, std::atomic<bool>* done) {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return qg::fail(QG_ERR_DEVICE, "no current device");
+    if (done[dev].load(std::memory_order_acquire)) return QG_OK;
+    const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return qg::fail(QG_ERR_DEVICE, "LDS size: %s", hipGetErrorString(e));
+    done[dev].store(true, std::memory_order_release);
+    return QG_OK;
+}
+
+template <int YT, int B, int WM, int WN>
+qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
+    typedef Tile<B, B, WM, WN> G;
+    if constexpr (G::LDS > 65536) {
+        static std::atomic<bool> done[64];
+        const qg_status st =
+            allow_lds(reinterpret_cast<const void*>(&gemm_i8_tile_kernel<YT, B, B, WM, WN, false>), G::LDS, done);
+        if (st) return st;
+    } else if (p.splits > 1) {
+        hipLaunchKernelGGL((gemm_i8_tile_kernel<YT, B, B, WM, WN, true>), dim3(p.tiles, p.splits), dim3(64 * G::W),
+                           G::LDS, s, a);
+        const qg_status st = qg::launch_status("qgemm_i8 (split)");
+        if (st) return st;
+        hipLaunchKernelGGL((gemm_i8_join_kernel<YT, B, B, WM, WN>), dim3(p.tiles * G::W * (G::MT / 2)), dim3(64), 0, s,
+                           a, p.tiles, p.splits);
+        return qg::launch_status("qgemm_i8 (join)");
+    }
+    hipLaunchKernelGGL((gemm_i8_tile_kernel<YT, B, B, WM, WN, false>), dim3(p.tiles), dim3(64 * G::W), G::LDS, s, a);
+    return qg::launch_status("qgemm_i8");
+}
+
+template <int YT>
+qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
+    switch (p.form) {
+        case FORM_64: return launch_tiles<YT, 64, 2, 2>(a, p, s);
+        case FORM_128: return launch_tiles<YT, 128, 2, 4>(a, p, s);
+        case FORM_256: return launch_tiles<YT, 256, 4, 2>(a, p, s);
+    }
+    if (a.N <= 16)
+        hipLaunchKernelGGL((gemm_i8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
+    else
+        hipLaunchKernelGGL((gemm_i8_stream_kernel<YT, 2, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
     return qg::launch_status("qgemm_i8");
 }
 
@@ -393,7 +702,10 @@ qg_status qg_quantize_i8_rows(const void* x, int x_type, int64_t ldx, int64_t N,
     return qg::launch_status("qg_quantize_i8_rows");
 }
 
-size_t qgemm_i8_workspace_bytes(int64_t M, int64_t K, int64_t N) { return 0; }
+size_t qgemm_i8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+    if (!qg_i8_bytes(M, K) || N < 1 || N > QG_I8_MAX_ROWS || M * N > (int64_t)1 << 32) return 0;
+    return plan(M, K, N).ws;
+}
 
 qg_status qgemm_i8(const void* w, const float* ws, const void* xq, int64_t ldx, const float* xs, const float* bias,
                    void* Y, int y_type, int64_t ldy, int64_t M, int64_t K, int64_t N, void* workspace,
@@ -407,8 +719,8 @@ qg_status qgemm_i8(const void* w, const float* ws, const void* xq, int64_t ldx, 
     if (N < 1 || N > QG_I8_MAX_ROWS || M * N > (int64_t)1 << 32)
         return qg::fail(QG_ERR_SHAPE, "N=%lld not in [1, %d], or M N over 2^32", (long long)N, QG_I8_MAX_ROWS);
     const int64_t most = ((int64_t)1 << 40) / N;
-    if (ldx < kp || ldx > most || ldx % 16)
-        return qg::fail(QG_ERR_SHAPE, "ldx=%lld not a multiple of 16 in [%lld, 2^40 / N]", (long long)ldx, (long long)kp);
+    if (ldx < kp || ldx > (1 << 22) || ldx % 16)  // 256 rows stay within 32-bit offsets
+        return qg::fail(QG_ERR_SHAPE, "ldx=%lld not a multiple of 16 in [%lld, 2^22]", (long long)ldx, (long long)kp);
     if (ldy < M || ldy > most || ldy % 4)
         return qg::fail(QG_ERR_SHAPE, "ldy=%lld not a multiple of 4 in [M, 2^40 / N]", (long long)ldy);
     if (!qg::aligned16(w) || !qg::aligned16(xq) || !qg::aligned16(Y))
@@ -420,6 +732,16 @@ qg_status qgemm_i8(const void* w, const float* ws, const void* xq, int64_t ldx, 
         overlap(Y, yb, ws, (size_t)M * 4) || overlap(Y, yb, xs, (size_t)N * 4) ||
         (bias && overlap(Y, yb, bias, (size_t)M * 4)))
         return qg::fail(QG_ERR_SHAPE, "Y overlaps an input");
+    const Plan p = plan(M, K, N);
+    if (p.ws && (!workspace || workspace_bytes < p.ws))
+        return qg::fail(QG_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", p.ws, workspace ? workspace_bytes : 0);
+    if (p.ws) {
+        if (!qg::aligned16(workspace)) return qg::fail(QG_ERR_ALIGN, "workspace not 16-byte aligned");
+        if (overlap(workspace, p.ws, Y, yb) || overlap(workspace, p.ws, xq, (size_t)(N - 1) * ldx + kp) ||
+            overlap(workspace, p.ws, w, qg_i8_bytes(M, K)) || overlap(workspace, p.ws, ws, (size_t)M * 4) ||
+            overlap(workspace, p.ws, xs, (size_t)N * 4) || (bias && overlap(workspace, p.ws, bias, (size_t)M * 4)))
+            return qg::fail(QG_ERR_SHAPE, "the workspace overlaps an operand");
+    }
     st = qg::check_device();
     if (st) return st;
     GArgs a{};
@@ -435,10 +757,12 @@ qg_status qgemm_i8(const void* w, const float* ws, const void* xq, int64_t ldx, 
     a.N = (int32_t)N;
     a.nb = (int32_t)(kp / kKB);
     a.mtiles = (int32_t)mt;
+    a.part = (qi4*)workspace;
+    a.kper = p.kper;
     hipStream_t s = (hipStream_t)stream;
-    if (y_type == QG_F32) return launch_gemm<QG_F32>(a, s);
-    if (y_type == QG_F16) return launch_gemm<QG_F16>(a, s);
-    return launch_gemm<QG_BF16>(a, s);
+    if (y_type == QG_F32) return launch_gemm<QG_F32>(a, p, s);
+    if (y_type == QG_F16) return launch_gemm<QG_F16>(a, p, s);
+    return launch_gemm<QG_BF16>(a, p, s);
 }
 
 }  // extern "C"
