@@ -503,7 +503,7 @@ qg_status qgemm_i8(const void* w_packed, const float* w_scale, const void* xq, i
  * parent -1, score -inf, finished 0, length 0. With n == beams, out->score,
  * out->finished and out->length may be the input arrays themselves (a step in
  * place); otherwise outputs must not overlap inputs.
- * 1 <= n <= QG_BEAM_MAX_SELECT, 1 <= beams <= QG_BEAM_MAX, batch * beams <= 2^20,
+ * 1 <= n <= QG_BEAM_MAX_SELECT, 1 <= beams <= QG_BEAM_MAX, batch * beams <= 65536,
  * 1 <= vocab <= QG_TOPK_MAX_ROWS, ld >= vocab; eos in [0, vocab), or -1 for none
  * (then finished must be NULL); length_penalty in [-16, 16]. The logits must be 16-byte
  * aligned, rows need not be; the other arrays 4-byte (finished: 1). Workspace:

@@ -13,6 +13,9 @@
 
 namespace {
 
+// 16 bytes as a vector type of the compiler's, which keeps arrays of it in registers
+typedef uint32_t u16B __attribute__((ext_vector_type(4)));
+
 struct RArgs {
     qg_beam_state st[QG_BEAM_MAX_STATES];
     uint32_t end[QG_BEAM_MAX_STATES];  // workgroups of the states up to this one
@@ -141,7 +144,7 @@ extern "C" qg_status qg_beam_reorder(const qg_beam_state* states, int count, con
     qg_status st = qg::check_device();
     if (st) return st;
     hipStream_t s = (hipStream_t)stream;
-    st = launch<uint4>(states, count, parent, batch, beams_in, beams_out, s);
+    st = launch<u16B>(states, count, parent, batch, beams_in, beams_out, s);
     if (!st) st = launch<uint32_t>(states, count, parent, batch, beams_in, beams_out, s);
     if (!st) st = launch<uint8_t>(states, count, parent, batch, beams_in, beams_out, s);
     return st;

@@ -10,18 +10,17 @@
 // decide near ties by their own rounding. z - m is exact there, so a constant added
 // to a row changes nothing.
 //
-// Stages.
+// Stages, two launches.
 //  1. beam_stats_kernel, one pass over the logits: per wavefront's segment its
-//     maximum m and sum of exp(z - m); per tile (16 lanes' vectors) the key of its
-//     best element.
-//  2. beam_row_kernel, one workgroup per row: the n-th best of the threads' best
-//     tile keys bounds the n-th best element from below (n elements reach it), so
-//     only tiles that reach it are read again, and of them only such elements; they
-//     are ranked by counting the larger ones.
-//  3. beam_item_kernel, one workgroup per item: scores of the rows' n best, ranked by
-//     counting.
-// Keys are order-preserving value bits above the complement of the token, so that
-// no two are equal and every order of arrival gives the same result.
+//     maximum m and sum of exp(z - m), and the maximum of every tile of 8 vectors of
+//     16 bytes.
+//  2. beam_rank_kernel, one workgroup per row: the n-th largest of the threads' best
+//     tile maxima is a bound that at least n elements reach, so only tiles that reach
+//     it are read again, and of them only such elements; they are ranked by counting
+//     the better ones. The item's last workgroup to finish scores its rows' n best
+//     and ranks those the same way.
+// Elements are ranked by keys, order-preserving value bits above the complement of
+// the token, no two equal: every order of arrival gives the same result.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -32,8 +31,9 @@
 namespace {
 
 constexpr int kWG = 256;
-constexpr int kSegVec = 8;      // 16-byte vectors per lane and segment
+constexpr int kMaxRows = 65536;
 constexpr int kBuf = 1024;      // candidate buffer of stage 2
+constexpr int kList = 1024;     // tiles of one listing
 constexpr double kMaxAlpha = 16;
 constexpr float kMaxF = 3.4028234663852886e38f;
 
@@ -77,288 +77,454 @@ struct BArgs {
     int32_t eos;
     float* segmax;      // [rows][segs]
     double* segsum;     // [rows][segs]
-    uint64_t* tkey;     // [rows][tiles]
+    float* tmax;        // [rows][tiles], rows of a multiple of 4
     uint64_t* rowkey;   // [rows][n], best first, 0: none
-    double2* rowstat;   // [rows]: maximum, log of the sum
+    double* rowstat;    // [rows][2]: maximum, log of the sum
+    uint32_t* arrived;  // [items]: rows ranked so far
     qg_beam_out out;
 };
 
+QG_DEV float neg_inf() { return -__builtin_huge_valf(); }
+
 // Masked elements (NaN, -inf) become -inf, +inf the largest float.
-QG_DEV float clean(float v) {
-    const float ninf = -__builtin_huge_valf();
-    return v != v ? ninf : fminf(v, kMaxF);
-}
+QG_DEV float clean(float v) { return v == v ? fminf(v, kMaxF) : neg_inf(); }
 QG_DEV uint64_t key_of(float v, int token) {
-    return v == -__builtin_huge_valf() ? 0 : ((uint64_t)qg_ord(v) << 32) | (0xffffffffu - (uint32_t)token);
+    return v == neg_inf() ? 0 : ((uint64_t)qg_ord(v) << 32) | (0xffffffffu - (uint32_t)token);
 }
 QG_DEV float key_value(uint64_t k) { return qg_unord((uint32_t)(k >> 32)); }
 QG_DEV int key_token(uint64_t k) { return (int)(0xffffffffu - (uint32_t)k); }
 
-QG_DEV uint64_t shfl_xor64(uint64_t v, int m) {
-    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, m), hi = (uint32_t)__shfl_xor((int)(v >> 32), m);
-    return ((uint64_t)hi << 32) | lo;
+// exp(x) for x <= 0 to about 1e-14 of the result: x = k ln 2 + r, |r| <= ln 2 / 2, the
+// Taylor sum of exp(r) to r^11 / 11! (the next term is below 7e-15), times 2^k. What k
+// times the error of ln 2 costs stays below 1e-14 down to exp(-300), and smaller
+// results do not show in the sums. x below -1000 gives 0.
+QG_DEV double exp_neg(double x) {
+    x = __builtin_fmax(x, -1000.);
+    const double k = __builtin_rint(x * 1.4426950408889634074);
+    const double r = __builtin_fma(-k, 0.69314718055994530942, x);
+    double p = 1. / 39916800;
+    p = __builtin_fma(p, r, 1. / 3628800);
+    p = __builtin_fma(p, r, 1. / 362880);
+    p = __builtin_fma(p, r, 1. / 40320);
+    p = __builtin_fma(p, r, 1. / 5040);
+    p = __builtin_fma(p, r, 1. / 720);
+    p = __builtin_fma(p, r, 1. / 120);
+    p = __builtin_fma(p, r, 1. / 24);
+    p = __builtin_fma(p, r, 1. / 6);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.);
+    p = __builtin_fma(p, r, 1.);
+    return __builtin_ldexp(p, (int)k);
 }
 
-// Rows start at any element: vectors are read from the 16-byte boundary at or below
-// a row's start, `sh` elements before it. (The base is aligned, so that boundary is
-// never before the buffer.)
+QG_DEV float wave_max(float v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
+    return v;
+}
+QG_DEV double wave_sum(double v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+}
+
+// A row's 16-byte vectors. Rows start at any element: vectors are cut from the
+// 16-byte boundary at or below the row's start, `sh` elements before it (the base is
+// aligned, so that boundary is never before the buffer). Vector i holds the elements
+// i N - sh + 0 .. N - 1; only the vector that holds the row's end is read element by
+// element.
 template <int XT>
 struct Row {
+    static constexpr int N = Log<XT>::N;
     const uint8_t* base;
     int sh, vocab;
     QG_DEV Row(const void* logits, int64_t ld, int64_t row, int vocab_) : vocab(vocab_) {
-        constexpr int eb = 16 / Log<XT>::N;
+        constexpr int eb = 16 / N;
         const uint8_t* p = (const uint8_t*)logits + row * ld * eb;
         sh = (int)((reinterpret_cast<uintptr_t>(p) & 15) / eb);
         base = p - sh * eb;
     }
-    // vector i's elements; outside the row -inf. Full vectors are one load, the
-    // last one stays inside the row.
-    QG_DEV void load(int64_t i, float (&v)[Log<XT>::N]) const {
-        constexpr int N = Log<XT>::N;
-        const int64_t e0 = i * N - sh;
-        const float ninf = -__builtin_huge_valf();
-        if (e0 + N <= vocab) {
-            const uint4 u = *reinterpret_cast<const uint4*>(base + i * 16);
+    QG_DEV bool whole(int i) const { return i * N - sh + N <= vocab; }      // ends inside the row
+    QG_DEV bool cut(int i) const { return i * N - sh < vocab && !whole(i); }
+    QG_DEV uint4 get(int i) const { return *reinterpret_cast<const uint4*>(base + (int64_t)i * 16); }
+    // elements outside the row: -inf
+    QG_DEV void mask(int i, float (&v)[N]) const {
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = e0 + e >= 0 ? clean(Log<XT>::get(u, e)) : ninf;
-        } else {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                v[e] = e0 + e >= 0 && e0 + e < vocab ? clean(Log<XT>::at(base, i * N + e)) : ninf;
+        for (int e = 0; e < N; ++e) {
+            const int at = i * N - sh + e;
+            if (at < 0 || at >= vocab) v[e] = neg_inf();
         }
+    }
+    QG_DEV void last(int i, float (&v)[N]) const {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = clean(Log<XT>::at(base, min(i * N + e, vocab - 1 + sh)));
+        mask(i, v);
     }
 };
 
 // ---------------------------------------------------------------- stage 1
-template <int XT>
+// SV vectors per lane; 8 / SV lanes' make a tile.
+template <int XT, int SV>
 __global__ __launch_bounds__(kWG) void beam_stats_kernel(BArgs a) {
     constexpr int N = Log<XT>::N;
     const int lane = threadIdx.x & 63;
-    const int64_t g = (int64_t)blockIdx.x * (kWG / 64) + (threadIdx.x >> 6);
-    const int64_t row = g / a.segs;
-    if (row >= a.rows) return;
+    const uint32_t g = blockIdx.x * (kWG / 64) + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (g < (uint32_t)(a.rows / a.beams) && lane == 0) a.arrived[g] = 0;  // (there are more wavefronts than items)
+    const uint32_t row = g / (uint32_t)a.segs;
+    if (row >= (uint32_t)a.rows) return;
     if (a.finished && a.finished[row]) return;
-    const int seg = (int)(g - row * a.segs);
+    const int seg = (int)(g - row * (uint32_t)a.segs);
     const Row<XT> r(a.logits, a.ld, row, a.vocab);
-    const float ninf = -__builtin_huge_valf();
-    float v[kSegVec][N];
+    const int first = seg * SV * 64;  // vector j of this lane: first + 64 j + lane
+    uint4 u[SV];
+    float v[SV][N];
+    const bool inside = first * N >= r.sh && r.whole(first + SV * 64 - 1);
+    if (inside) {
 #pragma unroll
-    for (int j = 0; j < kSegVec; ++j) r.load(((int64_t)seg * kSegVec + j) * 64 + lane, v[j]);
-    float mx = ninf;
+        for (int j = 0; j < SV; ++j) u[j] = r.get(first + 64 * j + lane);
 #pragma unroll
-    for (int j = 0; j < kSegVec; ++j) {
-        const int64_t i = ((int64_t)seg * kSegVec + j) * 64 + lane;
-        float best = v[j][0];
-        int at = 0;
+        for (int j = 0; j < SV; ++j)
 #pragma unroll
-        for (int e = 1; e < N; ++e)
-            if (v[j][e] > best) best = v[j][e], at = e;
-        uint64_t k = key_of(best, (int)(i * N - r.sh) + at);
+            for (int e = 0; e < N; ++e) v[j][e] = clean(Log<XT>::get(u[j], e));
+    } else {
 #pragma unroll
-        for (int m = 1; m < 16; m <<= 1) {
-            const uint64_t o = shfl_xor64(k, m);
-            k = o > k ? o : k;
+        for (int j = 0; j < SV; ++j) {
+            u[j] = make_uint4(0, 0, 0, 0);
+            if (r.whole(first + 64 * j + lane)) u[j] = r.get(first + 64 * j + lane);
         }
-        const int64_t tile = ((int64_t)seg * kSegVec + j) * 4 + (lane >> 4);
-        if ((lane & 15) == 0 && tile < a.tiles) a.tkey[row * a.tiles + tile] = k;
-        mx = fmaxf(mx, best);
+#pragma unroll
+        for (int j = 0; j < SV; ++j) {
+            const int i = first + 64 * j + lane;
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[j][e] = clean(Log<XT>::get(u[j], e));
+            if (r.cut(i))
+                r.last(i, v[j]);
+            else
+                r.mask(i, v[j]);
+        }
     }
+    float best = neg_inf();
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) mx = fmaxf(mx, __shfl_xor(mx, m));
-    double s = 0;
-    if (mx != ninf)
+    for (int j = 0; j < SV; ++j)
 #pragma unroll
-        for (int j = 0; j < kSegVec; ++j)
+        for (int e = 0; e < N; ++e) best = fmaxf(best, v[j][e]);
+    constexpr int L = 8 / SV;  // lanes of a tile
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (v[j][e] != ninf) s += exp((double)v[j][e] - (double)mx);
+    for (int m = 1; m < L; m <<= 1) best = fmaxf(best, __shfl_xor(best, m));
+    const int tile = seg * (64 / L) + lane / L;
+    if (lane % L == 0) a.tmax[(int64_t)row * a.tiles + tile] = best;
+    const float mx = wave_max(best);
+    double s[2] = {0., 0.};
+    if (mx != neg_inf())
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
+        for (int j = 0; j < SV; ++j)
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e & 1] += exp_neg((double)v[j][e] - (double)mx);
+    const double sum = wave_sum(s[0] + s[1]);
     if (lane == 0) {
-        a.segmax[row * a.segs + seg] = mx;
-        a.segsum[row * a.segs + seg] = s;
+        a.segmax[(int64_t)row * a.segs + seg] = mx;
+        a.segsum[(int64_t)row * a.segs + seg] = sum;
     }
 }
 
 // ---------------------------------------------------------------- stage 2
-// Ranks the `c` keys of buf (distinct, nonzero; c <= kBuf) by counting and moves the
-// best min(c, n) to buf in order. Every thread of the workgroup calls it.
+// Ranks the c keys of buf (distinct, nonzero; c <= kBuf) by counting the larger ones
+// and leaves the best min(c, n) in order. Every thread of the workgroup calls it.
 QG_DEV int rank_buf(uint64_t* buf, int c, int n) {
-    uint64_t k[kBuf / kWG];
-    int rk[kBuf / kWG];
+    constexpr int R = kBuf / kWG;
+    uint64_t k[R];
+    int rk[R];
 #pragma unroll
-    for (int j = 0; j < kBuf / kWG; ++j) {
+    for (int j = 0; j < R; ++j) {
         const int i = threadIdx.x + j * kWG;
         k[j] = i < c ? buf[i] : 0;
         rk[j] = 0;
     }
+    const int used = (c + kWG - 1) / kWG;
     for (int i = 0; i < c; ++i) {
         const uint64_t o = buf[i];
 #pragma unroll
-        for (int j = 0; j < kBuf / kWG; ++j) rk[j] += o > k[j];
+        for (int j = 0; j < R; ++j)
+            if (j < used) rk[j] += o > k[j];
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kBuf / kWG; ++j)
+    for (int j = 0; j < R; ++j)
         if (k[j] && rk[j] < n) buf[rk[j]] = k[j];
     __syncthreads();
     return min(c, n);
 }
 
-template <int XT>
-__global__ __launch_bounds__(kWG) void beam_row_kernel(BArgs a) {
+// Values that other workgroups of the launch read: past this XCD's L2.
+template <typename V>
+QG_DEV void put(V* p, V v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+QG_DEV V take(const V* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Tile maxima of a row: tiles of 32 (fp32) or 64 elements, one segment more for a row
+// that starts inside a vector.
+constexpr int kQuads = (QG_TOPK_MAX_ROWS / 32 + 64 + 4 * kWG - 1) / (4 * kWG);
+
+struct RowShared {
+    uint64_t buf[kBuf];
+    float tops[kWG];
+    int list[kList];
+    float bound;
+    int count, listed, reach, more;
+    float wmx[kWG / 64];
+    double wsum[kWG / 64];
+};
+
+// The row's n best keys, in order, to rowkey, and its maximum and log-sum to rowstat.
+template <int XT, int SV>
+QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
     constexpr int N = Log<XT>::N;
-    __shared__ uint64_t buf[kBuf];
-    __shared__ uint64_t bound;
-    __shared__ int count, waiting;
-    __shared__ float wmx[kWG / 64];
-    __shared__ double wsum[kWG / 64];
+    constexpr int L = 8 / SV;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t row = blockIdx.x;
-    if (a.finished && a.finished[row]) return;
-    const float ninf = -__builtin_huge_valf();
     const Row<XT> r(a.logits, a.ld, row, a.vocab);
 
-    // the row's maximum and log-sum, in a fixed order
+    // maximum and log-sum, in a fixed order; meanwhile the threads' best tile maxima
     const float* sm = a.segmax + row * a.segs;
     const double* ss = a.segsum + row * a.segs;
-    float mx = ninf;
+    const float* tm = a.tmax + row * a.tiles;
+    float mx = neg_inf(), best = neg_inf();
+    float4 tv[kQuads];  // this thread's tile maxima: tiles 4 (tid + kWG q) + 0 .. 3
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+        tv[q] = make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
+        if ((tid + kWG * q) * 4 < a.tiles) tv[q] = *reinterpret_cast<const float4*>(tm + (tid + kWG * q) * 4);
+    }
     for (int i = tid; i < a.segs; i += kWG) mx = fmaxf(mx, sm[i]);
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) mx = fmaxf(mx, __shfl_xor(mx, m));
-    if (lane == 0) wmx[wave] = mx;
+    for (int q = 0; q < kQuads; ++q) best = fmaxf(fmaxf(fmaxf(best, tv[q].x), tv[q].y), fmaxf(tv[q].z, tv[q].w));
+    mx = wave_max(mx);
+    if (lane == 0) sh.wmx[wave] = mx;
+    sh.tops[tid] = best;
+    if (tid == 0) {
+        sh.bound = neg_inf();
+        sh.count = sh.listed = sh.reach = 0;
+    }
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWG / 64; ++w) mx = fmaxf(mx, wmx[w]);
+    for (int w = 0; w < kWG / 64; ++w) mx = fmaxf(mx, sh.wmx[w]);
     double s = 0;
     for (int i = tid; i < a.segs; i += kWG)
-        if (sm[i] != ninf) s += ss[i] * exp((double)sm[i] - (double)mx);
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
-    if (lane == 0) wsum[wave] = s;
-
-    // a bound that at least n elements reach (or none, with fewer tiles than n)
-    const uint64_t* tk = a.tkey + row * a.tiles;
-    uint64_t best = 0;
-    for (int i = tid; i < a.tiles; i += kWG) best = max(best, tk[i]);
-    buf[tid] = best;
-    if (tid == 0) {
-        bound = 1;
-        count = 0;
+        if (sm[i] != neg_inf()) s += ss[i] * exp_neg((double)sm[i] - (double)mx);
+    s = wave_sum(s);
+    if (lane == 0) sh.wsum[wave] = s;
+    int rk = 0;  // among equal maxima the lower thread first
+    for (int i = 0; i < kWG; i += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(sh.tops + i);
+        rk += (o.x > best || (o.x == best && i < tid)) + (o.y > best || (o.y == best && i + 1 < tid)) +
+              (o.z > best || (o.z == best && i + 2 < tid)) + (o.w > best || (o.w == best && i + 3 < tid));
     }
+    if (rk == a.n - 1) sh.bound = best;  // (-inf where fewer than n threads hold any element)
     __syncthreads();
     if (tid == 0) {
         double t = 0;
-        for (int w = 0; w < kWG / 64; ++w) t += wsum[w];
-        a.rowstat[row] = make_double2((double)mx, mx == ninf ? 0. : log(t));
+        for (int w = 0; w < kWG / 64; ++w) t += sh.wsum[w];
+        put(a.rowstat + 2 * row, (double)mx);
+        put(a.rowstat + 2 * row + 1, mx == neg_inf() ? 0. : log(t));
     }
-    int rk = 0;
-    for (int i = 0; i < kWG; ++i) rk += buf[i] > best;
-    if (best && rk == a.n - 1) bound = best;
-    __syncthreads();
 
-    // Elements that reach the bound, tile by tile. The buffer is cut back to its n
-    // best whenever the next round could overflow it, and the bound rises with it.
-    uint64_t T0 = bound;
-    constexpr int L = 16;  // lanes per tile
-    const int grp = tid / L, sub = tid % L;
-    for (int t0 = 0; t0 < a.tiles; t0 += kWG / L) {
-        const int t = t0 + grp;
-        const bool go = t < a.tiles && tk[t] >= T0;
-        if (!__syncthreads_or(go)) continue;
-        float v[N];
-        const int64_t i = (int64_t)t * L + sub;
-        if (go) r.load(i, v);
+    // The tiles that reach the bound are listed, all at once where the list holds them,
+    // else those of one q at a time; each listed tile's eight vectors go to eight
+    // threads. Keys from the bound's value on go to the buffer; when they would not fit,
+    // it is cut back to its n best, which raises the bound.
+    uint64_t T0 = sh.bound == neg_inf() ? 1 : (uint64_t)qg_ord(sh.bound) << 32;
+    auto reaches = [&](float m) { return m != neg_inf() && (uint64_t)qg_ord(m) >= (T0 >> 32); };
+    int mine_t = 0;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const uint64_t k = go ? key_of(v[e], (int)(i * N - r.sh) + e) : 0;
-            if (tid == 0) waiting = count;
-            __syncthreads();
-            if (waiting + kWG > kBuf) {
-                const int c = rank_buf(buf, waiting, a.n);
-                if (c == a.n) T0 = buf[a.n - 1];
-                __syncthreads();
-                if (tid == 0) count = c;
-                __syncthreads();
+    for (int q = 0; q < kQuads; ++q)
+        mine_t += reaches(tv[q].x) + reaches(tv[q].y) + reaches(tv[q].z) + reaches(tv[q].w);
+    if (mine_t) atomicAdd(&sh.reach, mine_t);
+    __syncthreads();
+    const bool whole = sh.reach <= kList;
+    for (int turn = 0; turn < (whole ? 1 : kQuads); ++turn) {
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+            if (whole || q == turn) {
+                const int t = (tid + kWG * q) * 4;
+                if (reaches(tv[q].x)) sh.list[atomicAdd(&sh.listed, 1)] = t;
+                if (reaches(tv[q].y)) sh.list[atomicAdd(&sh.listed, 1)] = t + 1;
+                if (reaches(tv[q].z)) sh.list[atomicAdd(&sh.listed, 1)] = t + 2;
+                if (reaches(tv[q].w)) sh.list[atomicAdd(&sh.listed, 1)] = t + 3;
             }
-            if (k && k >= T0) buf[atomicAdd(&count, 1)] = k;
+        __syncthreads();
+        const int scanned = sh.listed;
+        __syncthreads();
+        if (tid == 0) sh.listed = 0;
+        for (int v0 = 0; v0 < scanned * 8; v0 += kWG) {
+            const int o = v0 + tid;
+            float v[N];
+            uint64_t key[N];
+            int mine = 0;
+            const bool on = o < scanned * 8;
+            int i = 0;
+            if (on) {
+                const int t = sh.list[o >> 3], part = o & 7;
+                const int seg = t / (64 / L), l = t % (64 / L) * L + part % L;
+                i = seg * SV * 64 + part / L * 64 + l;
+            }
+            const bool in = on && r.whole(i);
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (in) u = r.get(i);
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = clean(Log<XT>::get(u, e));
+            if (on && r.cut(i)) r.last(i, v);
+            if (on) r.mask(i, v);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                key[e] = on ? key_of(v[e], i * N - r.sh + e) : 0;
+                mine += key[e] >= T0;
+            }
+            if (tid == 0) sh.more = 0;
             __syncthreads();
+            if (mine) atomicAdd(&sh.more, mine);
+            __syncthreads();
+            if (sh.count + sh.more <= kBuf) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (key[e] >= T0) sh.buf[atomicAdd(&sh.count, 1)] = key[e];
+                __syncthreads();
+            } else {  // one element of every thread at a time
+#pragma unroll 1
+                for (int e = 0; e < N; ++e) {
+                    uint64_t k = key[0];
+#pragma unroll
+                    for (int d = 1; d < N; ++d) k = d == e ? key[d] : k;
+                    const int c = sh.count;
+                    __syncthreads();
+                    if (c + kWG > kBuf) {
+                        const int left = rank_buf(sh.buf, c, a.n);
+                        if (left == a.n) T0 = sh.buf[a.n - 1];
+                        if (tid == 0) sh.count = left;
+                        __syncthreads();
+                    }
+                    if (k && k >= T0) sh.buf[atomicAdd(&sh.count, 1)] = k;
+                    __syncthreads();
+                }
+            }
         }
+        __syncthreads();
     }
-    const int c = rank_buf(buf, count, a.n);
-    for (int i = tid; i < a.n; i += kWG) a.rowkey[row * a.n + i] = i < c ? buf[i] : 0;
+    const int c = rank_buf(sh.buf, sh.count, a.n);
+    for (int i = tid; i < a.n; i += kWG) put(a.rowkey + row * a.n + i, i < c ? sh.buf[i] : (uint64_t)0);
 }
 
-// ---------------------------------------------------------------- stage 3
-// Candidate i (beam-major, each beam's in order) of an item. Order: rank descending,
-// then i ascending.
-__global__ __launch_bounds__(kWG) void beam_item_kernel(BArgs a) {
-    __shared__ double rank[QG_BEAM_MAX * QG_BEAM_MAX_SELECT];
-    __shared__ int place[QG_BEAM_MAX_SELECT];
+struct ItemShared {
+    double rank[QG_BEAM_MAX * QG_BEAM_MAX_SELECT];  // of candidate i = beam * n + place in the beam
+    uint64_t key[QG_BEAM_MAX * QG_BEAM_MAX_SELECT];
+    double over[QG_BEAM_MAX];                       // len^alpha
+    double2 stat[QG_BEAM_MAX];
+    float cum[QG_BEAM_MAX];
+    int len[QG_BEAM_MAX];
+    bool done[QG_BEAM_MAX];
+    int place[QG_BEAM_MAX_SELECT];
+};
+struct Beam {  // of thread `beam`, read before the workgroup is counted
+    float cum;
+    int len;
+    bool done;
+};
+
+// An item's n best over its beams' n best. Order: rank descending, then i ascending.
+QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared& sh) {
     const int tid = threadIdx.x;
-    const int64_t item = blockIdx.x;
     const int total = a.beams * a.n;
     const double ninf = -__builtin_huge_val();
-    if (tid < a.n) place[tid] = -1;
-
-    auto candidate = [&](int i, double& sc, int& token, int& len, bool& done) {
-        const int w = i / a.n, j = i - w * a.n;
-        const int64_t row = item * a.beams + w;
-        const float cum = a.score[row];
-        done = a.finished && a.finished[row];
-        const int l = a.length ? a.length[row] : 0;
-        len = done ? l : l + 1;
-        sc = ninf;
+    for (int i = tid; i < total; i += kWG) sh.key[i] = take(a.rowkey + item * total + i);
+    if (tid < a.n) sh.place[tid] = -1;
+    if (tid < a.beams) {
+        const int64_t row = item * a.beams + tid;
+        const double2 st = beam.done ? make_double2(0., 0.) : make_double2(take(a.rowstat + 2 * row), take(a.rowstat + 2 * row + 1));
+        sh.cum[tid] = beam.cum;
+        sh.done[tid] = beam.done;
+        sh.len[tid] = beam.len;
+        sh.over[tid] = a.alpha != 0. ? pow((double)max(beam.len, 1), a.alpha) : 1.;
+        sh.stat[tid] = st;
+    }
+    __syncthreads();
+    auto candidate = [&](int i, int& token) -> double {
+        const int w = i / a.n;
+        const float cum = sh.cum[w];
         token = -1;
-        if (cum != cum || cum == -__builtin_huge_valf()) return;
-        if (done) {
-            if (j == 0) {
-                sc = cum;
-                token = a.eos;
-            }
-            return;
+        if (cum != cum || cum == neg_inf()) return ninf;
+        if (sh.done[w]) {
+            if (i != w * a.n) return ninf;
+            token = a.eos;
+            return cum;
         }
-        const uint64_t k = a.rowkey[row * a.n + j];
-        if (!k) return;
-        const double2 st = a.rowstat[row];
+        const uint64_t k = sh.key[i];
+        if (!k) return ninf;
         token = key_token(k);
-        sc = (double)cum + (((double)key_value(k) - st.x) - st.y);
+        return (double)cum + (((double)key_value(k) - sh.stat[w].x) - sh.stat[w].y);
     };
-
     for (int i = tid; i < total; i += kWG) {
-        double sc;
-        int token, len;
-        bool done;
-        candidate(i, sc, token, len, done);
-        if (token >= 0 && a.alpha != 0.) sc /= pow((double)max(len, 1), a.alpha);
-        rank[i] = sc;
+        int token;
+        const double sc = candidate(i, token);
+        sh.rank[i] = a.alpha != 0. && token >= 0 ? sc / sh.over[i / a.n] : sc;
     }
     __syncthreads();
     for (int i = tid; i < total; i += kWG) {
-        const double k = rank[i];
+        const double k = sh.rank[i];
         if (k == ninf) continue;
         int before = 0;
-        for (int o = 0; o < total; ++o) before += rank[o] > k || (rank[o] == k && o < i);
-        if (before < a.n) place[before] = i;
+        for (int o = 0; o < total; ++o) before += sh.rank[o] > k || (sh.rank[o] == k && o < i);
+        if (before < a.n) sh.place[before] = i;
     }
     __syncthreads();
-    double sc = ninf;
-    int token = -1, parent = -1, len = 0;
-    bool done = false;
-    if (tid < a.n && place[tid] >= 0) {
-        candidate(place[tid], sc, token, len, done);
-        parent = place[tid] / a.n;
-    }
-    __syncthreads();  // every input is read before an output, which may be the same array, is written
     if (tid < a.n) {
+        const int i = sh.place[tid];
+        int token = -1, w = -1;
+        double sc = ninf;
+        if (i >= 0) {
+            sc = candidate(i, token);
+            w = i / a.n;
+        }
         const int64_t o = item * a.n + tid;
         a.out.token[o] = token;
-        a.out.parent[o] = parent;
+        a.out.parent[o] = w;
         a.out.score[o] = (float)sc;
-        if (a.out.finished) a.out.finished[o] = parent >= 0 && (done || (a.eos >= 0 && token == a.eos));
-        if (a.out.length) a.out.length[o] = parent >= 0 ? len : 0;
+        if (a.out.finished) a.out.finished[o] = w >= 0 && (sh.done[max(w, 0)] || (a.eos >= 0 && token == a.eos));
+        if (a.out.length) a.out.length[o] = w >= 0 ? sh.len[max(w, 0)] : 0;
     }
+}
+
+template <int XT, int SV>
+__global__ __launch_bounds__(kWG) void beam_rank_kernel(BArgs a) {
+    __shared__ union {
+        RowShared row;
+        ItemShared item;
+    } sh;
+    __shared__ bool last;
+    const int64_t row = blockIdx.x;
+    const int64_t item = row / a.beams;
+    // The item's inputs, which its outputs may replace: read by every one of its
+    // workgroups before it is counted, while only the last one counted writes.
+    Beam beam{0.f, 0, false};
+    if ((int)threadIdx.x < a.beams) {
+        const int64_t b = item * a.beams + threadIdx.x;
+        beam.done = a.finished && a.finished[b];
+        beam.cum = a.score[b];
+        beam.len = (a.length ? a.length[b] : 0) + (beam.done ? 0 : 1);
+    }
+    if (!(a.finished && a.finished[row])) rank_row<XT, SV>(a, row, sh.row);
+    // The row's results are out (each wavefront waits for its stores before the barrier)
+    // before it is counted; the item's last row sees the others' counts, hence their
+    // results. No workgroup waits for another.
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(a.arrived + item, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+               (uint32_t)(a.beams - 1);
+    __syncthreads();
+    if (last) rank_item(a, item, beam, sh.item);
 }
 
 // ---------------------------------------------------------------- host
@@ -366,16 +532,19 @@ int vec_elems(int type) { return type == QG_F32 ? 4 : 8; }
 
 struct Plan {
     int64_t rows;
-    int tiles, segs;
-    size_t segmax, segsum, tkey, rowkey, rowstat, total;
+    int sv, tiles, segs;
+    size_t segmax, segsum, tmax, rowkey, rowstat, arrived, total;
 };
 Plan plan(int type, int64_t batch, int beams, int64_t vocab, int n) {
     Plan p;
     p.rows = batch * beams;
     const int64_t ve = vec_elems(type);
     const int64_t vecs = qg::ceil_div(vocab + ve - 1, ve);  // a row may start inside a vector
-    p.tiles = (int)qg::ceil_div(vecs, 16);
-    p.segs = (int)qg::ceil_div(vecs, 64 * kSegVec);
+    // Segments of eight vectors a lane, or of two where eight would leave most of the
+    // chip without one.
+    p.sv = p.rows * qg::ceil_div(vecs, 64 * 8) >= 2048 ? 8 : 2;
+    p.segs = (int)qg::ceil_div(vecs, 64 * p.sv);
+    p.tiles = p.segs * 8 * p.sv;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -384,9 +553,10 @@ Plan plan(int type, int64_t batch, int beams, int64_t vocab, int n) {
     };
     p.segmax = take((size_t)p.rows * p.segs * 4);
     p.segsum = take((size_t)p.rows * p.segs * 8);
-    p.tkey = take((size_t)p.rows * p.tiles * 8);
+    p.tmax = take((size_t)p.rows * p.tiles * 4);
     p.rowkey = take((size_t)p.rows * n * 8);
     p.rowstat = take((size_t)p.rows * 16);
+    p.arrived = take((size_t)batch * 4);
     p.total = at;
     return p;
 }
@@ -395,8 +565,8 @@ qg_status check_shape(int type, int64_t batch, int beams, int64_t vocab, int n) 
     if (type != QG_F32 && type != QG_F16 && type != QG_BF16)
         return qg::fail(QG_ERR_SHAPE, "logits_type=%d unknown", type);
     if (beams < 1 || beams > QG_BEAM_MAX) return qg::fail(QG_ERR_SHAPE, "beams=%d not in [1, %d]", beams, QG_BEAM_MAX);
-    if (batch < 1 || batch > (1 << 20) / beams)
-        return qg::fail(QG_ERR_SHAPE, "batch=%lld below 1, or over 2^20 rows", (long long)batch);
+    if (batch < 1 || batch > kMaxRows / beams)
+        return qg::fail(QG_ERR_SHAPE, "batch=%lld below 1, or over 65536 rows", (long long)batch);
     if (vocab < 1 || vocab > QG_TOPK_MAX_ROWS)
         return qg::fail(QG_ERR_SHAPE, "vocab=%lld not in [1, %d]", (long long)vocab, QG_TOPK_MAX_ROWS);
     if (n < 1 || n > QG_BEAM_MAX_SELECT) return qg::fail(QG_ERR_SHAPE, "n=%d not in [1, %d]", n, QG_BEAM_MAX_SELECT);
@@ -408,17 +578,18 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return a && b && x < y + nb && y < x + na;
 }
 
-template <int XT>
-qg_status launch(const BArgs& a, int64_t batch, hipStream_t s) {
+template <int XT, int SV>
+qg_status launch(const BArgs& a, hipStream_t s) {
     const int64_t waves = (int64_t)a.rows * a.segs;
-    hipLaunchKernelGGL(beam_stats_kernel<XT>, dim3((unsigned)qg::ceil_div(waves, kWG / 64)), dim3(kWG), 0, s, a);
-    qg_status st = qg::launch_status("logits_beam_select (statistics)");
+    hipLaunchKernelGGL((beam_stats_kernel<XT, SV>), dim3((unsigned)qg::ceil_div(waves, kWG / 64)), dim3(kWG), 0, s, a);
+    const qg_status st = qg::launch_status("logits_beam_select (statistics)");
     if (st) return st;
-    hipLaunchKernelGGL(beam_row_kernel<XT>, dim3((unsigned)a.rows), dim3(kWG), 0, s, a);
-    st = qg::launch_status("logits_beam_select (rows)");
-    if (st) return st;
-    hipLaunchKernelGGL(beam_item_kernel, dim3((unsigned)batch), dim3(kWG), 0, s, a);
-    return qg::launch_status("logits_beam_select (items)");
+    hipLaunchKernelGGL((beam_rank_kernel<XT, SV>), dim3((unsigned)a.rows), dim3(kWG), 0, s, a);
+    return qg::launch_status("logits_beam_select (ranking)");
+}
+template <int XT>
+qg_status launch_for(const BArgs& a, int sv, hipStream_t s) {
+    return sv == 8 ? launch<XT, 8>(a, s) : launch<XT, 2>(a, s);
 }
 
 }  // namespace
@@ -505,14 +676,15 @@ qg_status logits_beam_select(const qg_beam_in* in, int n, void* ws, size_t ws_by
     a.eos = in->eos;
     a.segmax = (float*)(w8 + p.segmax);
     a.segsum = (double*)(w8 + p.segsum);
-    a.tkey = (uint64_t*)(w8 + p.tkey);
+    a.tmax = (float*)(w8 + p.tmax);
     a.rowkey = (uint64_t*)(w8 + p.rowkey);
-    a.rowstat = (double2*)(w8 + p.rowstat);
+    a.rowstat = (double*)(w8 + p.rowstat);
+    a.arrived = (uint32_t*)(w8 + p.arrived);
     a.out = *out;
     hipStream_t s = (hipStream_t)stream;
-    if (in->logits_type == QG_F32) return launch<QG_F32>(a, in->batch, s);
-    if (in->logits_type == QG_F16) return launch<QG_F16>(a, in->batch, s);
-    return launch<QG_BF16>(a, in->batch, s);
+    if (in->logits_type == QG_F32) return launch_for<QG_F32>(a, p.sv, s);
+    if (in->logits_type == QG_F16) return launch_for<QG_F16>(a, p.sv, s);
+    return launch_for<QG_BF16>(a, p.sv, s);
 }
 
 }  // extern "C"

@@ -338,3 +338,22 @@ def test_beam_search_run():
         torch.cuda.synchronize()
         np.testing.assert_array_equal(history.cpu().numpy(), mirror)
         hidden = torch.tanh(hidden + ed[out.token.view(-1).clamp(min=0).long()])
+
+
+def test_signalling_nans_are_masked():
+    z = np.random.default_rng(15).standard_normal((2, 5000)).astype(np.float32)
+    bits = z.view(np.uint32)
+    bits[0, [0, 7, 4999]] = 0x7F800001   # signalling NaNs of both signs
+    bits[1, ::3] = 0xFFA00000
+    case("logits_beam_select signalling NaNs")
+    out = qg.logits_beam_select(to_dev(bits.view(np.int32)).view(torch.float32), torch.zeros(1, 2, device=DEV), 20)
+    ref = beamref.beam_select(z.astype(np.float64)[None], np.zeros((1, 2)), 20)
+    check_selection(out, ref, "sNaN", length=False)
+
+
+@pytest.mark.parametrize("kind", ["normal", "flat", "special"])
+@pytest.mark.parametrize("B,W,V,n", [(40, 8, 20000, 16), (70, 5, 9001, 10), (300, 1, 30000, 64), (16, 32, 33333, 32)])
+def test_select_many_rows(B, W, V, n, kind):
+    # enough rows for the longer segments
+    for i, t in enumerate(TYPES):
+        run_select(B, W, V, n, kind, t, seed=B + V + i, finished=i == 1, alpha=[0.0, 1.0, 0.0][i], ld=V + 3 * i)
