@@ -94,16 +94,19 @@ QG_DEV uint64_t key_of(float v, int token) {
 QG_DEV float key_value(uint64_t k) { return qg_unord((uint32_t)(k >> 32)); }
 QG_DEV int key_token(uint64_t k) { return (int)(0xffffffffu - (uint32_t)k); }
 
-// exp(x) for x <= 0 to about 1e-14 of the result: x = k ln 2 + r, |r| <= ln 2 / 2, the
-// Taylor sum of exp(r) to r^11 / 11! (the next term is below 7e-15), times 2^k. What k
-// times the error of ln 2 costs stays below 1e-14 down to exp(-300), and smaller
-// results do not show in the sums. x below -1000 gives 0.
-QG_DEV double exp_neg(double x) {
-    x = __builtin_fmax(x, -1000.);
-    const double k = __builtin_rint(x * 1.4426950408889634074);
-    const double r = __builtin_fma(-k, 0.69314718055994530942, x);
-    double p = 1. / 39916800;
-    p = __builtin_fma(p, r, 1. / 3628800);
+// exp(v - m) for float32 v <= m, m finite, to about 3e-13 of the result: x = v - m is
+// exact in double, x = k ln 2 + r with |r| <= ln 2 / 2, the Taylor sum of exp(r) to
+// r^10 / 10! (the next term is below 2.3e-13), and k added to the exponent. k comes from
+// the low bits of a sum with 1.5 * 2^52: the conversions, roundings and ldexp of double
+// precision run at a fraction of the rate of its additions and fmas. x below -600 (v =
+// -inf among them) counts as -600, which keeps the result normal and far below what a
+// sum can show.
+QG_DEV double exp_diff(float v, float m) {
+    const double x = __builtin_fmax((double)v - (double)m, -600.);
+    const double big = 6755399441055744.;
+    const double t = __builtin_fma(x, 1.4426950408889634074, big);
+    const double r = __builtin_fma(t - big, -0.69314718055994530942, x);
+    double p = 1. / 3628800;
     p = __builtin_fma(p, r, 1. / 362880);
     p = __builtin_fma(p, r, 1. / 40320);
     p = __builtin_fma(p, r, 1. / 5040);
@@ -114,7 +117,8 @@ QG_DEV double exp_neg(double x) {
     p = __builtin_fma(p, r, 0.5);
     p = __builtin_fma(p, r, 1.);
     p = __builtin_fma(p, r, 1.);
-    return __builtin_ldexp(p, (int)k);
+    const uint32_t k = (uint32_t)__builtin_bit_cast(uint64_t, t);
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, p) + ((uint64_t)(k << 20) << 32));
 }
 
 QG_DEV float wave_max(float v) {
@@ -219,7 +223,7 @@ __global__ __launch_bounds__(kWG) void beam_stats_kernel(BArgs a) {
 #pragma unroll
         for (int j = 0; j < SV; ++j)
 #pragma unroll
-            for (int e = 0; e < N; ++e) s[e & 1] += exp_neg((double)v[j][e] - (double)mx);
+            for (int e = 0; e < N; ++e) s[e & 1] += exp_diff(v[j][e], mx);
     const double sum = wave_sum(s[0] + s[1]);
     if (lane == 0) {
         a.segmax[(int64_t)row * a.segs + seg] = mx;
@@ -265,17 +269,16 @@ QG_DEV V take(const V* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Tile maxima of a row: tiles of 32 (fp32) or 64 elements, one segment more for a row
-// that starts inside a vector.
-constexpr int kQuads = (QG_TOPK_MAX_ROWS / 32 + 64 + 4 * kWG - 1) / (4 * kWG);
+// Tile maxima of a thread: tiles of 32 (fp32) or 64 elements, up to one segment of them
+// more for a row that starts inside a vector.
+constexpr int kMine = (QG_TOPK_MAX_ROWS / 32 + 32 + kWG - 1) / kWG;
 
 struct RowShared {
     uint64_t buf[kBuf];
-    float tops[kWG];
+    float tops[kWG / 2];
     int list[kList];
-    float bound;
-    int count, listed, reach, more;
-    float wmx[kWG / 64];
+    int count, listed, more;
+    float wmx[kWG / 64], wlow[kWG / 64];
     double wsum[kWG / 64];
 };
 
@@ -292,37 +295,39 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
     const double* ss = a.segsum + row * a.segs;
     const float* tm = a.tmax + row * a.tiles;
     float mx = neg_inf(), best = neg_inf();
-    float4 tv[kQuads];  // this thread's tile maxima: tiles 4 (tid + kWG q) + 0 .. 3
+    float tv[kMine];  // this thread's tile maxima: tiles tid + kWG q
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-        tv[q] = make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
-        if ((tid + kWG * q) * 4 < a.tiles) tv[q] = *reinterpret_cast<const float4*>(tm + (tid + kWG * q) * 4);
-    }
+    for (int q = 0; q < kMine; ++q) tv[q] = tid + kWG * q < a.tiles ? tm[tid + kWG * q] : neg_inf();
     for (int i = tid; i < a.segs; i += kWG) mx = fmaxf(mx, sm[i]);
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) best = fmaxf(fmaxf(fmaxf(best, tv[q].x), tv[q].y), fmaxf(tv[q].z, tv[q].w));
+    for (int q = 0; q < kMine; ++q) best = fmaxf(best, tv[q]);
     mx = wave_max(mx);
     if (lane == 0) sh.wmx[wave] = mx;
-    sh.tops[tid] = best;
+    best = fmaxf(best, __shfl_xor(best, 1));
+    if (!(tid & 1)) sh.tops[tid >> 1] = best;
     if (tid == 0) {
-        sh.bound = neg_inf();
-        sh.count = sh.listed = sh.reach = 0;
+        sh.count = sh.listed = 0;
     }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWG / 64; ++w) mx = fmaxf(mx, sh.wmx[w]);
     double s = 0;
     for (int i = tid; i < a.segs; i += kWG)
-        if (sm[i] != neg_inf()) s += ss[i] * exp_neg((double)sm[i] - (double)mx);
+        if (sm[i] != neg_inf()) s += ss[i] * exp_diff(sm[i], mx);
     s = wave_sum(s);
     if (lane == 0) sh.wsum[wave] = s;
-    int rk = 0;  // among equal maxima the lower thread first
-    for (int i = 0; i < kWG; i += 4) {
-        const float4 o = *reinterpret_cast<const float4*>(sh.tops + i);
-        rk += (o.x > best || (o.x == best && i < tid)) + (o.y > best || (o.y == best && i + 1 < tid)) +
-              (o.z > best || (o.z == best && i + 2 < tid)) + (o.w > best || (o.w == best && i + 3 < tid));
+    // The n-th largest of the 128 pairs' maxima: the largest value that n of them reach.
+    // The two threads of a pair count one half of the pairs each.
+    const int half = (tid & 1) * (kWG / 4);
+    int reached = 0;
+#pragma unroll
+    for (int i = 0; i < kWG / 4; i += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(sh.tops + half + i);
+        reached += (o.x >= best) + (o.y >= best) + (o.z >= best) + (o.w >= best);
     }
-    if (rk == a.n - 1) sh.bound = best;  // (-inf where fewer than n threads hold any element)
+    reached += __shfl_xor(reached, 1);
+    const float low = wave_max(reached >= a.n ? best : neg_inf());
+    if (lane == 0) sh.wlow[wave] = low;
     __syncthreads();
     if (tid == 0) {
         double t = 0;
@@ -332,32 +337,34 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
     }
 
     // The tiles that reach the bound are listed, all at once where the list holds them,
-    // else those of one q at a time; each listed tile's eight vectors go to eight
+    // else those of one round q at a time; each listed tile's eight vectors go to eight
     // threads. Keys from the bound's value on go to the buffer; when they would not fit,
     // it is cut back to its n best, which raises the bound.
-    uint64_t T0 = sh.bound == neg_inf() ? 1 : (uint64_t)qg_ord(sh.bound) << 32;
-    auto reaches = [&](float m) { return m != neg_inf() && (uint64_t)qg_ord(m) >= (T0 >> 32); };
+    float bound = -kMaxF;  // (every element that is not masked, where fewer than n pairs hold one)
+#pragma unroll
+    for (int w = 0; w < kWG / 64; ++w) bound = fmaxf(bound, sh.wlow[w]);
+    uint64_t T0 = (uint64_t)qg_ord(bound) << 32;
     int mine_t = 0;
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q)
-        mine_t += reaches(tv[q].x) + reaches(tv[q].y) + reaches(tv[q].z) + reaches(tv[q].w);
-    if (mine_t) atomicAdd(&sh.reach, mine_t);
+    for (int q = 0; q < kMine; ++q) mine_t += tv[q] >= bound;
+    int at = mine_t ? atomicAdd(&sh.listed, mine_t) : 0;
     __syncthreads();
-    const bool whole = sh.reach <= kList;
-    for (int turn = 0; turn < (whole ? 1 : kQuads); ++turn) {
+    const int reach = sh.listed;
+    const bool whole = reach <= kList;
+    for (int turn = 0; turn < (whole ? 1 : kMine); ++turn) {
+        if (!whole) {
+            __syncthreads();
+            if (tid == 0) sh.listed = 0;
+            __syncthreads();
+        }
 #pragma unroll
-        for (int q = 0; q < kQuads; ++q)
-            if (whole || q == turn) {
-                const int t = (tid + kWG * q) * 4;
-                if (reaches(tv[q].x)) sh.list[atomicAdd(&sh.listed, 1)] = t;
-                if (reaches(tv[q].y)) sh.list[atomicAdd(&sh.listed, 1)] = t + 1;
-                if (reaches(tv[q].z)) sh.list[atomicAdd(&sh.listed, 1)] = t + 2;
-                if (reaches(tv[q].w)) sh.list[atomicAdd(&sh.listed, 1)] = t + 3;
+        for (int q = 0; q < kMine; ++q)
+            if ((whole || q == turn) && tv[q] >= bound) {
+                if (!whole) at = atomicAdd(&sh.listed, 1);
+                sh.list[at++] = tid + kWG * q;
             }
         __syncthreads();
-        const int scanned = sh.listed;
-        __syncthreads();
-        if (tid == 0) sh.listed = 0;
+        const int scanned = whole ? reach : sh.listed;
         for (int v0 = 0; v0 < scanned * 8; v0 += kWG) {
             const int o = v0 + tid;
             float v[N];
@@ -475,7 +482,8 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
         const double k = sh.rank[i];
         if (k == ninf) continue;
         int before = 0;
-        for (int o = 0; o < total; ++o) before += sh.rank[o] > k || (sh.rank[o] == k && o < i);
+        for (int o = 0; o < i; ++o) before += sh.rank[o] >= k;
+        for (int o = i + 1; o < total; ++o) before += sh.rank[o] > k;
         if (before < a.n) sh.place[before] = i;
     }
     __syncthreads();
@@ -540,9 +548,9 @@ Plan plan(int type, int64_t batch, int beams, int64_t vocab, int n) {
     p.rows = batch * beams;
     const int64_t ve = vec_elems(type);
     const int64_t vecs = qg::ceil_div(vocab + ve - 1, ve);  // a row may start inside a vector
-    // Segments of eight vectors a lane, or of two where eight would leave most of the
+    // Segments of four vectors a lane, or of two where four would leave most of the
     // chip without one.
-    p.sv = p.rows * qg::ceil_div(vecs, 64 * 8) >= 2048 ? 8 : 2;
+    p.sv = p.rows * qg::ceil_div(vecs, 64 * 4) >= 2048 ? 4 : 2;
     p.segs = (int)qg::ceil_div(vecs, 64 * p.sv);
     p.tiles = p.segs * 8 * p.sv;
     size_t at = 0;
@@ -589,7 +597,7 @@ qg_status launch(const BArgs& a, hipStream_t s) {
 }
 template <int XT>
 qg_status launch_for(const BArgs& a, int sv, hipStream_t s) {
-    return sv == 8 ? launch<XT, 8>(a, s) : launch<XT, 2>(a, s);
+    return sv == 4 ? launch<XT, 4>(a, s) : launch<XT, 2>(a, s);
 }
 
 }  // namespace
