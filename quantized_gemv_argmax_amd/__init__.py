@@ -6,6 +6,7 @@ raises if the compiled library is missing: there is no fallback path.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -137,7 +138,7 @@ _SIGS = {
     "qgemm_i8": (_I, [_P, _P, _P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P, _SZ, _P]),
     "logits_beam_select_workspace_bytes": (_SZ, [_I, _I64, _I, _I64, _I]),
     "logits_beam_select": (_I, [ctypes.POINTER(_BeamIn), _I, _P, _SZ, ctypes.POINTER(_BeamOut), _P]),
-    "qg_beam_reorder": (_I, [ctypes.POINTER(_BeamState), _I, _P, _I64, _I, _I, _P]),
+    "qg_beam_reorder": (_I, [_P, _I, _P, _I64, _I, _I, _P]),
 }
 
 
@@ -615,33 +616,54 @@ _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _HERE_ALREADY = contextlib.nullcontext()
 
 
-def _on(device):
-    """Context in which `device` is the current one (kernels launch there)."""
-    return _HERE_ALREADY if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _on(index):
+    """Context in which GPU `index` is the current one (kernels launch there)."""
+    return _HERE_ALREADY if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _check_tensor(name, t, dtypes, device=None, shape=None):
-    """A GPU tensor of one of `dtypes` on `device` with the given shape (None: any extent)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _raw_stream(index) -> int:
+    """Handle of GPU `index`'s current stream (torch.cuda.current_stream without its object)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _gpu(name, t, dtypes):
+    """Index of the GPU that holds t, a tensor of one of `dtypes`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise ValueError(f"{name} must be a tensor on the GPU")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
-    if shape is not None and (t.dim() != len(shape) or any(e is not None and e != g for e, g in zip(shape, t.shape))):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('any' if e is None else e for e in shape)}")
+    return t.get_device()
 
 
-def _row_stride(name, t):
-    """Row stride in elements of a 2-D tensor with contiguous rows."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def _same(name, t, dtypes, index, shape):
+    """t: contiguous, of one of `dtypes` and of `shape`, on GPU `index`."""
+    if _gpu(name, t, dtypes) != index:
+        raise ValueError(f"{name} is on GPU {t.get_device()}, the other operands on GPU {index}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows_of(name, t, dtypes, index, rows, width):
+    """Row stride in elements of t, 2-D with contiguous rows of at least `width` on GPU
+    `index`; rows None: any number."""
+    if _gpu(name, t, dtypes) != index:
+        raise ValueError(f"{name} is on GPU {t.get_device()}, the other operands on GPU {index}")
+    if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    n, m = t.shape
+    if rows is not None and n != rows or m < width:
+        raise ValueError(f"{name} has shape {(n, m)}, expected {'any' if rows is None else rows} rows of at least {width}")
+    ld, one = t.stride()
+    if m > 1 and one != 1:
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    return ld if n > 1 else max(ld, m)
 
 
 def _scratch(ws, need, device):
-    """(address, bytes) of a call's workspace: the caller's, grown if need be, or one of
-    the call's own, so that calls on several streams and captured graphs never share."""
+    """(address, bytes, owner) of a call's workspace: the caller's, grown if need be, or one
+    of the call's own, so that calls on several streams and captured graphs never share."""
     if not need:
         return None, 0, None
     if ws is not None:
@@ -651,6 +673,10 @@ def _scratch(ws, need, device):
     return buf.data_ptr(), need, buf
 
 
+_F32, _I8, _U8, _I32 = (torch.float32,), (torch.int8,), (torch.uint8,), (torch.int32,)
+_FLAGS = (torch.bool, torch.uint8)
+
+
 def i8_bytes(M: int, K: int) -> int:
     return int(lib().qg_i8_bytes(M, K))
 
@@ -658,19 +684,17 @@ def i8_bytes(M: int, K: int) -> int:
 def pack_i8(w: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """Lay out row-major int8 weights (M, K), rows at any stride, for qgemm_i8
     (uint8 buffer of i8_bytes(M, K) bytes)."""
-    _check_tensor("w", w, (torch.int8,))
-    ldw = _row_stride("w", w)
+    gpu = _gpu("w", w, _I8)
+    ldw = _rows_of("w", w, _I8, gpu, None, 0)
     M, K = w.shape
     n = i8_bytes(M, K)
     if n == 0:
         raise ValueError(f"no int8 layout for a {M} x {K} matrix")
     if out is None:
         out = torch.empty(n, dtype=torch.uint8, device=w.device)
-    _check_tensor("out", out, (torch.uint8,), w.device)
-    if out.numel() != n or not out.is_contiguous():
-        raise ValueError(f"out must be {n} contiguous bytes")
-    with _on(w.device):
-        _check("qg_pack_i8", lib().qg_pack_i8(_ptr(w), ldw, _ptr(out), M, K, _stream(w.device)))
+    _same("out", out, _U8, gpu, (n,))
+    with _on(gpu):
+        _check("qg_pack_i8", lib().qg_pack_i8(w.data_ptr(), ldw, out.data_ptr(), M, K, _raw_stream(gpu)))
     return out
 
 
@@ -678,22 +702,21 @@ def quantize_i8_rows(x: torch.Tensor, out: torch.Tensor | None = None, scale: to
     """Int8 rows of x (N, K) in fp32, fp16 or bf16, a scale each (max|x| / 127):
     tokens for qgemm_i8, or the rows of a weight matrix before pack_i8. Returns
     (q int8 (N, ldq), scale float32 (N)), ldq = K rounded up to 64, zeros beyond K."""
-    _check_tensor("x", x, tuple(_TYPES))
-    ldx = _row_stride("x", x)
+    gpu = _gpu("x", x, _TYPES)
+    ldx = _rows_of("x", x, _TYPES, gpu, None, 0)
     N, K = x.shape
     kp = (K + 63) // 64 * 64
     if out is None:
-        out = torch.empty((N, kp), dtype=torch.int8, device=x.device)
+        out, ldq = torch.empty((N, kp), dtype=torch.int8, device=x.device), kp
+    else:
+        ldq = _rows_of("out", out, _I8, gpu, N, kp)
     if scale is None:
         scale = torch.empty(N, dtype=torch.float32, device=x.device)
-    _check_tensor("out", out, (torch.int8,), x.device, (N, None))
-    _check_tensor("scale", scale, (torch.float32,), x.device, (N,))
-    if out.shape[1] < kp or not scale.is_contiguous():
-        raise ValueError(f"out needs rows of {kp} bytes, scale {N} contiguous numbers")
-    ldq = _row_stride("out", out)
-    with _on(x.device):
-        _check("qg_quantize_i8_rows", lib().qg_quantize_i8_rows(_ptr(x), _TYPES[x.dtype], ldx, N, K, _ptr(out), ldq,
-                                                                _ptr(scale), _stream(x.device)))
+    else:
+        _same("scale", scale, _F32, gpu, (N,))
+    with _on(gpu):
+        _check("qg_quantize_i8_rows", lib().qg_quantize_i8_rows(x.data_ptr(), _TYPES[x.dtype], ldx, N, K, out.data_ptr(),
+                                                                ldq, scale.data_ptr(), _raw_stream(gpu)))
     return out, scale
 
 
@@ -708,33 +731,27 @@ def qgemm_i8(w: torch.Tensor, w_scale: torch.Tensor, xq: torch.Tensor, x_scale: 
     packed by pack_i8 and rows quantized by quantize_i8_rows. Returns Y (N, ldy) of
     `dtype` (fp32, fp16 or bf16) with Y[:, :M] written. Without ws, a call that needs
     a workspace (products split along K) allocates its own."""
-    _check_tensor("w", w, (torch.uint8,))
-    dev = w.device
-    _check_tensor("w_scale", w_scale, (torch.float32,), dev, (M,))
-    _check_tensor("xq", xq, (torch.int8,), dev, (None, None))
-    ldx = _row_stride("xq", xq)
-    N = xq.shape[0]
-    _check_tensor("x_scale", x_scale, (torch.float32,), dev, (N,))
-    if bias is not None:
-        _check_tensor("bias", bias, (torch.float32,), dev, (M,))
-    if w.numel() != i8_bytes(M, K) or not w.is_contiguous():
+    L = lib()
+    gpu = _gpu("w", w, _U8)
+    if w.numel() != L.qg_i8_bytes(M, K) or not w.is_contiguous():
         raise ValueError(f"w is not a packed {M} x {K} matrix")
-    if xq.shape[1] < (K + 63) // 64 * 64:
-        raise ValueError(f"xq needs rows of {(K + 63) // 64 * 64} bytes for K = {K}")
-    if not all(t is None or t.is_contiguous() for t in (w_scale, x_scale, bias)):
-        raise ValueError("w_scale, x_scale and bias must be contiguous")
+    ldx = _rows_of("xq", xq, _I8, gpu, None, (K + 63) // 64 * 64)
+    N = xq.shape[0]
+    _same("w_scale", w_scale, _F32, gpu, (M,))
+    _same("x_scale", x_scale, _F32, gpu, (N,))
+    if bias is not None:
+        _same("bias", bias, _F32, gpu, (M,))
     if Y is None:
         if dtype not in _TYPES:
             raise ValueError(f"no output of type {dtype}")
-        Y = torch.empty((N, (M + 3) // 4 * 4), dtype=dtype, device=dev)
-    _check_tensor("Y", Y, tuple(_TYPES), dev, (N, None))
-    if Y.shape[1] < M:
-        raise ValueError(f"Y needs rows of {M} numbers")
-    ldy = _row_stride("Y", Y)
-    wp, wb, keep = _scratch(ws, qgemm_i8_workspace_bytes(M, K, N), dev)
-    with _on(dev):
-        _check("qgemm_i8", lib().qgemm_i8(_ptr(w), _ptr(w_scale), _ptr(xq), ldx, _ptr(x_scale), _ptr(bias), _ptr(Y),
-                                          _TYPES[Y.dtype], ldy, M, K, N, wp, wb, _stream(dev)))
+        ldy = (M + 3) // 4 * 4
+        Y = torch.empty((N, ldy), dtype=dtype, device=w.device)
+    else:
+        ldy = _rows_of("Y", Y, _TYPES, gpu, N, M)
+    wp, wb, keep = _scratch(ws, L.qgemm_i8_workspace_bytes(M, K, N), w.device)
+    with _on(gpu):
+        _check("qgemm_i8", L.qgemm_i8(w.data_ptr(), w_scale.data_ptr(), xq.data_ptr(), ldx, x_scale.data_ptr(), _ptr(bias),
+                                      Y.data_ptr(), _TYPES[Y.dtype], ldy, M, K, N, wp, wb, _raw_stream(gpu)))
     return Y
 
 
@@ -759,51 +776,74 @@ def logits_beam_select(logits: torch.Tensor, score: torch.Tensor, n: int, finish
     beams) float32; finished (batch, beams) bool; length (batch, beams) int32. `out` may
     hold score, finished and length themselves when n is the number of beams (a step
     in place). Ranking and special values as include/qgemv.h states."""
-    _check_tensor("logits", logits, tuple(_TYPES), shape=(None, None))
-    dev = logits.device
-    _check_tensor("score", score, (torch.float32,), dev, (None, None))
-    B, W = score.shape
+    L = lib()
+    gpu = _gpu("logits", logits, _TYPES)
+    if score.dim() != 2:
+        raise ValueError("score must be (batch, beams)")
+    shape = score.shape
+    B, W = shape
+    _same("score", score, _F32, gpu, shape)
+    ld = _rows_of("logits", logits, _TYPES, gpu, B * W, 0)
     V = logits.shape[1]
-    if logits.shape[0] != B * W:
-        raise ValueError(f"logits has {logits.shape[0]} rows for {B} x {W} scores")
-    ld = _row_stride("logits", logits)
-    out = out if out is not None else BeamSelection(B, n, dev, length is not None)
-    named = [("score", score, (torch.float32,), (B, W)), ("finished", finished, (torch.bool, torch.uint8), (B, W)),
-             ("length", length, (torch.int32,), (B, W)), ("out.token", out.token, (torch.int32,), (B, n)),
-             ("out.parent", out.parent, (torch.int32,), (B, n)), ("out.score", out.score, (torch.float32,), (B, n)),
-             ("out.finished", out.finished, (torch.bool, torch.uint8), (B, n)),
-             ("out.length", out.length, (torch.int32,), (B, n))]
-    for name, t, types, shape in named:
-        if t is not None:
-            _check_tensor(name, t, types, dev, shape)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+    if finished is not None:
+        _same("finished", finished, _FLAGS, gpu, shape)
+    if length is not None:
+        _same("length", length, _I32, gpu, shape)
+    if out is None:
+        out = BeamSelection(B, n, logits.device, length is not None)
+    else:
+        for name, types in (("token", _I32), ("parent", _I32), ("score", _F32), ("finished", _FLAGS), ("length", _I32)):
+            t = getattr(out, name)
+            if t is not None:
+                _same("out." + name, t, types, gpu, (B, n))
     xt = _TYPES[logits.dtype]
-    need = int(lib().logits_beam_select_workspace_bytes(xt, B, W, V, n))
-    wp, wb, keep = _scratch(ws, need, dev)
-    ci = _BeamIn(_ptr(logits), xt, ld, B, W, V, _ptr(score), _ptr(finished), _ptr(length), length_penalty, eos)
+    wp, wb, keep = _scratch(ws, L.logits_beam_select_workspace_bytes(xt, B, W, V, n), logits.device)
+    ci = _BeamIn(logits.data_ptr(), xt, ld, B, W, V, score.data_ptr(), _ptr(finished), _ptr(length), length_penalty, eos)
     co = _BeamOut(_ptr(out.token), _ptr(out.parent), _ptr(out.score), _ptr(out.finished), _ptr(out.length))
-    with _on(dev):
-        _check("logits_beam_select", lib().logits_beam_select(ctypes.byref(ci), n, wp, wb, ctypes.byref(co),
-                                                              _stream(dev)))
+    with _on(gpu):
+        _check("logits_beam_select", L.logits_beam_select(ctypes.byref(ci), n, wp, wb, ctypes.byref(co),
+                                                          _raw_stream(gpu)))
     return out
 
 
-def _row_pieces(name, t):
-    """(row stride, piece stride, pieces, bytes of a piece) of a tensor whose rows (first
-    dimension) are equally spaced contiguous pieces."""
-    eb = t.element_size()
-    span, dims = 1, [(n, st) for n, st in zip(t.shape[1:], t.stride()[1:]) if n != 1]
+def _row_pieces(name, shape, strides, eb):
+    """(row stride, piece stride, pieces, bytes of a piece), strides in bytes, of a tensor
+    whose rows (first dimension) are equally spaced contiguous pieces."""
+    span, dims = 1, [(n, st) for n, st in zip(shape[1:], strides[1:]) if n != 1]
     while dims and dims[-1][1] == span:
         span *= dims.pop()[0]
     outer, step = 1, 0
     while dims:
         n, st = dims.pop()
         if outer > 1 and st != outer * step:
-            raise ValueError(f"{name}: a row must be equally spaced contiguous pieces, got strides {t.stride()}")
+            raise ValueError(f"{name}: a row must be equally spaced contiguous pieces, got strides {strides}")
         step = step if outer > 1 else st
         outer *= n
-    return t.stride(0) * eb, step * eb, outer, span * eb
+    return strides[0] * eb, step * eb, outer, span * eb
+
+
+def _moves(i, s, d, B, W, n):
+    """The last six fields of a qg_beam_state for state i moved from s to d, or None if it
+    holds nothing."""
+    if s.dim() < 1 or s.shape[0] != B * W or d.dim() != s.dim() or d.shape[0] != B * n or d.shape[1:] != s.shape[1:]:
+        raise ValueError(f"state {i}: shapes {tuple(s.shape)} and {tuple(d.shape)} for {B} x {W} beams and {n} parents")
+    if d.dtype != s.dtype:
+        raise ValueError(f"out[{i}] must be {s.dtype}, not {d.dtype}")
+    if s.numel() == 0:  # nothing cached yet
+        return None
+    eb = s.element_size()
+    sr, so, outer, span = _row_pieces(f"states[{i}]", s.shape, s.stride(), eb)
+    dr, do, outer_d, span_d = _row_pieces(f"out[{i}]", d.shape, d.stride(), eb)
+    if (outer, span) != (outer_d, span_d):
+        # pieces of the finer of the two cuts
+        fine = min(span, span_d)
+        if max(span, span_d) % fine or (outer != 1 and outer_d != 1):
+            raise ValueError(f"state {i}: rows of state and result are cut into pieces that do not match")
+        if span > fine:
+            so, outer, span = fine, outer_d, fine
+        else:
+            do = fine
+    return sr, dr, so, do, outer, span
 
 
 def beam_reorder(states, parent: torch.Tensor, out=None):
@@ -811,44 +851,35 @@ def beam_reorder(states, parent: torch.Tensor, out=None):
     b * beams + parent[b, j] of the state (first dimension batch * beams; parent int32
     (batch, n); a parent outside [0, beams) leaves the result's row as it was). In place
     without `out` (then n == beams), else into the tensors of `out`. States may be
-    views (a cache's filled part); returns the list of results."""
+    views (a cache's filled part) and of several shapes and types; launched in groups of
+    BEAM_MAX_STATES. Returns the list of results."""
     states = list(states)
     results = states if out is None else list(out)
-    if not states:
-        raise ValueError("no states given")
-    _check_tensor("parent", parent, (torch.int32,), None, (None, None))
-    dev = parent.device
-    if not parent.is_contiguous() or len(results) != len(states):
-        raise ValueError("parent must be contiguous, and out as long as states")
+    if not states or len(results) != len(states):
+        raise ValueError("no states given" if not states else f"{len(results)} results for {len(states)} states")
+    gpu = _gpu("parent", parent, _I32)
+    if parent.dim() != 2 or not parent.is_contiguous():
+        raise ValueError("parent must be (batch, n) and contiguous")
     B, n = parent.shape
-    if not B or not n or states[0].dim() < 1 or states[0].shape[0] % B:
-        raise ValueError(f"{tuple(parent.shape)} parents do not fit a state of shape {tuple(states[0].shape)}")
-    W = states[0].shape[0] // B
-    arr = (_BeamState * len(states))()
-    count = 0
+    first = states[0]
+    if not isinstance(first, torch.Tensor) or not B or not n or first.dim() < 1 or first.shape[0] % B:
+        raise ValueError(f"{tuple(parent.shape)} parents do not fit the first state")
+    W = first.shape[0] // B
+    # states that look alike (a model's layers) are cut into pieces once
+    words, seen = array.array("q"), None
     for i, (s, d) in enumerate(zip(states, results)):
-        _check_tensor(f"states[{i}]", s, (getattr(s, "dtype", None),), dev)
-        _check_tensor(f"out[{i}]", d, (s.dtype,), dev)
-        if s.dim() < 1 or s.shape[0] != B * W or d.dim() != s.dim() or d.shape[0] != B * n or d.shape[1:] != s.shape[1:]:
-            raise ValueError(f"state {i}: shapes {tuple(s.shape)} and {tuple(d.shape)} for {B} x {W} beams and {n} parents")
-        if s.numel() == 0:  # nothing cached yet
-            continue
-        sr, so, outer, span = _row_pieces(f"states[{i}]", s)
-        dr, do, outer_d, span_d = (sr, so, outer, span) if d is s else _row_pieces(f"out[{i}]", d)
-        if (outer, span) != (outer_d, span_d):
-            # pieces of the finer of the two cuts
-            fine = min(span, span_d)
-            if max(span, span_d) % fine or (outer != 1 and outer_d != 1):
-                raise ValueError(f"state {i}: rows of state and result are cut into pieces that do not match")
-            if span > fine:
-                so, outer, span = fine, outer_d, fine
-            else:
-                do = fine
-        arr[count] = _BeamState(_ptr(s), _ptr(d), sr, dr, so, do, outer, span)
-        count += 1
-    with _on(dev):
+        if not isinstance(s, torch.Tensor) or not isinstance(d, torch.Tensor) or s.get_device() != gpu or d.get_device() != gpu:
+            raise ValueError(f"states[{i}] and its result must be tensors on GPU {gpu}")
+        look = (s.shape, s.stride(), s.dtype) if d is s else (s.shape, s.stride(), s.dtype, d.shape, d.stride(), d.dtype)
+        if look != seen:
+            moves, seen = _moves(i, s, d, B, W, n), look
+        if moves is not None:
+            p = s.data_ptr()
+            words.extend((p, p if d is s else d.data_ptr(), *moves))
+    L, at, count = lib(), words.buffer_info()[0], len(words) // 8
+    with _on(gpu):
+        stream = _raw_stream(gpu)
         for k in range(0, count, BEAM_MAX_STATES):
-            m = min(BEAM_MAX_STATES, count - k)
-            part = ctypes.cast(ctypes.addressof(arr) + k * ctypes.sizeof(_BeamState), ctypes.POINTER(_BeamState))
-            _check("qg_beam_reorder", lib().qg_beam_reorder(part, m, _ptr(parent), B, W, n, _stream(dev)))
+            _check("qg_beam_reorder", L.qg_beam_reorder(at + k * 64, min(BEAM_MAX_STATES, count - k), parent.data_ptr(), B, W,
+                                                        n, stream))
     return results

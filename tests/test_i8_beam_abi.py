@@ -174,7 +174,7 @@ def test_reorder_validation(L):
 
     def call(*states, parent=C, batch=2, bi=3, bo=3, count=None):
         arr = (qg._BeamState * max(1, len(states)))(*states)
-        return f(arr, len(states) if count is None else count, parent, batch, bi, bo, None)
+        return f(ctypes.addressof(arr), len(states) if count is None else count, parent, batch, bi, bo, None)
 
     if no_gpu():
         for ok in [state(), state(dst=A), state(src_row=0), state(outer=4, span=64, src_outer=128, dst_outer=64, dst_row=256),
