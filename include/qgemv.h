@@ -550,10 +550,11 @@ qg_status logits_beam_select(const qg_beam_in* in /* host */, int n, void* works
  * call must not overlap each other's. A state's bytes are moved 16 at a time where its
  * pointers, strides and span allow it, else 4, else singly; states need no alignment.
  * 1 <= count <= QG_BEAM_MAX_STATES, 1 <= beams_in, beams_out <= QG_BEAM_MAX, 1 <= batch
- * <= 65535; outer * span < 2^40, and less than 2^32 such units over one row of every
- * state; strides in [0, 2^40], dst rows and pieces apart (the smaller stride at least
+ * <= 65535; outer * span < 2^40, and fewer than 2^32 such units in a row of a state;
+ * strides in [0, 2^40], dst rows and pieces apart (the smaller stride at least
  * a span, the larger at least all that the smaller steps over) and apart from parent.
- * Work is split by alignment into at most three launches. No workspace.
+ * States alike in alignment and, to a factor of two, in length share a launch. No
+ * workspace.
  */
 #define QG_BEAM_MAX_STATES 56
 typedef struct {

@@ -866,16 +866,23 @@ def beam_reorder(states, parent: torch.Tensor, out=None):
         raise ValueError(f"{tuple(parent.shape)} parents do not fit the first state")
     W = first.shape[0] // B
     # states that look alike (a model's layers) are cut into pieces once
-    words, seen = array.array("q"), None
-    for i, (s, d) in enumerate(zip(states, results)):
-        if not isinstance(s, torch.Tensor) or not isinstance(d, torch.Tensor) or s.get_device() != gpu or d.get_device() != gpu:
-            raise ValueError(f"states[{i}] and its result must be tensors on GPU {gpu}")
-        look = (s.shape, s.stride(), s.dtype) if d is s else (s.shape, s.stride(), s.dtype, d.shape, d.stride(), d.dtype)
+    fields, seen, moves = [], None, None
+    for i, s in enumerate(states):
+        d = results[i]
+        if not isinstance(s, torch.Tensor) or s.get_device() != gpu:
+            raise ValueError(f"states[{i}] must be a tensor on GPU {gpu}")
+        look = (s.shape, s.stride(), s.dtype)
+        if d is not s:
+            if not isinstance(d, torch.Tensor) or d.get_device() != gpu:
+                raise ValueError(f"out[{i}] must be a tensor on GPU {gpu}")
+            look += (d.shape, d.stride(), d.dtype)
         if look != seen:
             moves, seen = _moves(i, s, d, B, W, n), look
         if moves is not None:
             p = s.data_ptr()
-            words.extend((p, p if d is s else d.data_ptr(), *moves))
+            fields += (p, p if d is s else d.data_ptr())
+            fields += moves
+    words = array.array("q", fields)
     L, at, count = lib(), words.buffer_info()[0], len(words) // 8
     with _on(gpu):
         stream = _raw_stream(gpu)

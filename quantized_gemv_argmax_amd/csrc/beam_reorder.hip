@@ -16,44 +16,42 @@ namespace {
 // 16 bytes as a vector type of the compiler's, which keeps arrays of it in registers
 typedef uint32_t u16B __attribute__((ext_vector_type(4)));
 
+struct RState {
+    const uint8_t* src;
+    uint8_t* dst;
+    int64_t src_row, dst_row, src_outer, dst_outer;
+    uint32_t per, cols;  // units of a piece and of a row
+};
 struct RArgs {
-    qg_beam_state st[QG_BEAM_MAX_STATES];
-    uint32_t end[QG_BEAM_MAX_STATES];  // workgroups of the states up to this one
+    RState st[QG_BEAM_MAX_STATES];
     const int32_t* parent;
     int32_t beams_in, beams_out;
 };
 
 template <typename U, int W>
 __global__ __launch_bounds__(256) void beam_reorder_kernel(RArgs a) {
-    int k = 0;  // the state this workgroup belongs to: the first whose end is beyond it
-#pragma unroll
-    for (int step = 32; step; step >>= 1)
-        if (k + step < QG_BEAM_MAX_STATES && a.end[k + step - 1] <= blockIdx.x) k += step;
-    const qg_beam_state& s = a.st[k];
-    const uint32_t first = k ? a.end[k - 1] : 0u;
-    const int64_t per = s.span / (int64_t)sizeof(U);
-    const int64_t c = (int64_t)(blockIdx.x - first) * 256 + threadIdx.x;
-    if (c >= s.outer * per) return;
-    const int64_t o = c / per, i = c - o * per;
+    const RState& s = a.st[blockIdx.z];
+    const uint32_t c = blockIdx.x * 256u + threadIdx.x;
     const int64_t b = blockIdx.y;
-    const uint8_t* src = (const uint8_t*)s.src + b * a.beams_in * s.src_row + o * s.src_outer + i * (int64_t)sizeof(U);
-    uint8_t* dst = (uint8_t*)s.dst + b * a.beams_out * s.dst_row + o * s.dst_outer + i * (int64_t)sizeof(U);
-    const bool inplace = s.src == s.dst;
     const int32_t* par = a.parent + b * a.beams_out;
-    U v[W];
-    bool mv[W];
+    int p[W];  // parents of the rows that move, else -1
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        mv[j] = false;
-        if (j < a.beams_out) {
-            const int p = par[j];
-            mv[j] = p >= 0 && p < a.beams_in && !(inplace && p == j);
-            if (mv[j]) v[j] = *reinterpret_cast<const U*>(src + p * s.src_row);
-        }
-    }
+    for (int j = 0; j < W; ++j) p[j] = j < a.beams_out ? par[j] : -1;
+    const bool inplace = s.src == s.dst;
 #pragma unroll
     for (int j = 0; j < W; ++j)
-        if (mv[j]) *reinterpret_cast<U*>(dst + j * s.dst_row) = v[j];
+        if (p[j] < 0 || p[j] >= a.beams_in || (inplace && p[j] == j)) p[j] = -1;
+    if (c >= s.cols) return;
+    const uint32_t o = c / s.per, i = c - o * s.per;
+    const uint8_t* src = s.src + b * a.beams_in * s.src_row + o * s.src_outer + (int64_t)i * sizeof(U);
+    uint8_t* dst = s.dst + b * a.beams_out * s.dst_row + o * s.dst_outer + (int64_t)i * sizeof(U);
+    U v[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        if (p[j] >= 0) v[j] = *reinterpret_cast<const U*>(src + p[j] * s.src_row);
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        if (p[j] >= 0) *reinterpret_cast<U*>(dst + j * s.dst_row) = v[j];
 }
 
 // The largest unit of 16, 4 or 1 bytes that a state's pointers, strides and span allow.
@@ -63,30 +61,14 @@ int unit_of(const qg_beam_state& s) {
     if (s.outer > 1) bits |= (uintptr_t)s.src_outer | (uintptr_t)s.dst_outer;
     return (bits & 15) == 0 ? 16 : (bits & 3) == 0 ? 4 : 1;
 }
-int64_t groups_of(const qg_beam_state& s, int unit) { return qg::ceil_div(s.outer * (s.span / unit), 256); }
+int64_t cols_of(const qg_beam_state& s) { return s.outer * (s.span / unit_of(s)); }
 
-// One launch for the states of one unit.
 template <typename U>
-qg_status launch(const qg_beam_state* states, int count, const int32_t* parent, int64_t batch, int beams_in,
-                 int beams_out, hipStream_t stream) {
-    RArgs a{};
-    int n = 0;
-    uint32_t groups = 0;
-    for (int k = 0; k < count; ++k)
-        if (unit_of(states[k]) == (int)sizeof(U)) {
-            a.st[n] = states[k];
-            groups += (uint32_t)groups_of(states[k], (int)sizeof(U));
-            a.end[n++] = groups;
-        }
-    if (!n) return QG_OK;
-    for (int k = n; k < QG_BEAM_MAX_STATES; ++k) a.end[k] = groups;
-    a.parent = parent;
-    a.beams_in = beams_in;
-    a.beams_out = beams_out;
-    const dim3 g(groups, (unsigned)batch);
-    if (beams_out <= 4)
+qg_status launch(const RArgs& a, int n, uint32_t cols, int64_t batch, hipStream_t stream) {
+    const dim3 g((cols + 255) / 256, (unsigned)batch, (unsigned)n);
+    if (a.beams_out <= 4)
         hipLaunchKernelGGL((beam_reorder_kernel<U, 4>), g, dim3(256), 0, stream, a);
-    else if (beams_out <= 8)
+    else if (a.beams_out <= 8)
         hipLaunchKernelGGL((beam_reorder_kernel<U, 8>), g, dim3(256), 0, stream, a);
     else
         hipLaunchKernelGGL((beam_reorder_kernel<U, QG_BEAM_MAX>), g, dim3(256), 0, stream, a);
@@ -106,7 +88,6 @@ extern "C" qg_status qg_beam_reorder(const qg_beam_state* states, int count, con
     if (batch < 1 || batch > 65535) return qg::fail(QG_ERR_SHAPE, "batch=%lld not in [1, 65535]", (long long)batch);
     if (reinterpret_cast<uintptr_t>(parent) & 3) return qg::fail(QG_ERR_ALIGN, "parent not 4-byte aligned");
     const int64_t most = (int64_t)1 << 40;  // products with 2^21 rows stay below 2^62
-    int64_t groups = 0;
     for (int k = 0; k < count; ++k) {
         const qg_beam_state& s = states[k];
         if (!s.src || !s.dst) return qg::fail(QG_ERR_NULL, "state %d: src or dst is NULL", k);
@@ -137,15 +118,37 @@ extern "C" qg_status qg_beam_reorder(const qg_beam_state* states, int count, con
             const uintptr_t sn = (uintptr_t)((rin - 1) * s.src_row + (s.outer - 1) * s.src_outer + s.span);
             if (s0 < d0 + dn && d0 < s0 + sn) return qg::fail(QG_ERR_SHAPE, "state %d: src and dst overlap", k);
         }
-        groups += groups_of(s, unit_of(s));
-        if (groups >= (int64_t)1 << 24)  // a launch has fewer than 2^32 threads along x
-            return qg::fail(QG_ERR_SHAPE, "the states' rows hold over 2^32 units of their alignment");
+        if (cols_of(s) > 0xffffff00ll)  // a launch has fewer than 2^32 threads along x
+            return qg::fail(QG_ERR_SHAPE, "state %d: a row holds over 2^32 units of its alignment", k);
     }
     qg_status st = qg::check_device();
     if (st) return st;
-    hipStream_t s = (hipStream_t)stream;
-    st = launch<u16B>(states, count, parent, batch, beams_in, beams_out, s);
-    if (!st) st = launch<uint32_t>(states, count, parent, batch, beams_in, beams_out, s);
-    if (!st) st = launch<uint8_t>(states, count, parent, batch, beams_in, beams_out, s);
+    // One launch for the states of one unit whose rows are alike in length to a factor
+    // of two (a model's layers: one launch): a workgroup finds its state by its index.
+    uint64_t left = ((uint64_t)1 << count) - 1;
+    while (left) {
+        const int k0 = __builtin_ctzll(left), unit = unit_of(states[k0]);
+        const int64_t c0 = cols_of(states[k0]);
+        RArgs a{};
+        a.parent = parent;
+        a.beams_in = beams_in;
+        a.beams_out = beams_out;
+        int n = 0;
+        int64_t longest = 0;
+        for (int k = k0; k < count; ++k) {
+            const qg_beam_state& s = states[k];
+            const int64_t c = cols_of(s);
+            if (!(left >> k & 1) || unit_of(s) != unit || c > 2 * c0 || c0 > 2 * c) continue;
+            left &= ~((uint64_t)1 << k);
+            a.st[n++] = {(const uint8_t*)s.src, (uint8_t*)s.dst, s.src_row, s.dst_row, s.src_outer, s.dst_outer,
+                         (uint32_t)(s.span / unit), (uint32_t)c};
+            longest = std::max(longest, c);
+        }
+        hipStream_t h = (hipStream_t)stream;
+        st = unit == 16  ? launch<u16B>(a, n, (uint32_t)longest, batch, h)
+             : unit == 4 ? launch<uint32_t>(a, n, (uint32_t)longest, batch, h)
+                         : launch<uint8_t>(a, n, (uint32_t)longest, batch, h);
+        if (st) return st;
+    }
     return st;
 }
