@@ -7,7 +7,6 @@ raises if the compiled library is missing: there is no fallback path.
 from __future__ import annotations
 
 import array
-import contextlib
 import ctypes
 import os
 import re
@@ -613,17 +612,19 @@ def lmhead_topk(w: torch.Tensor, x: torch.Tensor, M: int, K: int, k: int, logits
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
-_HERE_ALREADY = contextlib.nullcontext()
 
 
-def _on(index):
-    """Context in which GPU `index` is the current one (kernels launch there)."""
-    return _HERE_ALREADY if torch.cuda.current_device() == index else torch.cuda.device(index)
-
-
-def _raw_stream(index) -> int:
-    """Handle of GPU `index`'s current stream (torch.cuda.current_stream without its object)."""
-    return torch._C._cuda_getCurrentRawStream(index)
+def _launch(name, gpu, *args):
+    """Calls the library's `name` on GPU `gpu`'s current stream with that GPU the current
+    one (kernels launch there); raises on an error status."""
+    f = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == gpu:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(gpu))
+    else:
+        with torch.cuda.device(gpu):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(gpu))
+    if status:
+        _check(name, status)
 
 
 def _gpu(name, t, dtypes):
@@ -637,35 +638,34 @@ def _gpu(name, t, dtypes):
 
 def _same(name, t, dtypes, index, shape):
     """t: contiguous, of one of `dtypes` and of `shape`, on GPU `index`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype in dtypes and t.shape == shape and \
+            t.is_contiguous():
+        return
     if _gpu(name, t, dtypes) != index:
         raise ValueError(f"{name} is on GPU {t.get_device()}, the other operands on GPU {index}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows_of(name, t, dtypes, index, rows, width):
-    """Row stride in elements of t, 2-D with contiguous rows of at least `width` on GPU
-    `index`; rows None: any number."""
+    """(rows, width, row stride in elements) of t, 2-D with contiguous rows of at least
+    `width` on GPU `index`; rows None: any number."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype in dtypes and t.dim() == 2:
+        n, m = t.shape
+        ld, one = t.stride()
+        if (rows is None or n == rows) and m >= width and (one == 1 or m <= 1):
+            return n, m, ld if n > 1 or ld > m else m
     if _gpu(name, t, dtypes) != index:
         raise ValueError(f"{name} is on GPU {t.get_device()}, the other operands on GPU {index}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D with contiguous rows")
-    n, m = t.shape
-    if rows is not None and n != rows or m < width:
-        raise ValueError(f"{name} has shape {(n, m)}, expected {'any' if rows is None else rows} rows of at least {width}")
-    ld, one = t.stride()
-    if m > 1 and one != 1:
-        raise ValueError(f"{name} must be 2-D with contiguous rows")
-    return ld if n > 1 else max(ld, m)
+    if t.dim() == 2 and not ((rows is None or t.shape[0] == rows) and t.shape[1] >= width):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {'any' if rows is None else rows} rows of at least {width}")
+    raise ValueError(f"{name} must be 2-D with contiguous rows")
 
 
 def _scratch(ws, need, device):
     """(address, bytes, owner) of a call's workspace: the caller's, grown if need be, or one
     of the call's own, so that calls on several streams and captured graphs never share."""
-    if not need:
-        return None, 0, None
     if ws is not None:
         ws.ensure(need)
         return ws.ptr(), ws.nbytes(), ws.buf
@@ -685,16 +685,14 @@ def pack_i8(w: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """Lay out row-major int8 weights (M, K), rows at any stride, for qgemm_i8
     (uint8 buffer of i8_bytes(M, K) bytes)."""
     gpu = _gpu("w", w, _I8)
-    ldw = _rows_of("w", w, _I8, gpu, None, 0)
-    M, K = w.shape
+    M, K, ldw = _rows_of("w", w, _I8, gpu, None, 0)
     n = i8_bytes(M, K)
     if n == 0:
         raise ValueError(f"no int8 layout for a {M} x {K} matrix")
     if out is None:
         out = torch.empty(n, dtype=torch.uint8, device=w.device)
     _same("out", out, _U8, gpu, (n,))
-    with _on(gpu):
-        _check("qg_pack_i8", lib().qg_pack_i8(w.data_ptr(), ldw, out.data_ptr(), M, K, _raw_stream(gpu)))
+    _launch("qg_pack_i8", gpu, w.data_ptr(), ldw, out.data_ptr(), M, K)
     return out
 
 
@@ -703,20 +701,17 @@ def quantize_i8_rows(x: torch.Tensor, out: torch.Tensor | None = None, scale: to
     tokens for qgemm_i8, or the rows of a weight matrix before pack_i8. Returns
     (q int8 (N, ldq), scale float32 (N)), ldq = K rounded up to 64, zeros beyond K."""
     gpu = _gpu("x", x, _TYPES)
-    ldx = _rows_of("x", x, _TYPES, gpu, None, 0)
-    N, K = x.shape
+    N, K, ldx = _rows_of("x", x, _TYPES, gpu, None, 0)
     kp = (K + 63) // 64 * 64
     if out is None:
         out, ldq = torch.empty((N, kp), dtype=torch.int8, device=x.device), kp
     else:
-        ldq = _rows_of("out", out, _I8, gpu, N, kp)
+        ldq = _rows_of("out", out, _I8, gpu, N, kp)[2]
     if scale is None:
         scale = torch.empty(N, dtype=torch.float32, device=x.device)
     else:
         _same("scale", scale, _F32, gpu, (N,))
-    with _on(gpu):
-        _check("qg_quantize_i8_rows", lib().qg_quantize_i8_rows(x.data_ptr(), _TYPES[x.dtype], ldx, N, K, out.data_ptr(),
-                                                                ldq, scale.data_ptr(), _raw_stream(gpu)))
+    _launch("qg_quantize_i8_rows", gpu, x.data_ptr(), _TYPES[x.dtype], ldx, N, K, out.data_ptr(), ldq, scale.data_ptr())
     return out, scale
 
 
@@ -735,8 +730,7 @@ def qgemm_i8(w: torch.Tensor, w_scale: torch.Tensor, xq: torch.Tensor, x_scale: 
     gpu = _gpu("w", w, _U8)
     if w.numel() != L.qg_i8_bytes(M, K) or not w.is_contiguous():
         raise ValueError(f"w is not a packed {M} x {K} matrix")
-    ldx = _rows_of("xq", xq, _I8, gpu, None, (K + 63) // 64 * 64)
-    N = xq.shape[0]
+    N, _, ldx = _rows_of("xq", xq, _I8, gpu, None, (K + 63) // 64 * 64)
     _same("w_scale", w_scale, _F32, gpu, (M,))
     _same("x_scale", x_scale, _F32, gpu, (N,))
     if bias is not None:
@@ -747,11 +741,12 @@ def qgemm_i8(w: torch.Tensor, w_scale: torch.Tensor, xq: torch.Tensor, x_scale: 
         ldy = (M + 3) // 4 * 4
         Y = torch.empty((N, ldy), dtype=dtype, device=w.device)
     else:
-        ldy = _rows_of("Y", Y, _TYPES, gpu, N, M)
-    wp, wb, keep = _scratch(ws, L.qgemm_i8_workspace_bytes(M, K, N), w.device)
-    with _on(gpu):
-        _check("qgemm_i8", L.qgemm_i8(w.data_ptr(), w_scale.data_ptr(), xq.data_ptr(), ldx, x_scale.data_ptr(), _ptr(bias),
-                                      Y.data_ptr(), _TYPES[Y.dtype], ldy, M, K, N, wp, wb, _raw_stream(gpu)))
+        ldy = _rows_of("Y", Y, _TYPES, gpu, N, M)[2]
+        dtype = Y.dtype
+    need = L.qgemm_i8_workspace_bytes(M, K, N)
+    wp, wb, keep = _scratch(ws, need, w.device) if need else (None, 0, None)
+    _launch("qgemm_i8", gpu, w.data_ptr(), w_scale.data_ptr(), xq.data_ptr(), ldx, x_scale.data_ptr(),
+            None if bias is None else bias.data_ptr(), Y.data_ptr(), _TYPES[dtype], ldy, M, K, N, wp, wb)
     return Y
 
 
@@ -783,8 +778,7 @@ def logits_beam_select(logits: torch.Tensor, score: torch.Tensor, n: int, finish
     shape = score.shape
     B, W = shape
     _same("score", score, _F32, gpu, shape)
-    ld = _rows_of("logits", logits, _TYPES, gpu, B * W, 0)
-    V = logits.shape[1]
+    _, V, ld = _rows_of("logits", logits, _TYPES, gpu, B * W, 0)
     if finished is not None:
         _same("finished", finished, _FLAGS, gpu, shape)
     if length is not None:
@@ -800,9 +794,7 @@ def logits_beam_select(logits: torch.Tensor, score: torch.Tensor, n: int, finish
     wp, wb, keep = _scratch(ws, L.logits_beam_select_workspace_bytes(xt, B, W, V, n), logits.device)
     ci = _BeamIn(logits.data_ptr(), xt, ld, B, W, V, score.data_ptr(), _ptr(finished), _ptr(length), length_penalty, eos)
     co = _BeamOut(_ptr(out.token), _ptr(out.parent), _ptr(out.score), _ptr(out.finished), _ptr(out.length))
-    with _on(gpu):
-        _check("logits_beam_select", L.logits_beam_select(ctypes.byref(ci), n, wp, wb, ctypes.byref(co),
-                                                          _raw_stream(gpu)))
+    _launch("logits_beam_select", gpu, ctypes.byref(ci), n, wp, wb, ctypes.byref(co))
     return out
 
 
@@ -883,10 +875,7 @@ def beam_reorder(states, parent: torch.Tensor, out=None):
             fields += (p, p if d is s else d.data_ptr())
             fields += moves
     words = array.array("q", fields)
-    L, at, count = lib(), words.buffer_info()[0], len(words) // 8
-    with _on(gpu):
-        stream = _raw_stream(gpu)
-        for k in range(0, count, BEAM_MAX_STATES):
-            _check("qg_beam_reorder", L.qg_beam_reorder(at + k * 64, min(BEAM_MAX_STATES, count - k), parent.data_ptr(), B, W,
-                                                        n, stream))
+    at, count = words.buffer_info()[0], len(words) // 8
+    for k in range(0, count, BEAM_MAX_STATES):
+        _launch("qg_beam_reorder", gpu, at + k * 64, min(BEAM_MAX_STATES, count - k), parent.data_ptr(), B, W, n)
     return results

@@ -28,30 +28,37 @@ struct RArgs {
     int32_t beams_in, beams_out;
 };
 
+// Rows J .. W - 1 of one column: all of them are read before the first is written (the
+// reads of the later rows lie inside the call between a row's read and its write). As
+// a recursion over single values: an array of them became one wide register that every
+// branch copied (226 registers at eight beams, here 40).
+template <typename U, int W, int J>
+QG_DEV void move_rows(const uint8_t* src, uint8_t* dst, const RState& s, const int (&p)[W]) {
+    if constexpr (J < W) {
+        U v{};
+        if (p[J] >= 0) v = *reinterpret_cast<const U*>(src + p[J] * s.src_row);
+        move_rows<U, W, J + 1>(src, dst, s, p);
+        if (p[J] >= 0) *reinterpret_cast<U*>(dst + J * s.dst_row) = v;
+    }
+}
+
 template <typename U, int W>
 __global__ __launch_bounds__(256) void beam_reorder_kernel(RArgs a) {
     const RState& s = a.st[blockIdx.z];
     const uint32_t c = blockIdx.x * 256u + threadIdx.x;
     const int64_t b = blockIdx.y;
     const int32_t* par = a.parent + b * a.beams_out;
+    const bool inplace = s.src == s.dst;
     int p[W];  // parents of the rows that move, else -1
 #pragma unroll
-    for (int j = 0; j < W; ++j) p[j] = j < a.beams_out ? par[j] : -1;
-    const bool inplace = s.src == s.dst;
-#pragma unroll
-    for (int j = 0; j < W; ++j)
+    for (int j = 0; j < W; ++j) {
+        p[j] = j < a.beams_out ? par[j] : -1;
         if (p[j] < 0 || p[j] >= a.beams_in || (inplace && p[j] == j)) p[j] = -1;
+    }
     if (c >= s.cols) return;
     const uint32_t o = c / s.per, i = c - o * s.per;
-    const uint8_t* src = s.src + b * a.beams_in * s.src_row + o * s.src_outer + (int64_t)i * sizeof(U);
-    uint8_t* dst = s.dst + b * a.beams_out * s.dst_row + o * s.dst_outer + (int64_t)i * sizeof(U);
-    U v[W];
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-        if (p[j] >= 0) v[j] = *reinterpret_cast<const U*>(src + p[j] * s.src_row);
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-        if (p[j] >= 0) *reinterpret_cast<U*>(dst + j * s.dst_row) = v[j];
+    move_rows<U, W, 0>(s.src + b * a.beams_in * s.src_row + o * s.src_outer + (int64_t)i * sizeof(U),
+                       s.dst + b * a.beams_out * s.dst_row + o * s.dst_outer + (int64_t)i * sizeof(U), s, p);
 }
 
 // The largest unit of 16, 4 or 1 bytes that a state's pointers, strides and span allow.
