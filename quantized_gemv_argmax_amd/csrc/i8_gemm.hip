@@ -21,6 +21,8 @@ typedef int qi4 __attribute__((ext_vector_type(4)));
 constexpr int T = QG_TILE_ROWS;
 constexpr int kKB = 64;           // k per matrix-core operand
 constexpr int kTileB = T * kKB;   // bytes of one operand (16 rows x 64 k)
+constexpr int kWalkBlocks = 64;   // k blocks of the walk form (K <= 4096)
+constexpr int kWalkGroups = 512;  // its workgroups
 
 QG_DEV uint16_t f32_to_bf16(float v) {
     // round to nearest even; a NaN stays one
@@ -272,6 +274,18 @@ QG_DEV void row_scales(const GArgs& a, int m, float (&sw)[C], float (&sb)[C]) {
     }
 }
 
+// A lane's four sums of one 16 x 16 product: rows m .. m + 3 of column n.
+template <int YT>
+QG_DEV void store_quad(const GArgs& a, const qi4& s, int m, int n) {
+    if (n >= a.N || m >= a.M) return;
+    float sw[4], sb[4], y[4];
+    row_scales(a, m, sw, sb);
+    const float xs = a.xs[n];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = scaled(s[e], xs, sw[e], sb[e]);
+    store_row<YT>(a.Y, n * a.ldy + m, y, a.M - m);
+}
+
 // ---------------------------------------------------------------- few columns
 // One 16-row tile and NB blocks of 16 columns per workgroup; its KW wavefronts take
 // the k blocks in turn, and their integer sums meet in LDS. The weights go from
@@ -306,26 +320,74 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_stream_kernel(GArgs a) {
         qi4 s = part[0][c][lane];
 #pragma unroll
         for (int k = 1; k < KW; ++k) s += part[k][c][lane];
-        const int n = 16 * c + (lane & 15), m = t * T + (lane >> 4) * 4;
-        if (n < a.N && m < a.M) {
-            float sw[4], sb[4], y[4];
-            row_scales(a, m, sw, sb);
-            const float xs = a.xs[n];
+        store_quad<YT>(a, s, t * T + (lane >> 4) * 4, 16 * c + (lane & 15));
+    }
+}
+
+// The same for many weight tiles and K <= 4096: each wavefront keeps its k blocks of
+// the columns in registers (up to XR of them) while its workgroup walks over tiles, so
+// that only weights are loaded, a tile ahead. Sums of alternate tiles meet in
+// alternate LDS buffers, one barrier a tile; the wavefronts take turns at adding them.
+template <int YT, int NB>
+__global__ __launch_bounds__(256) void gemm_i8_walk_kernel(GArgs a) {
+    constexpr int KW = 4, XR = kWalkBlocks / KW;
+    __shared__ qi4 part[2][KW][NB][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int mine = (a.nb - wave + KW - 1) / KW;  // blocks wave, wave + KW, ..
+    qi4 wv[XR], xv[XR][NB];
+    auto load = [&](int t) {
+        const uint8_t* w = a.w + ((size_t)t * a.nb + wave) * kTileB + lane * 16;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = scaled(s[e], xs, sw[e], sb[e]);
-            store_row<YT>(a.Y, n * a.ldy + m, y, a.M - m);
-        }
+        for (int i = 0; i < XR; ++i)
+            if (i < mine) wv[i] = __builtin_nontemporal_load(reinterpret_cast<const qi4*>(w + (size_t)i * KW * kTileB));
+    };
+    int t = blockIdx.x;
+    load(t);
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {  // columns beyond N read the last one; their sums are not stored
+        const int8_t* x = a.x + (int64_t)min(16 * c + (lane & 15), a.N - 1) * a.ldx + (lane >> 4) * 16 + wave * kKB;
+#pragma unroll
+        for (int i = 0; i < XR; ++i)
+            if (i < mine) xv[i][c] = *reinterpret_cast<const qi4*>(x + i * KW * kKB);
+    }
+    for (int turn = 0; t < a.mtiles; ++turn) {
+        qi4 acc[NB];
+#pragma unroll
+        for (int c = 0; c < NB; ++c) acc[c] = qi4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < XR; ++i)
+            if (i < mine)
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+                    acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[i], xv[i][c], acc[c], 0, 0, 0);
+        const int next = t + gridDim.x;
+        if (next < a.mtiles) load(next);
+        const int buf = turn & 1;
+#pragma unroll
+        for (int c = 0; c < NB; ++c) part[buf][wave][c][lane] = acc[c];
+        // (the loads of the next tile stay on their way across the barrier)
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < NB; ++c)
+            if ((turn * NB + c) % KW == wave) {
+                qi4 s = part[buf][0][c][lane];
+#pragma unroll
+                for (int k = 1; k < KW; ++k) s += part[buf][k][c][lane];
+                store_quad<YT>(a, s, t * T + (lane >> 4) * 4, 16 * c + (lane & 15));
+            }
+        t = next;
     }
 }
 
 // ---------------------------------------------------------------- many columns
 // Y in tiles of BM weight rows x BN columns, one per workgroup of WM x WN
-// wavefronts, K in tiles of 128 bytes through two LDS buffers.
-template <int BM, int BN, int WM, int WN>
+// wavefronts, K in tiles of 128 bytes through NS LDS buffers.
+template <int BM, int BN, int WM, int WN, int NS_>
 struct Tile {
+    static constexpr int NS = NS_;
     static constexpr int W = WM * WN;
     static constexpr int MT = BM / WM / 16, CT = BN / WN / 16;    // 16 x 16 products of a wavefront
-    static constexpr int AB = BM * 128, XB = BN * 128, STAGE = AB + XB, LDS = 2 * STAGE;
+    static constexpr int AB = BM * 128, XB = BN * 128, STAGE = AB + XB, LDS = NS * STAGE;
     static constexpr int AU = AB / 1024 / W, XU = XB / 1024 / W;  // 1 KB loads of a wavefront
     static_assert(MT % 2 == 0 && AU * 1024 * W == AB && XU * 1024 * W == XB, "tile does not split evenly");
 };
@@ -337,28 +399,39 @@ QG_DEV void lds_load(const __amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, voff, soff, 0, 0);
 }
 
-// Every wavefront's loads have arrived and its LDS reads are done, for all of them.
-QG_DEV void tile_sync() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// All but the last LATER of every wavefront's loads have arrived and its LDS reads are
+// done, for all wavefronts of the workgroup.
+template <int LATER>
+QG_DEV void tile_sync() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATER) : "memory");
+}
 
 // Outputs of a wavefront's accumulators. Product i of a pair (2c, 2c + 1) holds in its
 // row 4 q + e the weight row 32 c + 8 q + 4 (i % 2) + e, so a lane's pair is eight
 // consecutive outputs and four lanes' pairs are 32.
+template <int CT>
+struct PairScales {
+    float sw[8], sb[8], xs[CT];
+    QG_DEV PairScales(const GArgs& a, int m, int n0) {
+        row_scales(a, m, sw, sb);
+#pragma unroll
+        for (int j = 0; j < CT; ++j) xs[j] = a.xs[min(n0 + 16 * j, a.N - 1)];
+    }
+};
 template <int YT, int CT>
-QG_DEV void store_pair(const GArgs& a, const qi4 (&lo)[CT], const qi4 (&hi)[CT], int m, int n0) {
+QG_DEV void store_pair(const GArgs& a, const qi4 (&lo)[CT], const qi4 (&hi)[CT], const PairScales<CT>& p, int m,
+                       int n0) {
     const int count = a.M - m;
     if (count <= 0) return;
-    float sw[8], sb[8];
-    row_scales(a, m, sw, sb);
 #pragma unroll
     for (int j = 0; j < CT; ++j) {
         const int n = n0 + 16 * j;
         if (n < a.N) {
-            const float xs = a.xs[n];
             float y[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                y[e] = scaled(lo[j][e], xs, sw[e], sb[e]);
-                y[4 + e] = scaled(hi[j][e], xs, sw[4 + e], sb[4 + e]);
+                y[e] = scaled(lo[j][e], p.xs[j], p.sw[e], p.sb[e]);
+                y[4 + e] = scaled(hi[j][e], p.xs[j], p.sw[4 + e], p.sb[4 + e]);
             }
             store_row<YT>(a.Y, n * a.ldy + m, y, count);
         }
@@ -382,9 +455,9 @@ QG_DEV TileAt tile_at(const GArgs& a, int id) {
     return {(grp * GM + rem % gm) * (BM / 16), rem / gm * BN};
 }
 
-template <int YT, int BM, int BN, int WM, int WN, bool SPLIT>
+template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
-    typedef Tile<BM, BN, WM, WN> G;
+    typedef Tile<BM, BN, WM, WN, NS> G;
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -453,30 +526,35 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
     };
 
     // One barrier per K tile, between its two halves: the second half's operands are in
-    // registers then, so its buffer can be refilled, and the next tile's loads, sent a
-    // whole tile earlier, have arrived.
+    // registers then, so its buffer can be refilled, with the tile NS later; the next
+    // tile's loads, sent NS - 1 tiles earlier, have arrived, those of the NS - 2 tiles
+    // after it may still be on their way.
+    constexpr int U = G::AU + G::XU;
     qi4 a0[G::MT], x0[G::CT], a1[G::MT], x1[G::CT];
-    fetch(k0, 0);
-    tile_sync();
-    if (k0 + 1 < k1) fetch(k0 + 1, 1);
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+        if (k0 + i < k1) fetch(k0 + i, i);
+    if (k0 + NS <= k1)
+        tile_sync<(NS - 1) * U>();
+    else
+        tile_sync<0>();
     frags(0, 0, a0, x0);
     int t = k0, buf = 0;
-    for (; t + 2 < k1; ++t, buf ^= 1) {
+    auto next = [&](int i) { return i + 1 == NS ? 0 : i + 1; };
+    for (; t + NS < k1; ++t, buf = next(buf)) {
         frags(buf, 1, a1, x1);
         mma(a0, x0);
-        tile_sync();
-        frags(buf ^ 1, 0, a0, x0);
-        fetch(t + 2, buf);
+        tile_sync<(NS - 2) * U>();
+        frags(next(buf), 0, a0, x0);
+        fetch(t + NS, buf);
         mma(a1, x1);
     }
-    if (t + 1 < k1) {
+    for (; t + 1 < k1; ++t, buf = next(buf)) {
         frags(buf, 1, a1, x1);
         mma(a0, x0);
-        tile_sync();
-        frags(buf ^ 1, 0, a0, x0);
+        tile_sync<0>();
+        frags(next(buf), 0, a0, x0);
         mma(a1, x1);
-        ++t;
-        buf ^= 1;
     }
     frags(buf, 1, a1, x1);
     mma(a0, x0);
@@ -490,9 +568,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
             for (int j = 0; j < G::CT; ++j) p[(i * G::CT + j) * 64] = acc[i][j];
     } else {
 #pragma unroll
-        for (int c = 0; c < G::MT / 2; ++c)
-            store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], (t0 + wm * G::MT + 2 * c) * 16 + q * 8,
-                                  n0 + wn * G::CT * 16 + r);
+        for (int c = 0; c < G::MT / 2; ++c) {
+            const int m = (t0 + wm * G::MT + 2 * c) * 16 + q * 8, n = n0 + wn * G::CT * 16 + r;
+            store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], PairScales<G::CT>(a, m, n), m, n);
+        }
     }
 }
 
@@ -500,7 +579,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
 // a tile wavefront's products.
 template <int YT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64) void gemm_i8_join_kernel(GArgs a, int tiles, int splits) {
-    typedef Tile<BM, BN, WM, WN> G;
+    typedef Tile<BM, BN, WM, WN, 2> G;
     const int lane = threadIdx.x;
     const int c = blockIdx.x % (G::MT / 2), wave = blockIdx.x / (G::MT / 2) % G::W;
     const int id = blockIdx.x / (G::MT / 2 * G::W);
@@ -508,6 +587,8 @@ __global__ __launch_bounds__(64) void gemm_i8_join_kernel(GArgs a, int tiles, in
     const int wm = wave % WM, wn = wave / WM, r = lane & 15, q = lane >> 4;
     const qi4* p = a.part + (((size_t)id * G::W + wave) * (G::MT * G::CT) + 2 * c * G::CT) * 64 + lane;
     const size_t step = (size_t)tiles * G::W * (G::MT * G::CT) * 64;
+    const int m = (at.t0 + wm * G::MT + 2 * c) * 16 + q * 8, n = at.n0 + wn * G::CT * 16 + r;
+    const PairScales<G::CT> sc(a, m, n);  // (on their way while the sums are)
     qi4 lo[G::CT], hi[G::CT];
 #pragma unroll
     for (int j = 0; j < G::CT; ++j) lo[j] = hi[j] = qi4{0, 0, 0, 0};
@@ -518,28 +599,30 @@ __global__ __launch_bounds__(64) void gemm_i8_join_kernel(GArgs a, int tiles, in
             lo[j] += p[j * 64];
             hi[j] += p[(G::CT + j) * 64];
         }
-    store_pair<YT, G::CT>(a, lo, hi, (at.t0 + wm * G::MT + 2 * c) * 16 + q * 8, at.n0 + wn * G::CT * 16 + r);
+    store_pair<YT, G::CT>(a, lo, hi, sc, m, n);
 }
 
 // ---------------------------------------------------------------- launches
 // How a product runs: N <= 32 streams the weights past the columns; else a tile form,
 // perhaps split along K.
-enum { FORM_STREAM, FORM_64, FORM_128, FORM_256 };
+enum { FORM_STREAM, FORM_64, FORM_128_DEEP, FORM_128, FORM_256 };
 struct Plan {
     int form, tiles, splits, kper;
     size_t ws;
 };
 
 // The largest tile that still gives most compute units one, larger tiles reading the
-// operands less often: 37888 x 3584 by 4096 columns takes 534 us in tiles of 256 and
-// 1094 in tiles of 64; 18944 x 3584 by 256 takes 36.0 us in 296 tiles of 128 and 45.3
-// in 74 of 256 split three ways. With fewer tiles K is split until about 448
-// workgroups share it, each keeping at least 7 K tiles (14 of the larger ones) to repay
-// the second launch:
-// 3584 x 18944 by 64 columns takes 24.7 us in 8 splits and 33.9 in 4; 4608 x 3584 by
-// 64 12.2 in 4 and 13.4 in 7. Tiles of 128 are split where K is long (3584 x 18944 by
-// 256: 42.4 us, tiles of 64 46.4), tiles of 64 where it is not (4608 x 3584 by 512:
-// 19.8 us in 576 tiles, 23.4 in 144 of 128 split three ways).
+// operands less often (37888 x 3584 by 4096 columns: 534 us in tiles of 256, 1094 in
+// tiles of 64; 18944 x 3584 by 256: 36 us in 296 tiles of 128, 45 in 74 of 256 split
+// three ways; 1000 x 1000 by 1000: 6.2 us in 256 tiles of 64, 9.6 in 64 of 128), but
+// tiles of 128 where K is long (3584 x 18944 by 256: 36 us, tiles of 64 43).
+// Tiles of 128 take three LDS buffers up to a workgroup per compute unit, two, with two
+// workgroups per unit, beyond (296 tiles: 36 us, with three buffers 45; 144 tiles of
+// 4608 x 3584 by 512: 23 us, with three 19).
+// With fewer tiles than units a long K is split until about 256 workgroups share it,
+// each keeping some K tiles to repay the second launch: 3584 x 18944 by 64 columns takes
+// 21.1 us in 4 splits of tiles of 64 (3: 24.4, 8: 22.7), 4608 x 3584 by 64 9.9 unsplit
+// and 10.6 in two; in tiles of 128, 3584 x 18944 by 128 26 us in 8 and 28 in 6.
 Plan plan(int64_t M, int64_t K, int64_t N) {
     Plan p{};
     const int kt = (int)qg::ceil_div(K, 2 * kKB);
@@ -554,16 +637,16 @@ Plan plan(int64_t M, int64_t K, int64_t N) {
     int side = 64;
     if (N > 64 && tiles(256) >= 192)
         side = 256;
-    else if (N > 64 && (tiles(128) >= 192 || kt >= 64))
+    else if (N > 64 && (tiles(128) >= 128 || kt >= 64))
         side = 128;
-    p.form = side == 256 ? FORM_256 : side == 128 ? FORM_128 : FORM_64;
     p.tiles = (int)tiles(side);
-    const int s = side == 256 ? 1 : (int)std::min<int64_t>({448 / tiles(side), kt / (side == 128 ? 14 : 7), 16});
+    p.form = side == 256 ? FORM_256 : side == 64 ? FORM_64 : p.tiles > 256 ? FORM_128 : FORM_128_DEEP;
+    const int s = side == 256 ? 1 : std::min(256 / p.tiles, kt / (side == 128 ? 18 : 28));
     if (s > 1) {
         p.kper = (int)qg::ceil_div(kt, s);
         p.splits = (int)qg::ceil_div(kt, p.kper);
+        p.ws = (size_t)p.splits * p.tiles * side * side * 4;
     }
-    if (p.splits > 1) p.ws = (size_t)p.splits * p.tiles * side * side * 4;
     return p;
 }
 
@@ -578,35 +661,47 @@ qg_status allow_lds(const void* f, int bytes, std::atomic<bool>* done) {
     return QG_OK;
 }
 
-template <int YT, int B, int WM, int WN>
+template <int YT, int B, int WM, int WN, int NS, bool SPLIT>
 qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
-    typedef Tile<B, B, WM, WN> G;
+    typedef Tile<B, B, WM, WN, NS> G;
     if constexpr (G::LDS > 65536) {
         static std::atomic<bool> done[64];
         const qg_status st =
-            allow_lds(reinterpret_cast<const void*>(&gemm_i8_tile_kernel<YT, B, B, WM, WN, false>), G::LDS, done);
+            allow_lds(reinterpret_cast<const void*>(&gemm_i8_tile_kernel<YT, B, B, WM, WN, NS, SPLIT>), G::LDS, done);
         if (st) return st;
-    } else if (p.splits > 1) {
-        hipLaunchKernelGGL((gemm_i8_tile_kernel<YT, B, B, WM, WN, true>), dim3(p.tiles, p.splits), dim3(64 * G::W),
-                           G::LDS, s, a);
-        const qg_status st = qg::launch_status("qgemm_i8 (split)");
+    }
+    hipLaunchKernelGGL((gemm_i8_tile_kernel<YT, B, B, WM, WN, NS, SPLIT>), dim3(p.tiles, p.splits), dim3(64 * G::W),
+                       G::LDS, s, a);
+    qg_status st = qg::launch_status("qgemm_i8");
+    if constexpr (SPLIT) {
         if (st) return st;
         hipLaunchKernelGGL((gemm_i8_join_kernel<YT, B, B, WM, WN>), dim3(p.tiles * G::W * (G::MT / 2)), dim3(64), 0, s,
                            a, p.tiles, p.splits);
-        return qg::launch_status("qgemm_i8 (join)");
+        st = qg::launch_status("qgemm_i8 (join)");
     }
-    hipLaunchKernelGGL((gemm_i8_tile_kernel<YT, B, B, WM, WN, false>), dim3(p.tiles), dim3(64 * G::W), G::LDS, s, a);
-    return qg::launch_status("qgemm_i8");
+    return st;
 }
 
 template <int YT>
 qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
+    const bool split = p.splits > 1;
     switch (p.form) {
-        case FORM_64: return launch_tiles<YT, 64, 2, 2>(a, p, s);
-        case FORM_128: return launch_tiles<YT, 128, 2, 4>(a, p, s);
-        case FORM_256: return launch_tiles<YT, 256, 4, 2>(a, p, s);
+        case FORM_64: return split ? launch_tiles<YT, 64, 2, 2, 4, true>(a, p, s) : launch_tiles<YT, 64, 2, 2, 4, false>(a, p, s);
+        case FORM_128_DEEP:
+            return split ? launch_tiles<YT, 128, 2, 4, 3, true>(a, p, s) : launch_tiles<YT, 128, 2, 4, 3, false>(a, p, s);
+        case FORM_128: return launch_tiles<YT, 128, 2, 4, 2, false>(a, p, s);
+        case FORM_256: return launch_tiles<YT, 256, 4, 2, 2, false>(a, p, s);
     }
-    if (a.N <= 16)
+    // Few columns. The walk needs a tile for each of its workgroups, and K long enough
+    // that the barrier of a tile does not show: 152064 x 3584 takes 96 us at 16 columns
+    // and 104 at 32 (a tile per workgroup: 122 and 179), 4608 x 3584 at 4 columns 6.8
+    // (5.9), 20000 x 512 at 10 columns 5.9 (4.3).
+    const bool walk = a.mtiles >= kWalkGroups && a.nb >= 16 && a.nb <= kWalkBlocks;
+    if (walk && a.N <= 16)
+        hipLaunchKernelGGL((gemm_i8_walk_kernel<YT, 1>), dim3(kWalkGroups), dim3(256), 0, s, a);
+    else if (walk)
+        hipLaunchKernelGGL((gemm_i8_walk_kernel<YT, 2>), dim3(kWalkGroups), dim3(256), 0, s, a);
+    else if (a.N <= 16)
         hipLaunchKernelGGL((gemm_i8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
     else
         hipLaunchKernelGGL((gemm_i8_stream_kernel<YT, 2, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
