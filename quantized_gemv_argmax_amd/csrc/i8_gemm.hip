@@ -66,6 +66,7 @@ struct XVec;  // elements per 16-byte vector and their conversion to fp32
 template <>
 struct XVec<QG_F32> {
     typedef float E;
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(4)));
     static constexpr int N = 4;
     QG_DEV static float get(const uint4& v, int i) { return __builtin_bit_cast(float, (&v.x)[i]); }
     QG_DEV static float one(E e) { return e; }
@@ -73,6 +74,7 @@ struct XVec<QG_F32> {
 template <>
 struct XVec<QG_F16> {
     typedef uint16_t E;
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
     static constexpr int N = 8;
     QG_DEV static float get(const uint4& v, int i) {
         return (i & 1) ? qg_half_hi((&v.x)[i >> 1]) : qg_half_lo((&v.x)[i >> 1]);
@@ -82,6 +84,7 @@ struct XVec<QG_F16> {
 template <>
 struct XVec<QG_BF16> {
     typedef uint16_t E;
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
     static constexpr int N = 8;
     QG_DEV static float get(const uint4& v, int i) {
         const uint32_t w = (&v.x)[i >> 1];
@@ -90,14 +93,18 @@ struct XVec<QG_BF16> {
     QG_DEV static float one(E e) { return __builtin_bit_cast(float, (uint32_t)e << 16); }
 };
 
-// The 16-byte vector i of a row of K elements, zeros beyond K. `vec`: the row is
-// 16-byte aligned.
+// The 16-byte vector i of a row of K elements, zeros beyond K. Rows start at any
+// element: full vectors are one load whatever their alignment.
 template <int XT>
-QG_DEV uint4 row_vec(const typename XVec<XT>::E* p, int K, int i, bool vec) {
+QG_DEV uint4 row_vec(const typename XVec<XT>::E* p, int K, int i) {
     typedef typename XVec<XT>::E E;
+    typedef typename XVec<XT>::V vec;
     constexpr int N = XVec<XT>::N;
     const int k0 = i * N;
-    if (vec && k0 + N <= K) return *reinterpret_cast<const uint4*>(p + k0);
+    if (k0 + N <= K) {
+        const vec v = *reinterpret_cast<const vec*>(p + k0);
+        return make_uint4(v.x, v.y, v.z, v.w);
+    }
     union {
         uint4 v;
         E e[N];
@@ -157,7 +164,6 @@ __global__ __launch_bounds__(NT) void quantize_i8_kernel(const void* __restrict_
     const int tid = threadIdx.x;
     const E* p = reinterpret_cast<const E*>(x) + n * ldx;
     int8_t* o = q + n * ldq;
-    const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
     const int nv = (K + kKB - 1) / kKB * (kKB / N);  // vectors, the zero padding included
 
     // the largest |x| by its bits: above every finite value an infinity, above it a NaN
@@ -172,12 +178,12 @@ __global__ __launch_bounds__(NT) void quantize_i8_kernel(const void* __restrict_
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             v[r] = make_uint4(0, 0, 0, 0);
-            if (tid + r * NT < nv) v[r] = row_vec<XT>(p, K, tid + r * NT, vec);
+            if (tid + r * NT < nv) v[r] = row_vec<XT>(p, K, tid + r * NT);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) peak(v[r]);
     } else {
-        for (int i = tid; i < nv; i += NT) peak(row_vec<XT>(p, K, i, vec));
+        for (int i = tid; i < nv; i += NT) peak(row_vec<XT>(p, K, i));
     }
 #pragma unroll
     for (int m = 32; m; m >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, m));
@@ -200,7 +206,7 @@ __global__ __launch_bounds__(NT) void quantize_i8_kernel(const void* __restrict_
         for (int r = 0; r < R; ++r)
             if (tid + r * NT < nv) store_q<XT>(o, tid + r * NT, v[r], s, d, inv, ok);
     } else {
-        for (int i = tid; i < nv; i += NT) store_q<XT>(o, i, row_vec<XT>(p, K, i, vec), s, d, inv, ok);
+        for (int i = tid; i < nv; i += NT) store_q<XT>(o, i, row_vec<XT>(p, K, i), s, d, inv, ok);
     }
 }
 
@@ -720,12 +726,16 @@ void launch_quantize(const void* x, int64_t ldx, int64_t N, int K, int8_t* q, in
                      hipStream_t s) {
     const int nv = (int)qg::ceil_div(K, kKB) * (kKB / XVec<XT>::N);
     const dim3 g((unsigned)N);
-    if (nv <= 512)
+    if (nv <= 256)
+        hipLaunchKernelGGL((quantize_i8_kernel<XT, 64, 4>), g, dim3(64), 0, s, x, ldx, K, q, ldq, scale);
+    else if (nv <= 512)
         hipLaunchKernelGGL((quantize_i8_kernel<XT, 256, 2>), g, dim3(256), 0, s, x, ldx, K, q, ldq, scale);
+    else if (nv <= 1280)
+        hipLaunchKernelGGL((quantize_i8_kernel<XT, 256, 5>), g, dim3(256), 0, s, x, ldx, K, q, ldq, scale);
     else if (nv <= 2560)
-        hipLaunchKernelGGL((quantize_i8_kernel<XT, 256, 10>), g, dim3(256), 0, s, x, ldx, K, q, ldq, scale);
+        hipLaunchKernelGGL((quantize_i8_kernel<XT, 512, 5>), g, dim3(512), 0, s, x, ldx, K, q, ldq, scale);
     else if (nv <= 5120)
-        hipLaunchKernelGGL((quantize_i8_kernel<XT, 512, 10>), g, dim3(512), 0, s, x, ldx, K, q, ldq, scale);
+        hipLaunchKernelGGL((quantize_i8_kernel<XT, 1024, 5>), g, dim3(1024), 0, s, x, ldx, K, q, ldq, scale);
     else
         hipLaunchKernelGGL((quantize_i8_kernel<XT, 1024, 0>), g, dim3(1024), 0, s, x, ldx, K, q, ldq, scale);
 }
