@@ -224,6 +224,7 @@ struct GArgs {
     int32_t M, N, nb;    // nb: k blocks of 64
     int32_t mtiles;      // 16-row tiles of W
     int32_t kper;        // K tiles (two blocks) of a split
+    int32_t total;       // tiles of Y
 };
 
 QG_DEV float scaled(int acc, float xs, float ws, float b) { return (float)acc * (xs * ws) + b; }
@@ -258,8 +259,12 @@ QG_DEV void store_row(void* Y, int64_t at, const float (&y)[C], int count) {
 #pragma unroll
         for (int e = 0; e < C / 2; ++e) h[e] = pack2<YT>(y[2 * e], y[2 * e + 1]);
         if (count >= C) {
+            // (rows are 8 bytes aligned; one store of 16 all the same)
+            typedef uint32_t vec __attribute__((ext_vector_type(C / 2), aligned(8)));
+            vec v;
 #pragma unroll
-            for (int c = 0; c < C / 4; ++c) reinterpret_cast<uint2*>(p)[c] = make_uint2(h[2 * c], h[2 * c + 1]);
+            for (int e = 0; e < C / 2; ++e) v[e] = h[e];
+            *reinterpret_cast<vec*>(p) = v;
         } else {
 #pragma unroll
             for (int e = 0; e < C; ++e)
@@ -386,7 +391,7 @@ __global__ __launch_bounds__(256) void gemm_i8_walk_kernel(GArgs a) {
 }
 
 // ---------------------------------------------------------------- many columns
-// Y in tiles of BM weight rows x BN columns, one per workgroup of WM x WN
+// Y in tiles of BM weight rows x BN columns, one at a time per workgroup of WM x WN
 // wavefronts, K in tiles of 128 bytes through NS LDS buffers.
 template <int BM, int BN, int WM, int WN, int NS_>
 struct Tile {
@@ -410,6 +415,27 @@ QG_DEV void lds_load(const __amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff
 template <int LATER>
 QG_DEV void tile_sync() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATER) : "memory");
+}
+
+// Order of a half tile's instructions: its LDS reads, then its loads, each followed by an
+// even share of the products, nothing moved across its end. (Left to itself the compiler
+// bunches the reads in front of their first use: 546 us instead of 523 for 37888 x 3584
+// by 4096 columns.)
+template <int READS, int LOADS, int PRODUCTS>
+QG_DEV void interleave() {
+    constexpr int share = PRODUCTS / (READS + LOADS) > 0 ? PRODUCTS / (READS + LOADS) : 1;
+#pragma unroll
+    for (int i = 0; i < READS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x8, share, 0);  // matrix product
+    }
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);  // load
+        __builtin_amdgcn_sched_group_barrier(0x8, share, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, PRODUCTS, 0);
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Outputs of a wavefront's accumulators. Product i of a pair (2c, 2c + 1) holds in its
@@ -467,8 +493,6 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const TileAt at = tile_at<BM, BN>(a, blockIdx.x);
-    const int t0 = at.t0, n0 = at.n0;
     const int k0 = SPLIT ? blockIdx.y * a.kper : 0;
     const int k1 = SPLIT ? min((a.nb + 1) / 2, k0 + a.kper) : (a.nb + 1) / 2;
 
@@ -476,23 +500,30 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
     // not stored). Weights arrive in the packed order. Activations: eight lanes per row
     // of 128 bytes, the 16-byte chunk c of row r at place c ^ (r % 8), which spreads
     // the operand reads over the banks.
-    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(a.w + (size_t)t0 * a.nb * kTileB), (short)0,
-        (int)min((int64_t)(a.mtiles - t0) * a.nb * kTileB, (int64_t)INT32_MAX), kQgRawBufferFlags);
-    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(a.x + n0 * a.ldx), (short)0,
-        (int)min((int64_t)(a.N - 1 - n0) * a.ldx + a.nb * kKB, (int64_t)INT32_MAX), kQgRawBufferFlags);
-    uint32_t woff[G::AU], xoff[G::XU];
-#pragma unroll
-    for (int u = 0; u < G::AU; ++u)
-        woff[u] = (uint32_t)min((wave * G::AU + u) >> 1, a.mtiles - 1 - t0) * (uint32_t)a.nb * kTileB + lane * 16u;
     const int chunk = (lane & 7) ^ (lane >> 3);
-#pragma unroll
-    for (int u = 0; u < G::XU; ++u)
-        xoff[u] = (uint32_t)min((wave * G::XU + u) * 8 + (lane >> 3), a.N - 1 - n0) * (uint32_t)a.ldx + chunk * 16u;
     // an odd last block: its row ends after half of the 128 bytes, the lanes of the
     // other half read the first one again (and no product uses what they read)
     const uint32_t back = chunk >= 4 ? 64u : 0u;
+    __amdgpu_buffer_rsrc_t wr, xr;
+    uint32_t woff[G::AU], xoff[G::XU];
+    int t0, n0;
+    auto aim = [&](int id) {
+        const TileAt at = tile_at<BM, BN>(a, id);
+        t0 = at.t0;
+        n0 = at.n0;
+        wr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + (size_t)t0 * a.nb * kTileB), (short)0,
+                                               (int)min((int64_t)(a.mtiles - t0) * a.nb * kTileB, (int64_t)INT32_MAX),
+                                               kQgRawBufferFlags);
+        xr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.x + n0 * a.ldx), (short)0,
+                                               (int)min((int64_t)(a.N - 1 - n0) * a.ldx + a.nb * kKB, (int64_t)INT32_MAX),
+                                               kQgRawBufferFlags);
+#pragma unroll
+        for (int u = 0; u < G::AU; ++u)
+            woff[u] = (uint32_t)min((wave * G::AU + u) >> 1, a.mtiles - 1 - t0) * (uint32_t)a.nb * kTileB + lane * 16u;
+#pragma unroll
+        for (int u = 0; u < G::XU; ++u)
+            xoff[u] = (uint32_t)min((wave * G::XU + u) * 8 + (lane >> 3), a.N - 1 - n0) * (uint32_t)a.ldx + chunk * 16u;
+    };
     auto fetch = [&](int t, int buf) {
         uint8_t* A = lds + buf * G::STAGE;
         uint8_t* X = A + G::AB;
@@ -505,14 +536,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
 #pragma unroll
         for (int u = 0; u < G::XU; ++u) lds_load(xr, X + (wave * G::XU + u) * 1024, xoff[u] - sub, t * 128);
     };
+    auto start = [&]() {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (k0 + i < k1) fetch(k0 + i, i);
+    };
 
     const int wm = wave % WM, wn = wave / WM;
     const int r = lane & 15, q = lane >> 4;
     qi4 acc[G::MT][G::CT];
-#pragma unroll
-    for (int i = 0; i < G::MT; ++i)
-#pragma unroll
-        for (int j = 0; j < G::CT; ++j) acc[i][j] = qi4{0, 0, 0, 0};
     const int arow = (wm * G::MT + (r >> 3)) * 2048 + (q * 16 + ((r >> 2) & 1) * 8 + (r & 3)) * 16;
     const int xrow = (wn * G::CT * 16 + r) * 128;
     auto frags = [&](int buf, int h, qi4(&fa)[G::MT], qi4(&fx)[G::CT]) {
@@ -535,48 +567,71 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_tile_kernel(GArgs a) {
     // registers then, so its buffer can be refilled, with the tile NS later; the next
     // tile's loads, sent NS - 1 tiles earlier, have arrived, those of the NS - 2 tiles
     // after it may still be on their way.
+    // A workgroup with another tile to do sends that tile's first loads before it stores
+    // this one's outputs.
     constexpr int U = G::AU + G::XU;
-    qi4 a0[G::MT], x0[G::CT], a1[G::MT], x1[G::CT];
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-        if (k0 + i < k1) fetch(k0 + i, i);
-    if (k0 + NS <= k1)
-        tile_sync<(NS - 1) * U>();
-    else
-        tile_sync<0>();
-    frags(0, 0, a0, x0);
-    int t = k0, buf = 0;
-    auto next = [&](int i) { return i + 1 == NS ? 0 : i + 1; };
-    for (; t + NS < k1; ++t, buf = next(buf)) {
-        frags(buf, 1, a1, x1);
-        mma(a0, x0);
-        tile_sync<(NS - 2) * U>();
-        frags(next(buf), 0, a0, x0);
-        fetch(t + NS, buf);
-        mma(a1, x1);
-    }
-    for (; t + 1 < k1; ++t, buf = next(buf)) {
-        frags(buf, 1, a1, x1);
-        mma(a0, x0);
-        tile_sync<0>();
-        frags(next(buf), 0, a0, x0);
-        mma(a1, x1);
-    }
-    frags(buf, 1, a1, x1);
-    mma(a0, x0);
-    if (2 * t + 1 < a.nb) mma(a1, x1);
-
-    if constexpr (SPLIT) {
-        qi4* p = a.part + ((((size_t)blockIdx.y * gridDim.x + blockIdx.x) * G::W + wave) * (G::MT * G::CT)) * 64 + lane;
+    int id = blockIdx.x;
+    aim(id);
+    start();
+    while (true) {
 #pragma unroll
         for (int i = 0; i < G::MT; ++i)
 #pragma unroll
-            for (int j = 0; j < G::CT; ++j) p[(i * G::CT + j) * 64] = acc[i][j];
-    } else {
+            for (int j = 0; j < G::CT; ++j) acc[i][j] = qi4{0, 0, 0, 0};
+        qi4 a0[G::MT], x0[G::CT], a1[G::MT], x1[G::CT];
+        if (k0 + NS <= k1)
+            tile_sync<(NS - 1) * U>();
+        else
+            tile_sync<0>();
+        frags(0, 0, a0, x0);
+        int t = k0, buf = 0;
+        auto next = [&](int i) { return i + 1 == NS ? 0 : i + 1; };
+        for (; t + NS < k1; ++t, buf = next(buf)) {
+            frags(buf, 1, a1, x1);
+            mma(a0, x0);
+            interleave<G::MT + G::CT, 0, G::MT * G::CT>();
+            tile_sync<(NS - 2) * U>();
+            __builtin_amdgcn_sched_barrier(0);
+            frags(next(buf), 0, a0, x0);
+            fetch(t + NS, buf);
+            mma(a1, x1);
+            interleave<G::MT + G::CT, U, G::MT * G::CT>();
+        }
+        for (; t + 1 < k1; ++t, buf = next(buf)) {
+            frags(buf, 1, a1, x1);
+            mma(a0, x0);
+            tile_sync<0>();
+            frags(next(buf), 0, a0, x0);
+            mma(a1, x1);
+        }
+        frags(buf, 1, a1, x1);
+        mma(a0, x0);
+        const int m0 = (t0 + wm * G::MT) * 16 + q * 8, c0 = n0 + wn * G::CT * 16 + r;
+        if constexpr (SPLIT) {
+            if (2 * t + 1 < a.nb) mma(a1, x1);
+            qi4* p = a.part + ((((size_t)blockIdx.y * gridDim.x + blockIdx.x) * G::W + wave) * (G::MT * G::CT)) * 64 + lane;
 #pragma unroll
-        for (int c = 0; c < G::MT / 2; ++c) {
-            const int m = (t0 + wm * G::MT + 2 * c) * 16 + q * 8, n = n0 + wn * G::CT * 16 + r;
-            store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], PairScales<G::CT>(a, m, n), m, n);
+            for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < G::CT; ++j) p[(i * G::CT + j) * 64] = acc[i][j];
+            return;
+        } else {
+            id += gridDim.x;
+            const bool more = id < a.total;
+            // (the scales first: waiting for them must not mean waiting for the loads)
+            PairScales<G::CT> sc(a, m0, c0);
+            if (more) {
+                tile_sync<0>();
+                aim(id);
+                start();
+            }
+            if (2 * t + 1 < a.nb) mma(a1, x1);
+#pragma unroll
+            for (int c = 0; c < G::MT / 2; ++c) {
+                if (c) row_scales(a, m0 + 32 * c, sc.sw, sc.sb);
+                store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sc, m0 + 32 * c, c0);
+            }
+            if (!more) return;
         }
     }
 }
@@ -670,13 +725,16 @@ qg_status allow_lds(const void* f, int bytes, std::atomic<bool>* done) {
 template <int YT, int B, int WM, int WN, int NS, bool SPLIT>
 qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
     typedef Tile<B, B, WM, WN, NS> G;
+    // tiles of 256: a workgroup per compute unit takes tile after tile (523 -> 512 us for
+    // 37888 x 3584 by 4096 columns); smaller ones share a unit, which overlaps as much
+    const int groups = B == 256 ? std::min(p.tiles, qg::device_cus()) : p.tiles;
     if constexpr (G::LDS > 65536) {
         static std::atomic<bool> done[64];
         const qg_status st =
             allow_lds(reinterpret_cast<const void*>(&gemm_i8_tile_kernel<YT, B, B, WM, WN, NS, SPLIT>), G::LDS, done);
         if (st) return st;
     }
-    hipLaunchKernelGGL((gemm_i8_tile_kernel<YT, B, B, WM, WN, NS, SPLIT>), dim3(p.tiles, p.splits), dim3(64 * G::W),
+    hipLaunchKernelGGL((gemm_i8_tile_kernel<YT, B, B, WM, WN, NS, SPLIT>), dim3(groups, p.splits), dim3(64 * G::W),
                        G::LDS, s, a);
     qg_status st = qg::launch_status("qgemm_i8");
     if constexpr (SPLIT) {
@@ -696,7 +754,7 @@ qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
         case FORM_128_DEEP:
             return split ? launch_tiles<YT, 128, 2, 4, 3, true>(a, p, s) : launch_tiles<YT, 128, 2, 4, 3, false>(a, p, s);
         case FORM_128: return launch_tiles<YT, 128, 2, 4, 2, false>(a, p, s);
-        case FORM_256: return launch_tiles<YT, 256, 4, 2, 2, false>(a, p, s);
+        case FORM_256: return launch_tiles<YT, 256, 2, 4, 2, false>(a, p, s);
     }
     // Few columns. The walk needs a tile for each of its workgroups, and K long enough
     // that the barrier of a tile does not show: 152064 x 3584 takes 96 us at 16 columns
@@ -864,6 +922,7 @@ qg_status qgemm_i8(const void* w, const float* ws, const void* xq, int64_t ldx, 
     a.mtiles = (int32_t)mt;
     a.part = (qi4*)workspace;
     a.kper = p.kper;
+    a.total = p.tiles;
     hipStream_t s = (hipStream_t)stream;
     if (y_type == QG_F32) return launch_gemm<QG_F32>(a, p, s);
     if (y_type == QG_F16) return launch_gemm<QG_F16>(a, p, s);
