@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "qg_device.h"
 #include "qg_host.h"
@@ -94,32 +95,35 @@ QG_DEV uint64_t key_of(float v, int token) {
 QG_DEV float key_value(uint64_t k) { return qg_unord((uint32_t)(k >> 32)); }
 QG_DEV int key_token(uint64_t k) { return (int)(0xffffffffu - (uint32_t)k); }
 
-// exp(v - m) for float32 v <= m, m finite, to about 3e-13 of the result: x = v - m is
-// exact in double, x = k ln 2 + r with |r| <= ln 2 / 2, the Taylor sum of exp(r) to
-// r^10 / 10! (the next term is below 2.3e-13), and k added to the exponent. k comes from
-// the low bits of a sum with 1.5 * 2^52: the conversions, roundings and ldexp of double
-// precision run at a fraction of the rate of its additions and fmas. x below -600 (v =
-// -inf among them) counts as -600, which keeps the result normal and far below what a
-// sum can show.
+// exp(v - m) for float32 v <= m, m finite, to 1e-12 of the result: x = v - m is exact in
+// double, x = k ln 2 + r with |r| <= ln 2 / 2, exp(r) by the polynomial of degree 8 that
+// is 1 at 0 and whose largest relative error over that range is least (8.2e-13; found by
+// iterated least squares), and k added to the exponent. k comes from the low bits of a
+// sum with 1.5 * 2^52, and x is bounded below through v, one operation each: the
+// stage is bound by its instructions. With the bound at m - 600 (not for a large m,
+// where float32 steps are wide: there x is bounded), v below it, -inf among them, counts
+// as exp(-600), which keeps the result normal and far below what a sum can show.
+template <bool WIDE>
 QG_DEV double exp_diff(float v, float m) {
-    const double x = __builtin_fmax((double)v - (double)m, -600.);
+    const double x = WIDE ? __builtin_fmax((double)v - (double)m, -600.) : (double)fmaxf(v, m - 600.f) - (double)m;
     const double big = 6755399441055744.;
     const double t = __builtin_fma(x, 1.4426950408889634074, big);
     const double r = __builtin_fma(t - big, -0.69314718055994530942, x);
-    double p = 1. / 3628800;
-    p = __builtin_fma(p, r, 1. / 362880);
-    p = __builtin_fma(p, r, 1. / 40320);
-    p = __builtin_fma(p, r, 1. / 5040);
-    p = __builtin_fma(p, r, 1. / 720);
-    p = __builtin_fma(p, r, 1. / 120);
-    p = __builtin_fma(p, r, 1. / 24);
-    p = __builtin_fma(p, r, 1. / 6);
-    p = __builtin_fma(p, r, 0.5);
+    double p = 2.473297530561428e-05;
+    p = __builtin_fma(p, r, 0.0001991468052941343);
+    p = __builtin_fma(p, r, 0.001388915504606253);
+    p = __builtin_fma(p, r, 0.00833326875520095);
+    p = __builtin_fma(p, r, 0.041666664536176984);
+    p = __builtin_fma(p, r, 0.16666666873332264);
+    p = __builtin_fma(p, r, 0.5000000000458368);
+    p = __builtin_fma(p, r, 0.9999999999830598);
     p = __builtin_fma(p, r, 1.);
-    p = __builtin_fma(p, r, 1.);
-    const uint32_t k = (uint32_t)__builtin_bit_cast(uint64_t, t);
-    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, p) + ((uint64_t)(k << 20) << 32));
+    const uint64_t b = __builtin_bit_cast(uint64_t, p);
+    const uint32_t hi = (uint32_t)(b >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, t) << 20);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)b);
 }
+// Whether m is too large for the narrow form.
+QG_DEV bool wide(float m) { return fabsf(m) > 1e6f; }
 
 QG_DEV float wave_max(float v) {
 #pragma unroll
@@ -219,11 +223,17 @@ __global__ __launch_bounds__(kWG) void beam_stats_kernel(BArgs a) {
     if (lane % L == 0) a.tmax[(int64_t)row * a.tiles + tile] = best;
     const float mx = wave_max(best);
     double s[2] = {0., 0.};
-    if (mx != neg_inf())
+    auto add = [&](auto w) {
 #pragma unroll
         for (int j = 0; j < SV; ++j)
 #pragma unroll
-            for (int e = 0; e < N; ++e) s[e & 1] += exp_diff(v[j][e], mx);
+            for (int e = 0; e < N; ++e) s[e & 1] += exp_diff<decltype(w)::value>(v[j][e], mx);
+    };
+    if (wide(mx)) {
+        if (mx != neg_inf()) add(std::true_type());
+    } else {
+        add(std::false_type());
+    }
     const double sum = wave_sum(s[0] + s[1]);
     if (lane == 0) {
         a.segmax[(int64_t)row * a.segs + seg] = mx;
@@ -272,6 +282,9 @@ QG_DEV V take(const V* p) {
 // Tile maxima of a thread: tiles of 32 (fp32) or 64 elements, up to one segment of them
 // more for a row that starts inside a vector.
 constexpr int kMine = (QG_TOPK_MAX_ROWS / 32 + 32 + kWG - 1) / kWG;
+// Segments of a thread, of at least 512 elements.
+constexpr int kSegs = (QG_TOPK_MAX_ROWS / 512 + 1 + kWG - 1) / kWG;
+static_assert(kMine <= 64, "a thread's tiles are marked in 64 bits");
 
 struct RowShared {
     uint64_t buf[kBuf];
@@ -298,7 +311,16 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
     float tv[kMine];  // this thread's tile maxima: tiles tid + kWG q
 #pragma unroll
     for (int q = 0; q < kMine; ++q) tv[q] = tid + kWG * q < a.tiles ? tm[tid + kWG * q] : neg_inf();
-    for (int i = tid; i < a.segs; i += kWG) mx = fmaxf(mx, sm[i]);
+    float segm[kSegs];
+    double segs[kSegs];
+#pragma unroll
+    for (int q = 0; q < kSegs; ++q) {
+        const int i = tid + kWG * q;
+        segm[q] = i < a.segs ? sm[i] : neg_inf();
+        segs[q] = i < a.segs ? ss[i] : 0.;
+    }
+#pragma unroll
+    for (int q = 0; q < kSegs; ++q) mx = fmaxf(mx, segm[q]);
 #pragma unroll
     for (int q = 0; q < kMine; ++q) best = fmaxf(best, tv[q]);
     mx = wave_max(mx);
@@ -312,8 +334,9 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
 #pragma unroll
     for (int w = 0; w < kWG / 64; ++w) mx = fmaxf(mx, sh.wmx[w]);
     double s = 0;
-    for (int i = tid; i < a.segs; i += kWG)
-        if (sm[i] != neg_inf()) s += ss[i] * exp_diff(sm[i], mx);
+    if (mx != neg_inf())
+#pragma unroll
+        for (int q = 0; q < kSegs; ++q) s += segs[q] * exp_diff<true>(segm[q], mx);
     s = wave_sum(s);
     if (lane == 0) sh.wsum[wave] = s;
     // The n-th largest of the 128 pairs' maxima: the largest value that n of them reach.
@@ -344,9 +367,10 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
 #pragma unroll
     for (int w = 0; w < kWG / 64; ++w) bound = fmaxf(bound, sh.wlow[w]);
     uint64_t T0 = (uint64_t)qg_ord(bound) << 32;
-    int mine_t = 0;
+    uint64_t marked = 0;
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) mine_t += tv[q] >= bound;
+    for (int q = 0; q < kMine; ++q) marked |= (uint64_t)(tv[q] >= bound) << q;
+    const int mine_t = __builtin_popcountll(marked);
     int at = mine_t ? atomicAdd(&sh.listed, mine_t) : 0;
     __syncthreads();
     const int reach = sh.listed;
@@ -357,12 +381,12 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
             if (tid == 0) sh.listed = 0;
             __syncthreads();
         }
-#pragma unroll
-        for (int q = 0; q < kMine; ++q)
-            if ((whole || q == turn) && tv[q] >= bound) {
-                if (!whole) at = atomicAdd(&sh.listed, 1);
-                sh.list[at++] = tid + kWG * q;
-            }
+        uint64_t now = whole ? marked : marked & (1ull << turn);
+        if (!whole && now) at = atomicAdd(&sh.listed, 1);
+        while (now) {
+            sh.list[at++] = tid + kWG * __builtin_ctzll(now);
+            now &= now - 1;
+        }
         __syncthreads();
         const int scanned = whole ? reach : sh.listed;
         for (int v0 = 0; v0 < scanned * 8; v0 += kWG) {
@@ -433,6 +457,9 @@ struct ItemShared {
     int len[QG_BEAM_MAX];
     bool done[QG_BEAM_MAX];
     int place[QG_BEAM_MAX_SELECT];
+    int list[QG_BEAM_MAX * QG_BEAM_MAX_SELECT];
+    double bound;
+    int kept;
 };
 struct Beam {  // of thread `beam`, read before the workgroup is counted
     float cum;
@@ -478,12 +505,45 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
         sh.rank[i] = a.alpha != 0. && token >= 0 ? sc / sh.over[i / a.n] : sc;
     }
     __syncthreads();
-    for (int i = tid; i < total; i += kWG) {
+    // With many candidates only those that reach a bound are compared: the n-th best of
+    // the beams' first few (2 n of them or a few more).
+    int c = total;
+    if (total > kWG) {
+        const int heads = min(a.n, (2 * a.n + a.beams - 1) / a.beams);
+        const int of = a.beams * heads;  // <= 2 n + beams <= 160
+        if (tid == 0) {
+            sh.bound = ninf;
+            sh.kept = 0;
+        }
+        __syncthreads();
+        if (tid < of) {
+            const double k = sh.rank[tid / heads * a.n + tid % heads];
+            int above = 0, reach = 0;
+            for (int o = 0; o < of; ++o) {
+                const double r = sh.rank[o / heads * a.n + o % heads];
+                above += r > k;
+                reach += r >= k;
+            }
+            if (above < a.n && reach >= a.n) sh.bound = k;  // (all threads that write it hold the same)
+        }
+        __syncthreads();
+        const double bound = sh.bound;
+        for (int i = tid; i < total; i += kWG)
+            if (sh.rank[i] >= bound && sh.rank[i] > ninf) sh.list[atomicAdd(&sh.kept, 1)] = i;
+        __syncthreads();
+        c = sh.kept;
+    }
+    for (int j = tid; j < c; j += kWG) {
+        const int i = total > kWG ? sh.list[j] : j;
         const double k = sh.rank[i];
         if (k == ninf) continue;
         int before = 0;
-        for (int o = 0; o < i; ++o) before += sh.rank[o] >= k;
-        for (int o = i + 1; o < total; ++o) before += sh.rank[o] > k;
+#pragma unroll 8
+        for (int l = 0; l < c; ++l) {
+            const int o = total > kWG ? sh.list[l] : l;
+            const double r = sh.rank[o];
+            before += (int)(r > k) | ((int)(r == k) & (int)(o < i));
+        }
         if (before < a.n) sh.place[before] = i;
     }
     __syncthreads();
