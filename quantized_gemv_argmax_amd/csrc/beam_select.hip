@@ -125,15 +125,38 @@ QG_DEV double exp_diff(float v, float m) {
 // Whether m is too large for the narrow form.
 QG_DEV bool wide(float m) { return fabsf(m) > 1e6f; }
 
+template <int CTRL>
+QG_DEV float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+QG_DEV double dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+QG_DEV double readlane(double v, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), l);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// Maximum and sum over the wavefront, the same in every lane: quads, 8-lane and
+// 16-lane mirrors, then the four rows in order.
 QG_DEV float wave_max(float v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
-    return v;
+    v = fmaxf(v, dpp<0xb1>(v));
+    v = fmaxf(v, dpp<0x4e>(v));
+    v = fmaxf(v, dpp<0x141>(v));
+    v = fmaxf(v, dpp<0x140>(v));
+    return fmaxf(fmaxf(qg_readlane(v, 0), qg_readlane(v, 16)), fmaxf(qg_readlane(v, 32), qg_readlane(v, 48)));
 }
 QG_DEV double wave_sum(double v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-    return v;
+    v += dpp<0xb1>(v);
+    v += dpp<0x4e>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    return ((readlane(v, 0) + readlane(v, 16)) + readlane(v, 32)) + readlane(v, 48);
 }
 
 // A row's 16-byte vectors. Rows start at any element: vectors are cut from the
@@ -171,10 +194,16 @@ struct Row {
 };
 
 // ---------------------------------------------------------------- stage 1
-// SV vectors per lane; 8 / SV lanes' make a tile.
+// A segment per wavefront, SV vectors of each lane; 8 / SV lanes' make a tile. Bound by
+// its double-precision instructions, about 14 of 25 per element and at half the rate of
+// float32's: 16 x 8 rows of 152064 bf16 (39 MB) take 20 us, with the exponentials
+// replaced by a subtraction 12. (Walking wavefronts with the next segment's loads ahead
+// of the work on one: 22 us. Splitting the polynomial between float32 and double, or a
+// table of powers, trades as many instructions as it saves.)
 template <int XT, int SV>
 __global__ __launch_bounds__(kWG) void beam_stats_kernel(BArgs a) {
     constexpr int N = Log<XT>::N;
+    constexpr int L = 8 / SV;  // lanes of a tile
     const int lane = threadIdx.x & 63;
     const uint32_t g = blockIdx.x * (kWG / 64) + (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (g < (uint32_t)(a.rows / a.beams) && lane == 0) a.arrived[g] = 0;  // (there are more wavefronts than items)
@@ -186,25 +215,19 @@ __global__ __launch_bounds__(kWG) void beam_stats_kernel(BArgs a) {
     const int first = seg * SV * 64;  // vector j of this lane: first + 64 j + lane
     uint4 u[SV];
     float v[SV][N];
-    const bool inside = first * N >= r.sh && r.whole(first + SV * 64 - 1);
-    if (inside) {
 #pragma unroll
-        for (int j = 0; j < SV; ++j) u[j] = r.get(first + 64 * j + lane);
+    for (int j = 0; j < SV; ++j) {
+        u[j] = make_uint4(0, 0, 0, 0);
+        if (r.whole(first + 64 * j + lane)) u[j] = r.get(first + 64 * j + lane);
+    }
 #pragma unroll
-        for (int j = 0; j < SV; ++j)
+    for (int j = 0; j < SV; ++j)
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[j][e] = clean(Log<XT>::get(u[j], e));
-    } else {
-#pragma unroll
-        for (int j = 0; j < SV; ++j) {
-            u[j] = make_uint4(0, 0, 0, 0);
-            if (r.whole(first + 64 * j + lane)) u[j] = r.get(first + 64 * j + lane);
-        }
+        for (int e = 0; e < N; ++e) v[j][e] = clean(Log<XT>::get(u[j], e));
+    if (first * N < r.sh || !r.whole(first + SV * 64 - 1)) {  // a row's first or last segment
 #pragma unroll
         for (int j = 0; j < SV; ++j) {
             const int i = first + 64 * j + lane;
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[j][e] = clean(Log<XT>::get(u[j], e));
             if (r.cut(i))
                 r.last(i, v[j]);
             else
@@ -216,28 +239,27 @@ __global__ __launch_bounds__(kWG) void beam_stats_kernel(BArgs a) {
     for (int j = 0; j < SV; ++j)
 #pragma unroll
         for (int e = 0; e < N; ++e) best = fmaxf(best, v[j][e]);
-    constexpr int L = 8 / SV;  // lanes of a tile
-#pragma unroll
-    for (int m = 1; m < L; m <<= 1) best = fmaxf(best, __shfl_xor(best, m));
-    const int tile = seg * (64 / L) + lane / L;
-    if (lane % L == 0) a.tmax[(int64_t)row * a.tiles + tile] = best;
+    static_assert(L == 4 || L == 2, "tiles are lanes of a quad");
+    best = fmaxf(best, dpp<0xb1>(best));
+    if (L == 4) best = fmaxf(best, dpp<0x4e>(best));
+    if (lane % L == 0) a.tmax[(int64_t)row * a.tiles + seg * (64 / L) + lane / L] = best;
     const float mx = wave_max(best);
-    double s[2] = {0., 0.};
+    double sum[2] = {0., 0.};
     auto add = [&](auto w) {
 #pragma unroll
         for (int j = 0; j < SV; ++j)
 #pragma unroll
-            for (int e = 0; e < N; ++e) s[e & 1] += exp_diff<decltype(w)::value>(v[j][e], mx);
+            for (int e = 0; e < N; ++e) sum[e & 1] += exp_diff<decltype(w)::value>(v[j][e], mx);
     };
     if (wide(mx)) {
         if (mx != neg_inf()) add(std::true_type());
     } else {
         add(std::false_type());
     }
-    const double sum = wave_sum(s[0] + s[1]);
+    const double all = wave_sum(sum[0] + sum[1]);
     if (lane == 0) {
         a.segmax[(int64_t)row * a.segs + seg] = mx;
-        a.segsum[(int64_t)row * a.segs + seg] = sum;
+        a.segsum[(int64_t)row * a.segs + seg] = all;
     }
 }
 
@@ -325,8 +347,10 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
     for (int q = 0; q < kMine; ++q) best = fmaxf(best, tv[q]);
     mx = wave_max(mx);
     if (lane == 0) sh.wmx[wave] = mx;
-    best = fmaxf(best, __shfl_xor(best, 1));
-    if (!(tid & 1)) sh.tops[tid >> 1] = best;
+    const bool quads = a.n <= 16;
+    best = fmaxf(best, dpp<0xb1>(best));
+    if (quads) best = fmaxf(best, dpp<0x4e>(best));
+    if (quads ? !(tid & 3) : !(tid & 1)) sh.tops[quads ? tid >> 2 : tid >> 1] = best;
     if (tid == 0) {
         sh.count = sh.listed = 0;
     }
@@ -339,16 +363,22 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
         for (int q = 0; q < kSegs; ++q) s += segs[q] * exp_diff<true>(segm[q], mx);
     s = wave_sum(s);
     if (lane == 0) sh.wsum[wave] = s;
-    // The n-th largest of the 128 pairs' maxima: the largest value that n of them reach.
-    // The two threads of a pair count one half of the pairs each.
-    const int half = (tid & 1) * (kWG / 4);
+    // The n-th largest of the 64 quads' (for up to 16) or 128 pairs' maxima: the largest
+    // value that n of them reach. The threads of a group count a share of them each.
     int reached = 0;
+    auto count = [&](const float* tops, auto of) {
 #pragma unroll
-    for (int i = 0; i < kWG / 4; i += 4) {
-        const float4 o = *reinterpret_cast<const float4*>(sh.tops + half + i);
-        reached += (o.x >= best) + (o.y >= best) + (o.z >= best) + (o.w >= best);
-    }
+        for (int i = 0; i < decltype(of)::value; i += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(tops + i);
+            reached += (o.x >= best) + (o.y >= best) + (o.z >= best) + (o.w >= best);
+        }
+    };
+    if (quads)
+        count(sh.tops + (tid & 3) * (kWG / 16), std::integral_constant<int, kWG / 16>());
+    else
+        count(sh.tops + (tid & 1) * (kWG / 4), std::integral_constant<int, kWG / 4>());
     reached += __shfl_xor(reached, 1);
+    if (quads) reached += __shfl_xor(reached, 2);
     const float low = wave_max(reached >= a.n ? best : neg_inf());
     if (lane == 0) sh.wlow[wave] = low;
     __syncthreads();
@@ -363,7 +393,7 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
     // else those of one round q at a time; each listed tile's eight vectors go to eight
     // threads. Keys from the bound's value on go to the buffer; when they would not fit,
     // it is cut back to its n best, which raises the bound.
-    float bound = -kMaxF;  // (every element that is not masked, where fewer than n pairs hold one)
+    float bound = -kMaxF;  // (every element that is not masked, where fewer than n groups hold one)
 #pragma unroll
     for (int w = 0; w < kWG / 64; ++w) bound = fmaxf(bound, sh.wlow[w]);
     uint64_t T0 = (uint64_t)qg_ord(bound) << 32;
@@ -465,6 +495,7 @@ struct Beam {  // of thread `beam`, read before the workgroup is counted
     float cum;
     int len;
     bool done;
+    double over;  // len^alpha
 };
 
 // An item's n best over its beams' n best. Order: rank descending, then i ascending.
@@ -480,7 +511,7 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
         sh.cum[tid] = beam.cum;
         sh.done[tid] = beam.done;
         sh.len[tid] = beam.len;
-        sh.over[tid] = a.alpha != 0. ? pow((double)max(beam.len, 1), a.alpha) : 1.;
+        sh.over[tid] = beam.over;
         sh.stat[tid] = st;
     }
     __syncthreads();
@@ -575,12 +606,13 @@ __global__ __launch_bounds__(kWG) void beam_rank_kernel(BArgs a) {
     const int64_t item = row / a.beams;
     // The item's inputs, which its outputs may replace: read by every one of its
     // workgroups before it is counted, while only the last one counted writes.
-    Beam beam{0.f, 0, false};
+    Beam beam{0.f, 0, false, 1.};
     if ((int)threadIdx.x < a.beams) {
         const int64_t b = item * a.beams + threadIdx.x;
         beam.done = a.finished && a.finished[b];
         beam.cum = a.score[b];
         beam.len = (a.length ? a.length[b] : 0) + (beam.done ? 0 : 1);
+        if (a.alpha != 0.) beam.over = pow((double)max(beam.len, 1), a.alpha);
     }
     if (!(a.finished && a.finished[row])) rank_row<XT, SV>(a, row, sh.row);
     // The row's results are out (each wavefront waits for its stores before the barrier)
