@@ -669,7 +669,7 @@ def _scratch(ws, need, device):
     if ws is not None:
         ws.ensure(need)
         return ws.ptr(), ws.nbytes(), ws.buf
-    buf = torch.empty(need, dtype=torch.uint8, device=device)
+    buf = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
     return buf.data_ptr(), need, buf
 
 
@@ -704,11 +704,11 @@ def quantize_i8_rows(x: torch.Tensor, out: torch.Tensor | None = None, scale: to
     N, K, ldx = _rows_of("x", x, _TYPES, gpu, None, 0)
     kp = (K + 63) // 64 * 64
     if out is None:
-        out, ldq = torch.empty((N, kp), dtype=torch.int8, device=x.device), kp
+        out, ldq = torch.empty_strided((N, kp), (kp, 1), dtype=torch.int8, device=x.device), kp
     else:
         ldq = _rows_of("out", out, _I8, gpu, N, kp)[2]
     if scale is None:
-        scale = torch.empty(N, dtype=torch.float32, device=x.device)
+        scale = torch.empty_strided((N,), (1,), dtype=torch.float32, device=x.device)
     else:
         _same("scale", scale, _F32, gpu, (N,))
     _launch("qg_quantize_i8_rows", gpu, x.data_ptr(), _TYPES[x.dtype], ldx, N, K, out.data_ptr(), ldq, scale.data_ptr())
@@ -739,7 +739,7 @@ def qgemm_i8(w: torch.Tensor, w_scale: torch.Tensor, xq: torch.Tensor, x_scale: 
         if dtype not in _TYPES:
             raise ValueError(f"no output of type {dtype}")
         ldy = (M + 3) // 4 * 4
-        Y = torch.empty((N, ldy), dtype=dtype, device=w.device)
+        Y = torch.empty_strided((N, ldy), (ldy, 1), dtype=dtype, device=w.device)
     else:
         ldy = _rows_of("Y", Y, _TYPES, gpu, N, M)[2]
         dtype = Y.dtype
@@ -756,11 +756,11 @@ class BeamSelection:
     score (float32), finished (bool) and, if lengths were given, length (int32)."""
 
     def __init__(self, batch: int, n: int, device, length: bool):
-        self.token = torch.empty((batch, n), dtype=torch.int32, device=device)
-        self.parent = torch.empty((batch, n), dtype=torch.int32, device=device)
-        self.score = torch.empty((batch, n), dtype=torch.float32, device=device)
-        self.finished = torch.empty((batch, n), dtype=torch.bool, device=device)
-        self.length = torch.empty((batch, n), dtype=torch.int32, device=device) if length else None
+        whole = torch.empty((3 if length else 2, batch, n), dtype=torch.int32, device=device).unbind()
+        self.token, self.parent = whole[:2]
+        self.length = whole[2] if length else None
+        self.score = torch.empty_strided((batch, n), (n, 1), dtype=torch.float32, device=device)
+        self.finished = torch.empty_strided((batch, n), (n, 1), dtype=torch.bool, device=device)
 
 
 def logits_beam_select(logits: torch.Tensor, score: torch.Tensor, n: int, finished: torch.Tensor | None = None,

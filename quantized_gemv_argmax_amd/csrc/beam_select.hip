@@ -536,10 +536,29 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
         sh.rank[i] = a.alpha != 0. && token >= 0 ? sc / sh.over[i / a.n] : sc;
     }
     __syncthreads();
-    // With many candidates only those that reach a bound are compared: the n-th best of
-    // the beams' first few (2 n of them or a few more).
-    int c = total;
-    if (total > kWG) {
+    // Four threads compare a candidate with the others. With many candidates only those
+    // that reach a bound are compared: the n-th best of the beams' first few (2 n of them
+    // or a few more).
+    auto place = [&](int c, auto listed) {
+        for (int j0 = 0; j0 < c; j0 += kWG / 4) {
+            const int j = j0 + (tid >> 2);
+            const int i = j < c ? (listed ? sh.list[j] : j) : 0;
+            const double k = sh.rank[i];
+            int before = 0;
+#pragma unroll 4
+            for (int l = tid & 3; l < c; l += 4) {
+                const int o = listed ? sh.list[l] : l;
+                const double r = sh.rank[o];
+                before += (int)(r > k) | ((int)(r == k) & (int)(o < i));
+            }
+            before += __shfl_xor(before, 1);
+            before += __shfl_xor(before, 2);
+            if (j < c && k != ninf && before < a.n && !(tid & 3)) sh.place[before] = i;
+        }
+    };
+    if (total <= kWG) {
+        place(total, std::false_type());
+    } else {
         const int heads = min(a.n, (2 * a.n + a.beams - 1) / a.beams);
         const int of = a.beams * heads;  // <= 2 n + beams <= 160
         if (tid == 0) {
@@ -562,20 +581,7 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
         for (int i = tid; i < total; i += kWG)
             if (sh.rank[i] >= bound && sh.rank[i] > ninf) sh.list[atomicAdd(&sh.kept, 1)] = i;
         __syncthreads();
-        c = sh.kept;
-    }
-    for (int j = tid; j < c; j += kWG) {
-        const int i = total > kWG ? sh.list[j] : j;
-        const double k = sh.rank[i];
-        if (k == ninf) continue;
-        int before = 0;
-#pragma unroll 8
-        for (int l = 0; l < c; ++l) {
-            const int o = total > kWG ? sh.list[l] : l;
-            const double r = sh.rank[o];
-            before += (int)(r > k) | ((int)(r == k) & (int)(o < i));
-        }
-        if (before < a.n) sh.place[before] = i;
+        place(sh.kept, std::true_type());
     }
     __syncthreads();
     if (tid < a.n) {
