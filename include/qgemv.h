@@ -547,14 +547,12 @@ qg_status logits_beam_select(const qg_beam_in* in /* host */, int n, void* works
  * beams_out and equal strides): rows whose parent is themselves are not touched, and
  * every row is read before any is overwritten. Otherwise src and dst must not
  * overlap. A parent outside [0, beams_in) leaves its dst row as it was. States of one
- * call must not overlap each other's. A state's bytes are moved 16 at a time where its
- * pointers, strides and span allow it, else 4, else singly; states need no alignment.
+ * call must not overlap each other's; they need no alignment.
  * 1 <= count <= QG_BEAM_MAX_STATES, 1 <= beams_in, beams_out <= QG_BEAM_MAX, 1 <= batch
- * <= 65535; outer * span < 2^40, and fewer than 2^32 such units in a row of a state;
+ * <= 65535; outer * span < 2^40, and outer * ceil(span / 16) < 2^32 - 256;
  * strides in [0, 2^40], dst rows and pieces apart (the smaller stride at least
  * a span, the larger at least all that the smaller steps over) and apart from parent.
- * States alike in alignment and, to a factor of two, in length share a launch. No
- * workspace.
+ * States alike in length to a factor of two share a launch. No workspace.
  */
 #define QG_BEAM_MAX_STATES 56
 typedef struct {

@@ -13,14 +13,36 @@
 
 namespace {
 
-// 16 bytes as a vector type of the compiler's, which keeps arrays of it in registers
-typedef uint32_t u16B __attribute__((ext_vector_type(4)));
+// Units of any alignment: the hardware takes unaligned accesses of up to 16 bytes.
+template <int B>
+struct Unit;
+template <>
+struct Unit<16> {
+    typedef uint32_t T __attribute__((ext_vector_type(4), aligned(1)));
+};
+template <>
+struct Unit<8> {
+    typedef uint32_t T __attribute__((ext_vector_type(2), aligned(1)));
+};
+template <>
+struct Unit<4> {
+    typedef uint32_t T __attribute__((aligned(1)));
+};
+template <>
+struct Unit<2> {
+    typedef uint16_t T __attribute__((aligned(1)));
+};
+template <>
+struct Unit<1> {
+    typedef uint8_t T;
+};
 
 struct RState {
     const uint8_t* src;
     uint8_t* dst;
     int64_t src_row, dst_row, src_outer, dst_outer;
-    uint32_t per, cols;  // units of a piece and of a row
+    uint32_t per, cols;  // 16-byte columns of a piece and of a row
+    uint32_t tail;       // bytes of a piece's last column, 16 or fewer
 };
 struct RArgs {
     RState st[QG_BEAM_MAX_STATES];
@@ -28,21 +50,22 @@ struct RArgs {
     int32_t beams_in, beams_out;
 };
 
-// Rows J .. W - 1 of one column: all of them are read before the first is written (the
-// reads of the later rows lie inside the call between a row's read and its write). As
-// a recursion over single values: an array of them became one wide register that every
-// branch copied (226 registers at eight beams, here 40).
-template <typename U, int W, int J>
+// Rows J .. W - 1 of B bytes of a column: all of them are read before the first is
+// written (the reads of the later rows lie inside the call between a row's read and its
+// write). As a recursion over single values: an array of them became one wide register
+// that every branch copied (226 registers at eight beams, here 40).
+template <int B, int W, int J>
 QG_DEV void move_rows(const uint8_t* src, uint8_t* dst, const RState& s, const int (&p)[W]) {
+    typedef typename Unit<B>::T U;
     if constexpr (J < W) {
         U v{};
         if (p[J] >= 0) v = *reinterpret_cast<const U*>(src + p[J] * s.src_row);
-        move_rows<U, W, J + 1>(src, dst, s, p);
+        move_rows<B, W, J + 1>(src, dst, s, p);
         if (p[J] >= 0) *reinterpret_cast<U*>(dst + J * s.dst_row) = v;
     }
 }
 
-template <typename U, int W>
+template <int W>
 __global__ __launch_bounds__(256) void beam_reorder_kernel(RArgs a) {
     const RState& s = a.st[blockIdx.z];
     const uint32_t c = blockIdx.x * 256u + threadIdx.x;
@@ -57,28 +80,30 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(RArgs a) {
     }
     if (c >= s.cols) return;
     const uint32_t o = c / s.per, i = c - o * s.per;
-    move_rows<U, W, 0>(s.src + b * a.beams_in * s.src_row + o * s.src_outer + (int64_t)i * sizeof(U),
-                       s.dst + b * a.beams_out * s.dst_row + o * s.dst_outer + (int64_t)i * sizeof(U), s, p);
+    const uint8_t* src = s.src + b * a.beams_in * s.src_row + o * s.src_outer + (int64_t)i * 16;
+    uint8_t* dst = s.dst + b * a.beams_out * s.dst_row + o * s.dst_outer + (int64_t)i * 16;
+    const uint32_t bytes = i + 1 == s.per ? s.tail : 16;
+    if (bytes == 16) {
+        move_rows<16, W, 0>(src, dst, s, p);
+        return;
+    }
+    uint32_t at = 0;
+    if (bytes & 8) move_rows<8, W, 0>(src, dst, s, p), at = 8;
+    if (bytes & 4) move_rows<4, W, 0>(src + at, dst + at, s, p), at += 4;
+    if (bytes & 2) move_rows<2, W, 0>(src + at, dst + at, s, p), at += 2;
+    if (bytes & 1) move_rows<1, W, 0>(src + at, dst + at, s, p);
 }
 
-// The largest unit of 16, 4 or 1 bytes that a state's pointers, strides and span allow.
-int unit_of(const qg_beam_state& s) {
-    uintptr_t bits = reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst) | (uintptr_t)s.src_row |
-                     (uintptr_t)s.dst_row | (uintptr_t)s.span;
-    if (s.outer > 1) bits |= (uintptr_t)s.src_outer | (uintptr_t)s.dst_outer;
-    return (bits & 15) == 0 ? 16 : (bits & 3) == 0 ? 4 : 1;
-}
-int64_t cols_of(const qg_beam_state& s) { return s.outer * (s.span / unit_of(s)); }
+int64_t cols_of(const qg_beam_state& s) { return s.outer * qg::ceil_div(s.span, 16); }
 
-template <typename U>
 qg_status launch(const RArgs& a, int n, uint32_t cols, int64_t batch, hipStream_t stream) {
     const dim3 g((cols + 255) / 256, (unsigned)batch, (unsigned)n);
     if (a.beams_out <= 4)
-        hipLaunchKernelGGL((beam_reorder_kernel<U, 4>), g, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((beam_reorder_kernel<4>), g, dim3(256), 0, stream, a);
     else if (a.beams_out <= 8)
-        hipLaunchKernelGGL((beam_reorder_kernel<U, 8>), g, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((beam_reorder_kernel<8>), g, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((beam_reorder_kernel<U, QG_BEAM_MAX>), g, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((beam_reorder_kernel<QG_BEAM_MAX>), g, dim3(256), 0, stream, a);
     return qg::launch_status("qg_beam_reorder");
 }
 
@@ -126,35 +151,31 @@ extern "C" qg_status qg_beam_reorder(const qg_beam_state* states, int count, con
             if (s0 < d0 + dn && d0 < s0 + sn) return qg::fail(QG_ERR_SHAPE, "state %d: src and dst overlap", k);
         }
         if (cols_of(s) > 0xffffff00ll)  // a launch has fewer than 2^32 threads along x
-            return qg::fail(QG_ERR_SHAPE, "state %d: a row holds over 2^32 units of its alignment", k);
+            return qg::fail(QG_ERR_SHAPE, "state %d: a row holds over 2^32 columns of 16 bytes", k);
     }
     qg_status st = qg::check_device();
     if (st) return st;
-    // One launch for the states of one unit whose rows are alike in length to a factor
-    // of two (a model's layers: one launch): a workgroup finds its state by its index.
+    // One launch for the states whose rows are alike in length to a factor of two (a
+    // model's layers: one launch): a workgroup finds its state by its index.
     uint64_t left = ((uint64_t)1 << count) - 1;
     while (left) {
-        const int k0 = __builtin_ctzll(left), unit = unit_of(states[k0]);
-        const int64_t c0 = cols_of(states[k0]);
+        const int64_t c0 = cols_of(states[__builtin_ctzll(left)]);
         RArgs a{};
         a.parent = parent;
         a.beams_in = beams_in;
         a.beams_out = beams_out;
         int n = 0;
         int64_t longest = 0;
-        for (int k = k0; k < count; ++k) {
+        for (int k = __builtin_ctzll(left); k < count; ++k) {
             const qg_beam_state& s = states[k];
             const int64_t c = cols_of(s);
-            if (!(left >> k & 1) || unit_of(s) != unit || c > 2 * c0 || c0 > 2 * c) continue;
+            if (!(left >> k & 1) || c > 2 * c0 || c0 > 2 * c) continue;
             left &= ~((uint64_t)1 << k);
             a.st[n++] = {(const uint8_t*)s.src, (uint8_t*)s.dst, s.src_row, s.dst_row, s.src_outer, s.dst_outer,
-                         (uint32_t)(s.span / unit), (uint32_t)c};
+                         (uint32_t)qg::ceil_div(s.span, 16), (uint32_t)c, (uint32_t)((s.span - 1) % 16 + 1)};
             longest = std::max(longest, c);
         }
-        hipStream_t h = (hipStream_t)stream;
-        st = unit == 16  ? launch<u16B>(a, n, (uint32_t)longest, batch, h)
-             : unit == 4 ? launch<uint32_t>(a, n, (uint32_t)longest, batch, h)
-                         : launch<uint8_t>(a, n, (uint32_t)longest, batch, h);
+        st = launch(a, n, (uint32_t)longest, batch, (hipStream_t)stream);
         if (st) return st;
     }
     return st;

@@ -357,3 +357,18 @@ def test_select_many_rows(B, W, V, n, kind):
     # enough rows for the longer segments
     for i, t in enumerate(TYPES):
         run_select(B, W, V, n, kind, t, seed=B + V + i, finished=i == 1, alpha=[0.0, 1.0, 0.0][i], ld=V + 3 * i)
+
+
+@pytest.mark.parametrize("span", [1, 2, 3, 5, 8, 14, 15, 16, 17, 31, 33, 66, 271])
+def test_reorder_any_span_and_alignment(span):
+    # pieces of every length at odd addresses, in place: what surrounds them stays
+    rng = np.random.default_rng(span)
+    B, W, outer = 2, 6, 3
+    base = to_dev(rng.integers(0, 256, (B * W, outer, span + 5)).astype(np.uint8))
+    want = base.cpu().numpy().copy()
+    parent = rng.integers(-1, W + 1, (B, W)).astype(np.int32)
+    case(f"beam_reorder span={span}")
+    qg.beam_reorder([base[:, :, 3:3 + span]], to_dev(parent))
+    want[:, :, 3:3 + span] = beamref.reorder(want[:, :, 3:3 + span], parent, W, want[:, :, 3:3 + span])
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(base.cpu().numpy(), want)

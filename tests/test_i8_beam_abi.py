@@ -195,4 +195,4 @@ def test_reorder_validation(L):
                dict(dst=A, dst_row=2048), dict(dst=A + 64), dict(dst=A - 64), dict(dst=C - 64)]:
         assert call(state(**kw)) == ESHAPE, kw
     assert call(state(dst=A), bi=3, bo=2) == ESHAPE
-    assert call(state(src=A + 1, span=1 << 34, src_row=1 << 34, dst_row=1 << 34, dst=1 << 45)) == ESHAPE  # too many single bytes
+    assert call(state(span=1 << 36, src_row=1 << 36, dst_row=1 << 36, dst=1 << 45)) == ESHAPE  # 2^32 columns of 16 bytes
