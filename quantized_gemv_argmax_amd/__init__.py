@@ -195,18 +195,34 @@ def _need_cuda(*ts):
 # ------------------------------------------------------------------ workspace
 class Workspace:
     """A device scratch buffer reused across calls on one stream (grown on demand).
-    It starts all-zero, as the library requires, and every call leaves it so."""
+    It starts all-zero, as most entry points require, and their calls leave it so. The
+    calls that leave it undefined instead (qgemm_i8, logits_beam_select) need one of
+    their own: a workspace serves the one kind or the other, whichever came first.
+    Outgrown buffers are kept, as a captured graph may still hold them."""
 
     def __init__(self, device=None, nbytes: int = 0):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf = None
+        self.outgrown = []
+        self.zeros = None  # whether its users need zeros (None: unused)
         if nbytes:
             self.ensure(nbytes)
 
     def ensure(self, nbytes: int):
         if nbytes and (self.buf is None or self.buf.numel() < nbytes):
+            if self.buf is not None:
+                self.outgrown.append(self.buf)
             self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=self.device)
         return self
+
+    def serve(self, nbytes: int, zeros: bool):
+        """ensure(nbytes) for a call that needs zeros (and leaves them) or one that does not."""
+        if self.zeros is not zeros:
+            if self.zeros is not None:
+                raise ValueError("a workspace of qgemm_i8 or logits_beam_select, which leave it undefined, cannot serve "
+                                 "a call that needs zeros, nor the other way round: give each kind its own")
+            self.zeros = zeros
+        return self.ensure(nbytes)
 
     def ptr(self) -> int | None:
         return None if self.buf is None else self.buf.data_ptr()
@@ -228,8 +244,7 @@ def default_workspace(device=None) -> Workspace:
 
 def _ws(ws: Workspace | None, need: int, device) -> Workspace:
     ws = ws if ws is not None else default_workspace(device)
-    ws.ensure(need)
-    return ws
+    return ws.serve(need, True)
 
 
 # ------------------------------------------------------------------ sizes / packing
@@ -487,7 +502,7 @@ def qgemm_q4k_smalln_batch_ws(problems, ws: Workspace | None = None):
     if ws is None:  # scratch contents: never the zero-kept workspace of the LM-head calls
         key = ("scratch", str(dev))
         ws = _default_ws.setdefault(key, Workspace(dev))
-    ws.ensure(need)
+    ws.serve(need, True)
     _check("qgemm_q4k_smalln_batch_ws",
            lib().qgemm_q4k_smalln_batch_ws(arr, len(problems), ws.ptr(), ws.nbytes(), _stream(dev)))
     return [p[2] for p in problems]
@@ -667,7 +682,7 @@ def _scratch(ws, need, device):
     """(address, bytes, owner) of a call's workspace: the caller's, grown if need be, or one
     of the call's own, so that calls on several streams and captured graphs never share."""
     if ws is not None:
-        ws.ensure(need)
+        ws.serve(need, False)
         return ws.ptr(), ws.nbytes(), ws.buf
     buf = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
     return buf.data_ptr(), need, buf

@@ -24,13 +24,6 @@ constexpr int kTileB = T * kKB;   // bytes of one operand (16 rows x 64 k)
 constexpr int kWalkBlocks = 64;   // k blocks of the walk form (K <= 4096)
 constexpr int kWalkGroups = 512;  // its workgroups
 
-QG_DEV uint16_t f32_to_bf16(float v) {
-    // round to nearest even; a NaN stays one
-    const uint32_t b = __builtin_bit_cast(uint32_t, v);
-    if (v != v) return (uint16_t)((b >> 16) | 0x40u);
-    return (uint16_t)((b + 0x7fffu + ((b >> 16) & 1u)) >> 16);
-}
-
 // ---------------------------------------------------------------- weight layout
 __global__ __launch_bounds__(256) void pack_i8_kernel(const int8_t* __restrict__ src, int64_t ldw,
                                                       uint4* __restrict__ dst, int64_t M, int K, int nb,
@@ -47,9 +40,11 @@ __global__ __launch_bounds__(256) void pack_i8_kernel(const int8_t* __restrict__
         } o;
         o.v = make_uint4(0, 0, 0, 0);
         if (row < M) {
+            typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(1)));  // rows start anywhere
             const int8_t* p = src + row * ldw + k0;
-            if (k0 + 16 <= K && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-                o.v = *reinterpret_cast<const uint4*>(p);
+            if (k0 + 16 <= K) {
+                const vec v = *reinterpret_cast<const vec*>(p);
+                o.v = make_uint4(v.x, v.y, v.z, v.w);
             } else {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
@@ -231,11 +226,15 @@ QG_DEV float scaled(int acc, float xs, float ws, float b) { return (float)acc * 
 
 template <int YT>
 QG_DEV uint32_t pack2(float lo, float hi) {
+    // (round to nearest even, a NaN stays one)
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const f2 v = {lo, hi};
     if constexpr (YT == QG_F16)
-        return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) |
-               (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, h2));
     else
-        return (uint32_t)f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
 }
 
 // C (4 or 8) consecutive outputs from element `at` of Y on, `count` of them inside

@@ -372,3 +372,57 @@ def test_reorder_any_span_and_alignment(span):
     want[:, :, 3:3 + span] = beamref.reorder(want[:, :, 3:3 + span], parent, W, want[:, :, 3:3 + span])
     torch.cuda.synchronize()
     np.testing.assert_array_equal(base.cpu().numpy(), want)
+
+
+def test_workspaces():
+    # one workspace serves the selection and split products in turn, keeps what a captured
+    # graph holds when it grows, and is refused by calls that need zeros (and theirs here)
+    ws = qg.Workspace(DEV)
+    z = to_dev(np.random.default_rng(16).standard_normal((8, 30000)).astype(np.float32))
+    score = torch.zeros(2, 4, device=DEV)
+    case("workspaces")
+    sel = qg.logits_beam_select(z, score, 8)
+    M, K, N = 256, 18944, 40
+    w = torch.randint(-127, 128, (M, K), dtype=torch.int8, device=DEV)
+    x = torch.randint(-127, 128, (N, K), dtype=torch.int8, device=DEV)
+    wp, one_m, one_n = qg.pack_i8(w), torch.ones(M, device=DEV), torch.ones(N, device=DEV)
+    assert qg.qgemm_i8_workspace_bytes(M, K, N) > 0
+    y = qg.qgemm_i8(wp, one_m, x, one_n, M, K)
+    out = qg.BeamSelection(2, 8, DEV, False)
+    qg.logits_beam_select(z, score, 8, out=out, ws=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qg.logits_beam_select(z, score, 8, out=out, ws=ws)
+    for _ in range(3):
+        assert torch.equal(qg.qgemm_i8(wp, one_m, x, one_n, M, K, ws=ws), y)
+        ws.ensure(2 * ws.nbytes())  # outgrown while a graph holds the old buffer
+        out.token.fill_(-5)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.token, sel.token) and torch.equal(out.parent, sel.parent)
+        assert torch.equal(out.score, sel.score)
+    with pytest.raises(ValueError):
+        qg.logits_topk(z[0].contiguous(), 20, ws=ws)
+    zeros = qg.Workspace(DEV)
+    qg.logits_topk(z[0].contiguous(), 20, ws=zeros)
+    with pytest.raises(ValueError):
+        qg.logits_beam_select(z, score, 8, ws=zeros)
+    with pytest.raises(ValueError):
+        qg.qgemm_i8(wp, one_m, x, one_n, M, K, ws=zeros)
+
+
+def test_calls_from_several_threads():
+    import threading
+    z = to_dev(np.random.default_rng(17).standard_normal((4, 999)).astype(np.float32))
+    want = qg.logits_beam_select(z, torch.zeros(1, 4, device=DEV), 4)
+    got = []
+
+    def work():
+        got.append(qg.logits_beam_select(z, torch.zeros(1, 4, device=DEV), 4))
+        torch.cuda.synchronize()
+
+    case("logits_beam_select from two threads")
+    ts = [threading.Thread(target=work) for _ in range(2)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert len(got) == 2 and all(torch.equal(r.token, want.token) for r in got)
