@@ -5,7 +5,9 @@
 // moved row written once. One thread owns one 16-byte column of all the rows of an
 // item: it reads that column of every row that moves, then writes them. No other
 // thread touches the column, so the same kernel moves in place, without a second
-// buffer and whatever cycles or repetitions the parents hold.
+// buffer and whatever cycles or repetitions the parents hold. Measured: 16 tensors of
+// 32 rows of 2 MB in 300 us (1.8 GB, 6.0 TB/s); 56 tensors of 4 rows of 38 KB in place in
+// 4.4 us, three memory round trips (arguments, parents, rows).
 #include <algorithm>
 
 #include "qg_device.h"
@@ -98,6 +100,9 @@ int64_t cols_of(const qg_beam_state& s) { return s.outer * qg::ceil_div(s.span, 
 
 qg_status launch(const RArgs& a, int n, uint32_t cols, int64_t batch, hipStream_t stream) {
     const dim3 g((cols + 255) / 256, (unsigned)batch, (unsigned)n);
+    // (no instance for 16: with 9 to 16 beams the one for 32, at three wavefronts per SIMD
+    // instead of six, moves 400 MB of 12 beams in 120 us instead of 131; with four beams it
+    // takes 435 us where the first takes 300)
     if (a.beams_out <= 4)
         hipLaunchKernelGGL((beam_reorder_kernel<4>), g, dim3(256), 0, stream, a);
     else if (a.beams_out <= 8)

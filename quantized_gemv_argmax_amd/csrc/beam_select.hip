@@ -601,6 +601,9 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
     }
 }
 
+// Bound by latency: 9.7 us for 4 rows of 152064 fp32 and n = 8, of them about 1 us each for
+// reading the tile maxima, for the bound, for the listed tiles' elements and for the
+// candidates of the other rows, under 1 us for each ranking and for the arrival.
 template <int XT, int SV>
 __global__ __launch_bounds__(kWG) void beam_rank_kernel(BArgs a) {
     __shared__ union {
