@@ -302,15 +302,17 @@ QG_DEV void store_quad(const GArgs& a, const qi4& s, int m, int n) {
 
 // ---------------------------------------------------------------- few columns
 // One 16-row tile and NB blocks of 16 columns per workgroup; its KW wavefronts take
-// the k blocks in turn, and their integer sums meet in LDS. The weights go from
-// memory straight to the operand registers, in the packed order. For few tiles, where
-// it is bound by latency (4608 x 3584 by 4 columns: 5.2 us for 16.6 MB; 16 instead of 8
-// wavefronts: 6.3), and for long K, where the columns, read from L2 by every tile,
-// weigh as much as the weights.
+// pairs of k blocks in turn, and their integer sums meet in LDS. The weights go from
+// memory straight to the operand registers, in the packed order; a pair's two column
+// operands are the halves of 128 bytes of a row, one cache line (block by block over
+// the wavefronts: 30000 x 6000 by 16 columns 44.2 us, in pairs 38; 3584 x 18944 by 16
+// 19.1 and 17). For few tiles, where it is bound by latency (4608 x 3584 by 4 columns:
+// 5.7 us for 16.6 MB; 16 instead of 8 wavefronts: 6.4), and for long K, where the
+// columns, read from L2 by every tile, weigh as much as the weights.
 template <int YT, int NB, int KW>
 __global__ __launch_bounds__(64 * KW) void gemm_i8_stream_kernel(GArgs a) {
     __shared__ qi4 part[KW][NB][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = blockIdx.x;
     const uint8_t* w = a.w + ((size_t)t * a.nb) * kTileB + lane * 16;
     const int8_t* xr[NB];
@@ -320,15 +322,38 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_stream_kernel(GArgs a) {
     qi4 acc[NB];
 #pragma unroll
     for (int c = 0; c < NB; ++c) acc[c] = qi4{0, 0, 0, 0};
-#pragma unroll 2
-    for (int b = wave; b < a.nb; b += KW) {
-        const qi4 wv = *reinterpret_cast<const qi4*>(w + (size_t)b * kTileB);
+    qi4 wv[2][2], xv[2][2][NB];  // [pair in flight][block]
+    auto load = [&](int p, int b, int count) {
 #pragma unroll
-        for (int c = 0; c < NB; ++c) {
-            const qi4 xv = *reinterpret_cast<const qi4*>(xr[c] + b * kKB);
-            acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, xv, acc[c], 0, 0, 0);
-        }
+        for (int h = 0; h < 2; ++h)
+            if (h < count) {
+                wv[p][h] = __builtin_nontemporal_load(reinterpret_cast<const qi4*>(w + (size_t)(b + h) * kTileB));
+#pragma unroll
+                for (int c = 0; c < NB; ++c) xv[p][h][c] = *reinterpret_cast<const qi4*>(xr[c] + (b + h) * kKB);
+            }
+    };
+    auto mma = [&](int p, int count) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (h < count)
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+                    acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[p][h], xv[p][h][c], acc[c], 0, 0, 0);
+    };
+    const int pairs = a.nb / 2;
+    int b = wave;
+    for (; b + KW < pairs; b += 2 * KW) {
+        load(0, 2 * b, 2);
+        load(1, 2 * (b + KW), 2);
+        mma(0, 2);
+        mma(1, 2);
     }
+    // what is left: a pair, and for one wavefront the odd block
+    const bool odd = (a.nb & 1) && wave == KW - 1;
+    if (b < pairs) load(0, 2 * b, 2);
+    if (odd) load(1, a.nb - 1, 1);
+    if (b < pairs) mma(0, 2);
+    if (odd) mma(1, 1);
 #pragma unroll
     for (int c = 0; c < NB; ++c) part[wave][c][lane] = acc[c];
     __syncthreads();
@@ -671,8 +696,10 @@ __global__ __launch_bounds__(64) void gemm_i8_join_kernel(GArgs a, int tiles, in
 }
 
 // ---------------------------------------------------------------- launches
-// How a product runs: N <= 32 streams the weights past the columns; else a tile form,
-// perhaps split along K.
+// How a product runs: few columns stream the weights past them; else a tile form,
+// perhaps split along K. 17 to 32 columns take tiles of 64 for K beyond the walk's
+// (3584 x 18944 by 32: 18.8 us in 4 splits, streamed 26.6; 30000 x 6000 by 32: 42.6 and
+// 63.7) unless the tiles are few (2000 x 8000 by 20: 10.2 and 9.4).
 enum { FORM_STREAM, FORM_64, FORM_128_DEEP, FORM_128, FORM_256 };
 struct Plan {
     int form, tiles, splits, kper;
@@ -696,12 +723,12 @@ Plan plan(int64_t M, int64_t K, int64_t N) {
     const int kt = (int)qg::ceil_div(K, 2 * kKB);
     p.splits = 1;
     p.kper = kt;
-    if (N <= 32) {
+    auto tiles = [&](int b) { return qg::ceil_div(M, b) * qg::ceil_div(N, b); };
+    if (N <= 16 || (N <= 32 && (K <= kWalkBlocks * kKB || tiles(64) < 48))) {
         p.form = FORM_STREAM;
         p.tiles = (int)qg::ceil_div(M, T);
         return p;
     }
-    auto tiles = [&](int b) { return qg::ceil_div(M, b) * qg::ceil_div(N, b); };
     int side = 64;
     if (N > 64 && tiles(256) >= 192)
         side = 256;

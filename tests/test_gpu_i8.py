@@ -110,7 +110,8 @@ SHAPES = [(1, 1, 1), (16, 64, 16), (17, 65, 17), (5, 1000, 1), (100, 3, 33), (51
           (1000, 257, 15), (3584, 18944, 3), (640, 18944, 16), (333, 1001, 31), (4608, 512, 64), (2000, 640, 65),
           (257, 191, 129), (1031, 1024, 255), (700, 2048, 256), (519, 130, 513), (2050, 320, 1000), (384, 18944, 130),
           (520, 9000, 100), (2050, 191, 1537), (2050, 64, 1500), (3300, 200, 4001), (3300, 60, 3900), (3300, 1000, 3900),
-          (8200, 3584, 16), (8200, 4096, 31), (9000, 1024, 1), (8195, 1030, 20), (300, 60, 70), (300, 4000, 70), (2600, 500, 300)]
+          (8200, 3584, 16), (8200, 4096, 31), (9000, 1024, 1), (8195, 1030, 20), (300, 60, 70), (300, 4000, 70), (2600, 500, 300),
+          (3600, 4200, 17), (3600, 18944, 32), (3600, 4161, 20), (100, 4161, 20), (6000, 5003, 16), (33, 129, 7), (33, 127, 2)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
