@@ -550,7 +550,7 @@ qg_status logits_beam_select(const qg_beam_in* in /* host */, int n, void* works
  * call must not overlap each other's; they need no alignment.
  * 1 <= count <= QG_BEAM_MAX_STATES, 1 <= beams_in, beams_out <= QG_BEAM_MAX, 1 <= batch
  * <= 65535; outer * span < 2^40, and outer * ceil(span / 16) < 2^32 - 256;
- * strides in [0, 2^40], dst rows and pieces apart (the smaller stride at least
+ * strides in [0, 2^40], (outer - 1) times them at most 2^60, dst rows and pieces apart (the smaller stride at least
  * a span, the larger at least all that the smaller steps over) and apart from parent.
  * States alike in length to a factor of two share a launch. No workspace.
  */

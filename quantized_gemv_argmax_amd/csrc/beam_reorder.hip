@@ -134,6 +134,11 @@ extern "C" qg_status qg_beam_reorder(const qg_beam_state* states, int count, con
         if (s.src_row < 0 || s.dst_row < 0 || s.src_outer < 0 || s.dst_outer < 0 || s.src_row > most ||
             s.dst_row > most || s.src_outer > most || s.dst_outer > most)
             return qg::fail(QG_ERR_SHAPE, "state %d: a stride is not in [0, 2^40]", k);
+        if (s.outer > 1 && std::max(s.src_outer, s.dst_outer) > ((int64_t)1 << 60) / (s.outer - 1))
+            return qg::fail(QG_ERR_SHAPE, "state %d: a row spans over 2^60 bytes", k);
+        for (int j = 0; j < k; ++j)
+            if (s.dst == states[j].dst || s.dst == states[j].src || s.src == states[j].dst)
+                return qg::fail(QG_ERR_SHAPE, "states %d and %d share a result", j, k);
         const int64_t rin = batch * beams_in, rout = batch * beams_out;
         // dst's rows and pieces are apart if the smaller stride clears a span and the
         // larger one everything that the smaller one steps over

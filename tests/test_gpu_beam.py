@@ -286,6 +286,8 @@ def test_reorder_refusals():
             qg.beam_reorder(bad[0], bad[1], out=bad[2])
     with pytest.raises(qg.QGError):  # rows of the result on top of each other
         qg.beam_reorder([s], p, out=[torch.zeros(1, 8, device=DEV).expand(6, 8)])
+    with pytest.raises(qg.QGError):  # one state twice
+        qg.beam_reorder([s, s], p)
     both = torch.zeros(9, 8, device=DEV)
     with pytest.raises(qg.QGError):
         qg.beam_reorder([both[:6]], p, out=[both[3:]])

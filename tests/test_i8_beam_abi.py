@@ -195,4 +195,11 @@ def test_reorder_validation(L):
                dict(dst=A, dst_row=2048), dict(dst=A + 64), dict(dst=A - 64), dict(dst=C - 64)]:
         assert call(state(**kw)) == ESHAPE, kw
     assert call(state(dst=A), bi=3, bo=2) == ESHAPE
+    assert call(state(outer=1 << 30, span=1, src_outer=1 << 40, dst_outer=1 << 40, src_row=1, dst_row=1)) == ESHAPE
+    # one result twice, a result that another state reads
+    assert call(state(), state(src=D)) == ESHAPE
+    assert call(state(), state(src=B, dst=D)) == ESHAPE
+    assert call(state(src=D, dst=E), state(dst=D)) == ESHAPE
+    if no_gpu():
+        assert call(state(), state(dst=D)) in (EDEV, EUNSUP)  # one source twice is fine
     assert call(state(span=1 << 36, src_row=1 << 36, dst_row=1 << 36, dst=1 << 45)) == ESHAPE  # 2^32 columns of 16 bytes
