@@ -434,7 +434,7 @@ qg_status lmhead_topk(const void* w_packed, const float* x, int64_t M, int64_t K
  * with int8 xq, wq and float32 scales. The sums are exact int32 (hence
  * K <= QG_I8_MAX_K); each is converted to float32, multiplied by the rounded
  * product of the two scales, the bias is added, all in float32, and the result is
- * rounded once more when Y is fp16 or bf16. Any number of columns N >= 1: decode
+ * rounded once more when Y is fp16 (beyond +-65504 infinite) or bf16. Any number of columns N >= 1: decode
  * and verification columns, beams, prefill tokens. Matrices that share their
  * activations (Q, K and V; gate and up) are one product over their rows stacked.
  *

@@ -367,10 +367,10 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_stream_kernel(GArgs a) {
 }
 
 // The same for many weight tiles and K <= 4096, bound by HBM (152064 x 3584 by 16 columns:
-// 555 MB in 95 us, 5.8 TB/s): each wavefront keeps its k blocks of
-// the columns in registers (up to XR of them) while its workgroup walks over tiles, so
-// that only weights are loaded, a tile ahead. Sums of alternate tiles meet in
-// alternate LDS buffers, one barrier a tile; the wavefronts take turns at adding them.
+// 555 MB in 95 us, 5.8 TB/s): each wavefront keeps its k blocks of the columns in
+// registers (up to XR of them) while its workgroup walks over tiles, so that only
+// weights are loaded, a tile ahead. Sums of alternate tiles meet in alternate LDS
+// buffers, one barrier a tile; the wavefronts take turns at adding them.
 template <int YT, int NB>
 __global__ __launch_bounds__(256) void gemm_i8_walk_kernel(GArgs a) {
     constexpr int KW = 4, XR = kWalkBlocks / KW;
