@@ -428,3 +428,30 @@ def test_calls_from_several_threads():
     [t.start() for t in ts]
     [t.join() for t in ts]
     assert len(got) == 2 and all(torch.equal(r.token, want.token) for r in got)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("V,n", [(97, 64), (255, 33), (1025, 64), (2244, 64), (4091, 17), (4096, 64), (4103, 64),
+                                 (8185, 64), (8192, 3), (8201, 64)])
+def test_select_short_rows(V, n, t):
+    """Rows around the lengths at which the bound is taken differently, with and without
+    room beside them."""
+    for i, kind in enumerate(["normal", "ties", "masked", "special"]):
+        run_select(2, 3, V, n, kind, t, seed=V + n + i, ld=V + 5 if i % 2 else None)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("V,live,n", [(900, 5, 16), (5000, 0, 64), (20000, 40, 64), (152064, 100, 64), (152064, 3, 8)])
+def test_select_masked_by_the_lowest_value(V, live, n, t):
+    """Masked entries at the type's lowest finite value are values like others: they rank
+    last, the lower token first."""
+    rng = np.random.default_rng(V + live)
+    z = torch.full((4, V), torch.finfo(TYPES[t]).min, dtype=TYPES[t])
+    for row in z:
+        at = torch.from_numpy(rng.choice(V, live, replace=False))
+        row[at] = torch.from_numpy(rng.standard_normal(live) * 3).to(TYPES[t])
+    score = (-rng.random((2, 2)) * 20).astype(np.float32)
+    case(f"logits_beam_select lowest V={V} live={live} n={n} {t}")
+    out = qg.logits_beam_select(z.to(DEV), to_dev(score), n)
+    ref = beamref.beam_select(z.double().numpy().reshape(2, 2, V), score, n)
+    check_selection(out, ref, f"lowest {V} {live} {n} {t}", length=False)
