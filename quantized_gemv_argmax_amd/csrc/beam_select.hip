@@ -534,6 +534,7 @@ struct ItemShared {
     bool done[QG_BEAM_MAX];
     int place[QG_BEAM_MAX_SELECT];
     int list[QG_BEAM_MAX * QG_BEAM_MAX_SELECT];
+    double head[2 * QG_BEAM_MAX_SELECT + QG_BEAM_MAX];
     double bound;
     int kept;
 };
@@ -612,14 +613,20 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
             sh.kept = 0;
         }
         __syncthreads();
-        if (tid < of) {
-            const double k = sh.rank[tid / heads * a.n + tid % heads];
+        if (tid < of) sh.head[tid] = sh.rank[tid / heads * a.n + tid % heads];
+        __syncthreads();
+        for (int j0 = 0; j0 < of; j0 += kWG / 4) {
+            const int j = min(j0 + (tid >> 2), of - 1);
+            const double k = sh.head[j];
             int above = 0, reach = 0;
-            for (int o = 0; o < of; ++o) {
-                const double r = sh.rank[o / heads * a.n + o % heads];
+#pragma unroll 4
+            for (int o = tid & 3; o < of; o += 4) {
+                const double r = sh.head[o];
                 above += r > k;
                 reach += r >= k;
             }
+            above += __shfl_xor(above, 1), reach += __shfl_xor(reach, 1);
+            above += __shfl_xor(above, 2), reach += __shfl_xor(reach, 2);
             if (above < a.n && reach >= a.n) sh.bound = k;  // (all threads that write it hold the same)
         }
         __syncthreads();
