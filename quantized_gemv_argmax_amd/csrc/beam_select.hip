@@ -585,7 +585,9 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
     __syncthreads();
     // Four threads compare a candidate with the others. With many candidates only those
     // that reach a bound are compared: the n-th best of the beams' first few (2 n of them
-    // or a few more).
+    // or a few more). A call of 16 beams with n = 16 takes 28 us if all are compared, 21
+    // with the bound; of 8 beams 17.6 and 16.3; up to 64 candidates, one each for every
+    // four threads, the bound costs 0.4 us (8 beams with n = 8: 15.1 and 15.5).
     auto place = [&](int c, auto listed) {
         for (int j0 = 0; j0 < c; j0 += kWG / 4) {
             const int j = j0 + (tid >> 2);
@@ -603,7 +605,7 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
             if (j < c && k != ninf && before < a.n && !(tid & 3)) sh.place[before] = i;
         }
     };
-    if (total <= kWG) {
+    if (total <= kWG / 4) {
         place(total, std::false_type());
     } else {
         const int heads = min(a.n, (2 * a.n + a.beams - 1) / a.beams);
