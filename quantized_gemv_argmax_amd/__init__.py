@@ -627,8 +627,6 @@ def lmhead_topk(w: torch.Tensor, x: torch.Tensor, M: int, K: int, k: int, logits
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
-
-
 def _launch(name, gpu, *args):
     """Calls the library's `name` on GPU `gpu`'s current stream with that GPU the current
     one (kernels launch there); raises on an error status."""
@@ -683,6 +681,8 @@ def _scratch(ws, need, device):
     of the call's own, so that calls on several streams and captured graphs never share."""
     if ws is not None:
         ws.serve(need, False)
+        if ws.buf is not None and ws.buf.device != device:
+            raise ValueError(f"the workspace is on {ws.buf.device}, the operands on {device}")
         return ws.ptr(), ws.nbytes(), ws.buf
     buf = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
     return buf.data_ptr(), need, buf
@@ -805,6 +805,8 @@ def logits_beam_select(logits: torch.Tensor, score: torch.Tensor, n: int, finish
             t = getattr(out, name)
             if t is not None:
                 _same("out." + name, t, types, gpu, (B, n))
+    if not -(1 << 31) <= eos < 1 << 31:
+        raise ValueError(f"eos={eos} is no token")
     xt = _TYPES[logits.dtype]
     wp, wb, keep = _scratch(ws, L.logits_beam_select_workspace_bytes(xt, B, W, V, n), logits.device)
     ci = _BeamIn(logits.data_ptr(), xt, ld, B, W, V, score.data_ptr(), _ptr(finished), _ptr(length), length_penalty, eos)

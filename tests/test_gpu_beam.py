@@ -455,3 +455,18 @@ def test_select_masked_by_the_lowest_value(V, live, n, t):
     out = qg.logits_beam_select(z.to(DEV), to_dev(score), n)
     ref = beamref.beam_select(z.double().numpy().reshape(2, 2, V), score, n)
     check_selection(out, ref, f"lowest {V} {live} {n} {t}", length=False)
+
+
+def test_workspace_of_another_device_and_wrapped_token():
+    z, s = torch.zeros(6, 100, device=DEV), torch.zeros(2, 3, device=DEV)
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        qg.logits_beam_select(z, s, 3, ws=qg.Workspace("cpu"))
+    M, K, N = 256, 8192, 64  # split along K
+    assert qg.qgemm_i8_workspace_bytes(M, K, N) > 0
+    w = qg.pack_i8(torch.zeros(M, K, dtype=torch.int8, device=DEV))
+    xq, xs = torch.zeros(N, K, dtype=torch.int8, device=DEV), torch.ones(N, device=DEV)
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        qg.qgemm_i8(w, torch.ones(M, device=DEV), xq, xs, M, K, ws=qg.Workspace("cpu"))
+    for eos in (2 ** 32 + 5, -(2 ** 32) - 1):  # not the token of its low 32 bits
+        with pytest.raises(ValueError, match="eos"):
+            qg.logits_beam_select(z, s, 3, eos=eos)
