@@ -434,9 +434,10 @@ qg_status lmhead_topk(const void* w_packed, const float* x, int64_t M, int64_t K
  * with int8 xq, wq and float32 scales. The sums are exact int32 (hence
  * K <= QG_I8_MAX_K); each is converted to float32, multiplied by the rounded
  * product of the two scales, the bias is added, all in float32, and the result is
- * rounded once more when Y is fp16 (beyond +-65504 infinite) or bf16. Any number of columns N >= 1: decode
- * and verification columns, beams, prefill tokens. Matrices that share their
- * activations (Q, K and V; gate and up) are one product over their rows stacked.
+ * rounded once more when Y is fp16 (beyond +-65504 infinite) or bf16. Any number
+ * of columns N >= 1: decode and verification columns, beams, prefill tokens.
+ * Matrices that share their activations (Q, K and V; gate and up) are one product
+ * over their rows stacked.
  *
  * qg_pack_i8 lays the weights out once, at load time: wq is row-major int8, M rows
  * of K at stride ldw >= K bytes. The packed buffer has qg_i8_bytes(M, K) bytes: rows
