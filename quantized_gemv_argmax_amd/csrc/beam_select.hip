@@ -42,13 +42,15 @@ template <int XT>
 struct Log;
 template <>
 struct Log<QG_F32> {
-    static constexpr int N = 4;
+    static constexpr int N = 4;  // elements of a 16-byte vector
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(4)));
     QG_DEV static float get(const uint4& v, int i) { return __builtin_bit_cast(float, (&v.x)[i]); }
     QG_DEV static float at(const void* p, int64_t i) { return reinterpret_cast<const float*>(p)[i]; }
 };
 template <>
 struct Log<QG_F16> {
     static constexpr int N = 8;
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
     QG_DEV static float get(const uint4& v, int i) {
         return (i & 1) ? qg_half_hi((&v.x)[i >> 1]) : qg_half_lo((&v.x)[i >> 1]);
     }
@@ -57,6 +59,7 @@ struct Log<QG_F16> {
 template <>
 struct Log<QG_BF16> {
     static constexpr int N = 8;
+    typedef uint32_t V __attribute__((ext_vector_type(4), aligned(2)));
     QG_DEV static float get(const uint4& v, int i) {
         const uint32_t w = (&v.x)[i >> 1];
         return __builtin_bit_cast(float, (i & 1) ? (w & 0xffff0000u) : (w << 16));
@@ -159,36 +162,35 @@ QG_DEV double wave_sum(double v) {
     return ((readlane(v, 0) + readlane(v, 16)) + readlane(v, 32)) + readlane(v, 48);
 }
 
-// A row's 16-byte vectors. Rows start at any element: vectors are cut from the
-// 16-byte boundary at or below the row's start, `sh` elements before it (the base is
-// aligned, so that boundary is never before the buffer). Vector i holds the elements
-// i N - sh + 0 .. N - 1; only the vector that holds the row's end is read element by
-// element.
+// A row's 16-byte vectors, cut from the row's own first element, whatever its address
+// (the hardware takes unaligned loads): which lane and segment an element falls to, and
+// so the order of every sum, depends on the vocabulary alone, and rows that are equal
+// wherever they lie, or equal but for a constant, get equal sums to the last bit. Vector
+// i holds the elements i N .. i N + N - 1; only the one that holds the row's end is read
+// element by element.
 template <int XT>
 struct Row {
     static constexpr int N = Log<XT>::N;
+    typedef typename Log<XT>::V vec;
     const uint8_t* base;
-    int sh, vocab;
-    QG_DEV Row(const void* logits, int64_t ld, int64_t row, int vocab_) : vocab(vocab_) {
-        constexpr int eb = 16 / N;
-        const uint8_t* p = (const uint8_t*)logits + row * ld * eb;
-        sh = (int)((reinterpret_cast<uintptr_t>(p) & 15) / eb);
-        base = p - sh * eb;
+    int vocab;
+    QG_DEV Row(const void* logits, int64_t ld, int64_t row, int vocab_)
+        : base((const uint8_t*)logits + row * ld * (16 / N)), vocab(vocab_) {}
+    QG_DEV bool whole(int i) const { return i * N + N <= vocab; }  // ends inside the row
+    QG_DEV bool cut(int i) const { return i * N < vocab && !whole(i); }
+    QG_DEV uint4 get(int i) const {
+        const vec v = *reinterpret_cast<const vec*>(base + (int64_t)i * 16);
+        return make_uint4(v.x, v.y, v.z, v.w);
     }
-    QG_DEV bool whole(int i) const { return i * N - sh + N <= vocab; }      // ends inside the row
-    QG_DEV bool cut(int i) const { return i * N - sh < vocab && !whole(i); }
-    QG_DEV uint4 get(int i) const { return *reinterpret_cast<const uint4*>(base + (int64_t)i * 16); }
-    // elements outside the row: -inf
+    // elements beyond the row: -inf
     QG_DEV void mask(int i, float (&v)[N]) const {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int at = i * N - sh + e;
-            if (at < 0 || at >= vocab) v[e] = neg_inf();
-        }
+        for (int e = 0; e < N; ++e)
+            if (i * N + e >= vocab) v[e] = neg_inf();
     }
     QG_DEV void last(int i, float (&v)[N]) const {
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = clean(Log<XT>::at(base, min(i * N + e, vocab - 1 + sh)));
+        for (int e = 0; e < N; ++e) v[e] = clean(Log<XT>::at(base, min(i * N + e, vocab - 1)));
         mask(i, v);
     }
     QG_DEV void load(int i, float (&v)[N]) const {
@@ -232,7 +234,7 @@ __global__ __launch_bounds__(kWG) void beam_stats_kernel(BArgs a) {
     for (int j = 0; j < SV; ++j)
 #pragma unroll
         for (int e = 0; e < N; ++e) v[j][e] = clean(Log<XT>::get(u[j], e));
-    if (first * N < r.sh || !r.whole(first + SV * 64 - 1)) {  // a row's first or last segment
+    if (!r.whole(first + SV * 64 - 1)) {  // a row's last segment
 #pragma unroll
         for (int j = 0; j < SV; ++j) {
             const int i = first + 64 * j + lane;
@@ -282,11 +284,11 @@ QG_DEV V take(const V* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Tile maxima of a thread: tiles of 32 (fp32) or 64 elements, up to one segment of them
-// more for a row that starts inside a vector.
-constexpr int kMine = (QG_TOPK_MAX_ROWS / 32 + 32 + kWG - 1) / kWG;
-// Segments of a thread, of at least 512 elements.
-constexpr int kSegs = (QG_TOPK_MAX_ROWS / 512 + 1 + kWG - 1) / kWG;
+// Tile maxima of a thread, tiles of 32 (fp32) or 64 elements, and its segments, of at
+// least 512 (both divide the longest row).
+constexpr int kMine = (QG_TOPK_MAX_ROWS / 32 + kWG - 1) / kWG;
+constexpr int kSegs = (QG_TOPK_MAX_ROWS / 512 + kWG - 1) / kWG;
+static_assert(QG_TOPK_MAX_ROWS % (4 * 64 * 8) == 0, "whole segments in the longest row");
 static_assert(kMine <= 64, "a thread's tiles are marked in 64 bits");
 
 // Rows of up to so many tiles, of eight vectors each, take their bound from the vectors:
@@ -486,7 +488,7 @@ QG_DEV void rank_row(const BArgs& a, int64_t row, RowShared& sh) {
             if (on) r.load(i, v);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                key[e] = on ? key_of(v[e], i * N - r.sh + e) : 0;
+                key[e] = on ? key_of(v[e], i * N + e) : 0;
                 mine += key[e] >= T0;
             }
             if (tid == 0) sh.more = 0;
@@ -703,7 +705,7 @@ Plan plan(int type, int64_t batch, int beams, int64_t vocab, int n) {
     Plan p;
     p.rows = batch * beams;
     const int64_t ve = vec_elems(type);
-    const int64_t vecs = qg::ceil_div(vocab + ve - 1, ve);  // a row may start inside a vector
+    const int64_t vecs = qg::ceil_div(vocab, ve);
     // Segments of four vectors a lane, or of two where four would leave most of the
     // chip without one.
     p.sv = p.rows * qg::ceil_div(vecs, 64 * 4) >= 2048 ? 4 : 2;

@@ -470,3 +470,34 @@ def test_workspace_of_another_device_and_wrapped_token():
     for eos in (2 ** 32 + 5, -(2 ** 32) - 1):  # not the token of its low 32 bits
         with pytest.raises(ValueError, match="eos"):
             qg.logits_beam_select(z, s, 3, eos=eos)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("V,gap", [(5003, 0), (50257, 0), (333, 0), (1001, 2), (4096, 1), (9001, 3), (152063, 0)])
+def test_equal_beams_tie_wherever_their_rows_start(V, gap, t):
+    """Rows that are equal, or equal but for a constant, at every alignment that an odd
+    vocabulary or stride gives them: with equal scores their candidates tie, and the
+    lower beam's come first. Values are halves below 16 shifted to at most 108, exact in
+    every type."""
+    B, W, n = 2, 8, 16
+    rng = np.random.default_rng(V + gap)
+    for shifts in (np.zeros(W), np.array([0, 32, -100, 0, 64, 32, -32, 96])):
+        base = rng.integers(-16, 16, (B, 1, V)) / 2
+        z = torch.from_numpy((base + shifts[None, :, None]).reshape(B * W, V))
+        wide = torch.full((B * W, V + gap), 50.0, dtype=TYPES[t], device=DEV)
+        wide[:, :V] = z.to(TYPES[t]).to(DEV)
+        zd = wide[:, :V]
+        assert torch.equal(zd.double().cpu(), z)
+        score = np.full((B, W), -1.25, np.float32)
+        case(f"logits_beam_select ties V={V} gap={gap} {t} shifted={bool(shifts.any())}")
+        out = qg.logits_beam_select(zd, to_dev(score), n)
+        ref = beamref.beam_select(z.numpy().reshape(B, W, V), score, n)
+        check_selection(out, ref, f"ties {V} {gap} {t}", length=False)
+    z = rng.standard_normal((B, 1, V)).astype(np.float32) * 3  # values of full precision, beams alike
+    z = torch.from_numpy(np.broadcast_to(z, (B, W, V)).reshape(B * W, V).copy()).to(TYPES[t])
+    wide = torch.full((B * W, V + gap), 50.0, dtype=TYPES[t], device=DEV)
+    wide[:, :V] = z.to(DEV)
+    case(f"logits_beam_select ties V={V} gap={gap} {t} alike")
+    out = qg.logits_beam_select(wide[:, :V], to_dev(score), n)
+    ref = beamref.beam_select(z.double().numpy().reshape(B, W, V), score, n)
+    check_selection(out, ref, f"alike {V} {gap} {t}", length=False)
