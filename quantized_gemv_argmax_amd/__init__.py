@@ -195,16 +195,19 @@ def _need_cuda(*ts):
 # ------------------------------------------------------------------ workspace
 class Workspace:
     """A device scratch buffer reused across calls on one stream (grown on demand).
-    It starts all-zero, as most entry points require, and their calls leave it so. The
-    calls that leave it undefined instead (qgemm_i8, logits_beam_select) need one of
-    their own: a workspace serves the one kind or the other, whichever came first.
-    Outgrown buffers are kept, as a captured graph may still hold them."""
+    It starts all-zero. Three kinds of calls use one: "zeros" (the LM-head and top-k
+    calls) needs it so and leaves it so; "counters" (qgemm_q4k_smalln_batch_ws) needs its
+    counters zero and leaves the rest undefined; "scratch" (qgemm_i8, logits_beam_select)
+    needs nothing and leaves all of it undefined. One workspace may serve the first two
+    in turn, cleared between them by the calls themselves, but not those and the third,
+    whichever came first. Outgrown buffers are kept, as a captured graph may still hold
+    them."""
 
     def __init__(self, device=None, nbytes: int = 0):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf = None
         self.outgrown = []
-        self.zeros = None  # whether its users need zeros (None: unused)
+        self.kinds = set()  # of the calls it has served
         if nbytes:
             self.ensure(nbytes)
 
@@ -215,14 +218,30 @@ class Workspace:
             self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=self.device)
         return self
 
-    def serve(self, nbytes: int, zeros: bool):
-        """ensure(nbytes) for a call that needs zeros (and leaves them) or one that does not."""
-        if self.zeros is not zeros:
-            if self.zeros is not None:
+    def serve(self, nbytes: int, kind: str):
+        """ensure(nbytes) for a call of `kind`, zeros where it needs them."""
+        if kind not in self.kinds:
+            if self.kinds and "scratch" in (kind, *self.kinds):
                 raise ValueError("a workspace of qgemm_i8 or logits_beam_select, which leave it undefined, cannot serve "
                                  "a call that needs zeros, nor the other way round: give each kind its own")
-            self.zeros = zeros
-        return self.ensure(nbytes)
+            self.kinds.add(kind)
+        self.ensure(nbytes)
+        # A captured "counters" call may have run since, so this is not done once. (A
+        # captured "zeros" call does not come here again: served() sees to that one.)
+        if kind == "zeros" and "counters" in self.kinds:
+            self.clear()
+        return self
+
+    def served(self, kind: str):
+        """After a call of `kind`: clears what it left, where other calls need zeros."""
+        if kind == "counters" and "zeros" in self.kinds:
+            self.clear()
+
+    def clear(self):
+        """Zeros on the current stream (a call that failed may have left something else)."""
+        if self.buf is not None:
+            self.buf.zero_()
+        return self
 
     def ptr(self) -> int | None:
         return None if self.buf is None else self.buf.data_ptr()
@@ -244,7 +263,7 @@ def default_workspace(device=None) -> Workspace:
 
 def _ws(ws: Workspace | None, need: int, device) -> Workspace:
     ws = ws if ws is not None else default_workspace(device)
-    return ws.serve(need, True)
+    return ws.serve(need, "zeros")
 
 
 # ------------------------------------------------------------------ sizes / packing
@@ -495,16 +514,20 @@ def qgemm_q4k_smalln_batch_ws(problems, ws: Workspace | None = None):
     qgemm_q4k_smalln_batch_workspace_bytes; a per-device scratch buffer if None),
     which lets the library split few-tile, many-column products over K slices. One
     workspace serves batches of any shapes; its counters come back zero and the rest
-    of it undefined. Calls sharing a workspace (the scratch one included) must not
-    overlap: calls on concurrent streams pass workspaces of their own."""
+    of it undefined (all of it zero if it also serves the LM-head or top-k calls). Calls
+    sharing a workspace (the scratch one included) must not overlap: calls on concurrent
+    streams pass workspaces of their own."""
     arr, dev = _gemm_problems(problems)
     need = lib().qgemm_q4k_smalln_batch_workspace_bytes(arr, len(problems))
     if ws is None:  # scratch contents: never the zero-kept workspace of the LM-head calls
         key = ("scratch", str(dev))
         ws = _default_ws.setdefault(key, Workspace(dev))
-    ws.serve(need, True)
+    if need:
+        ws.serve(need, "counters")
     _check("qgemm_q4k_smalln_batch_ws",
            lib().qgemm_q4k_smalln_batch_ws(arr, len(problems), ws.ptr(), ws.nbytes(), _stream(dev)))
+    if need:
+        ws.served("counters")
     return [p[2] for p in problems]
 
 
@@ -680,7 +703,7 @@ def _scratch(ws, need, device):
     """(address, bytes, owner) of a call's workspace: the caller's, grown if need be, or one
     of the call's own, so that calls on several streams and captured graphs never share."""
     if ws is not None:
-        ws.serve(need, False)
+        ws.serve(need, "scratch")
         if ws.buf is not None and ws.buf.device != device:
             raise ValueError(f"the workspace is on {ws.buf.device}, the operands on {device}")
         return ws.ptr(), ws.nbytes(), ws.buf
