@@ -258,6 +258,7 @@ def default_workspace(device=None) -> Workspace:
     key = (dev.type, dev.index if dev.index is not None else torch.cuda.current_device())
     if key not in _default_ws:
         _default_ws[key] = Workspace(dev)
+        _default_ws[key].kinds.add("zeros")  # handed to a "scratch" call first, it would refuse its own
     return _default_ws[key]
 
 

@@ -42,6 +42,13 @@ def test_undefined_contents_are_not_shared(other):
         ws.serve(64, a)  # goes on serving its own
 
 
+def test_default_workspace_is_kept_for_calls_that_need_zeros(monkeypatch):
+    monkeypatch.setattr(qg, "_default_ws", {})
+    with pytest.raises(ValueError, match="give each kind its own"):
+        qg.default_workspace("cpu:0").serve(64, "scratch")
+    qg._ws(None, 64, "cpu:0")  # what the LM-head calls take
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("first", ["product", "head", "topk"])
 def test_products_and_heads_share_a_workspace(first):
