@@ -554,6 +554,11 @@ qg_status logits_beam_select(const qg_beam_in* in /* host */, int n, void* works
  * strides in [0, 2^40], (outer - 1) times them at most 2^60, dst rows and pieces apart (the smaller stride at least
  * a span, the larger at least all that the smaller steps over) and apart from parent.
  * States alike in length to a factor of two share a launch. No workspace.
+ *
+ * qg_beam_reorder_check refuses what qg_beam_reorder would refuse of the same
+ * arguments, and launches nothing: a caller with more states than one call takes
+ * checks all of its calls before the first one moves anything (that no state of one
+ * call overlaps one of another is for the caller to see to).
  */
 #define QG_BEAM_MAX_STATES 56
 typedef struct {
@@ -565,6 +570,8 @@ typedef struct {
 } qg_beam_state;
 qg_status qg_beam_reorder(const qg_beam_state* states /* host */, int count, const int32_t* parent, int64_t batch,
                           int beams_in, int beams_out, qg_stream_t stream);
+qg_status qg_beam_reorder_check(const qg_beam_state* states /* host */, int count, const int32_t* parent, int64_t batch,
+                                int beams_in, int beams_out);
 
 /*
  * Launch override, for tests and measurements only (not needed for correct

@@ -138,6 +138,7 @@ _SIGS = {
     "logits_beam_select_workspace_bytes": (_SZ, [_I, _I64, _I, _I64, _I]),
     "logits_beam_select": (_I, [ctypes.POINTER(_BeamIn), _I, _P, _SZ, ctypes.POINTER(_BeamOut), _P]),
     "qg_beam_reorder": (_I, [_P, _I, _P, _I64, _I, _I, _P]),
+    "qg_beam_reorder_check": (_I, [_P, _I, _P, _I64, _I, _I]),
 }
 
 
@@ -885,7 +886,8 @@ def beam_reorder(states, parent: torch.Tensor, out=None):
     (batch, n); a parent outside [0, beams) leaves the result's row as it was). In place
     without `out` (then n == beams), else into the tensors of `out`. States may be
     views (a cache's filled part) and of several shapes and types; launched in groups of
-    BEAM_MAX_STATES. Returns the list of results."""
+    BEAM_MAX_STATES, after all of them are checked: a refused call moves nothing.
+    Returns the list of results."""
     states = list(states)
     results = states if out is None else list(out)
     if not states or len(results) != len(states):
@@ -917,6 +919,14 @@ def beam_reorder(states, parent: torch.Tensor, out=None):
             fields += moves
     words = array.array("q", fields)
     at, count = words.buffer_info()[0], len(words) // 8
-    for k in range(0, count, BEAM_MAX_STATES):
+    groups = range(0, count, BEAM_MAX_STATES)
+    if len(groups) > 1:  # (a group's own call checks it, too late for the groups before it)
+        src, dst = fields[0::8], fields[1::8]
+        if len(set(dst)) != count or not {s for s, d in zip(src, dst) if s != d}.isdisjoint(dst):
+            raise ValueError("two states share a result, or one is another's result")
+        for k in groups:
+            _check("qg_beam_reorder", lib().qg_beam_reorder_check(at + k * 64, min(BEAM_MAX_STATES, count - k),
+                                                                  parent.data_ptr(), B, W, n))
+    for k in groups:
         _launch("qg_beam_reorder", gpu, at + k * 64, min(BEAM_MAX_STATES, count - k), parent.data_ptr(), B, W, n)
     return results

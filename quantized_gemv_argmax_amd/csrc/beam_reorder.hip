@@ -112,11 +112,8 @@ qg_status launch(const RArgs& a, int n, uint32_t cols, int64_t batch, hipStream_
     return qg::launch_status("qg_beam_reorder");
 }
 
-}  // namespace
-
-extern "C" qg_status qg_beam_reorder(const qg_beam_state* states, int count, const int32_t* parent, int64_t batch,
-                                     int beams_in, int beams_out, qg_stream_t stream) {
-    qg::clear_error();
+qg_status check(const qg_beam_state* states, int count, const int32_t* parent, int64_t batch, int beams_in,
+                int beams_out) {
     if (!states || !parent) return qg::fail(QG_ERR_NULL, "NULL pointer (states, parent)");
     if (count < 1 || count > QG_BEAM_MAX_STATES)
         return qg::fail(QG_ERR_SHAPE, "count=%d not in [1, %d]", count, QG_BEAM_MAX_STATES);
@@ -163,7 +160,23 @@ extern "C" qg_status qg_beam_reorder(const qg_beam_state* states, int count, con
         if (cols_of(s) > 0xffffff00ll)  // a launch has fewer than 2^32 threads along x
             return qg::fail(QG_ERR_SHAPE, "state %d: a row holds over 2^32 columns of 16 bytes", k);
     }
-    qg_status st = qg::check_device();
+    return QG_OK;
+}
+
+}  // namespace
+
+extern "C" qg_status qg_beam_reorder_check(const qg_beam_state* states, int count, const int32_t* parent, int64_t batch,
+                                           int beams_in, int beams_out) {
+    qg::clear_error();
+    return check(states, count, parent, batch, beams_in, beams_out);
+}
+
+extern "C" qg_status qg_beam_reorder(const qg_beam_state* states, int count, const int32_t* parent, int64_t batch,
+                                     int beams_in, int beams_out, qg_stream_t stream) {
+    qg::clear_error();
+    qg_status st = check(states, count, parent, batch, beams_in, beams_out);
+    if (st) return st;
+    st = qg::check_device();
     if (st) return st;
     // One launch for the states whose rows are alike in length to a factor of two (a
     // model's layers: one launch): a workgroup finds its state by its index.

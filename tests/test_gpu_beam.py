@@ -501,3 +501,46 @@ def test_equal_beams_tie_wherever_their_rows_start(V, gap, t):
     out = qg.logits_beam_select(wide[:, :V], to_dev(score), n)
     ref = beamref.beam_select(z.double().numpy().reshape(B, W, V), score, n)
     check_selection(out, ref, f"alike {V} {gap} {t}", length=False)
+
+
+@pytest.mark.parametrize("at,count", [(56, 57), (63, 64), (120, 130)])
+def test_reorder_of_many_states_refuses_before_it_moves(at, count):
+    """More states than one launch takes: a result given twice, one that another state
+    reads, and one refused by itself, each beyond the first group. Nothing has moved."""
+    rng = np.random.default_rng(at)
+    all_ = to_dev(rng.integers(-99, 99, (count, 6, 8)).astype(np.int32))
+    second = torch.full_like(all_, 7)
+    parent = torch.tensor([[1, 2, 0], [2, 2, 1]], dtype=torch.int32, device=DEV)
+    before = all_.clone()
+    case(f"beam_reorder {count} states, refused at {at}")
+    for first in (0, 3):
+        states = list(all_.unbind())
+        states[at] = states[first]
+        with pytest.raises(ValueError, match="share a result"):
+            qg.beam_reorder(states, parent)
+        states, out = list(all_.unbind()), list(second.unbind())
+        out[at] = out[first]
+        with pytest.raises(ValueError, match="share a result"):
+            qg.beam_reorder(states, parent, out=out)
+        states[at], out = out[first], list(second.unbind())  # reads what the first group writes
+        with pytest.raises(ValueError, match="share a result"):
+            qg.beam_reorder(states, parent, out=out)
+    states = list(all_.unbind())
+    states[at] = parent.view(6, 1)  # a state over the parents
+    with pytest.raises(qg.QGError):
+        qg.beam_reorder(states, parent)
+    states, out = list(all_.unbind()), list(second.unbind())
+    both = torch.zeros(9, 8, dtype=torch.int32, device=DEV)
+    states[at], out[at] = both[:6], both[3:]
+    with pytest.raises(qg.QGError):
+        qg.beam_reorder(states, parent, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(all_, before) and bool((second == 7).all())
+    states = list(all_.unbind())
+    states[at] = states[first]
+    out = list(second.unbind())  # one source twice is fine
+    qg.beam_reorder(states, parent, out=out)
+    rows = torch.tensor([1, 2, 0, 5, 5, 4], device=DEV)
+    assert all(torch.equal(o, s[rows]) for o, s in zip(out, states))
+    qg.beam_reorder(list(all_.unbind()), parent)
+    assert torch.equal(all_, before[:, rows])

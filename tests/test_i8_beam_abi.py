@@ -203,3 +203,16 @@ def test_reorder_validation(L):
     if no_gpu():
         assert call(state(), state(dst=D)) in (EDEV, EUNSUP)  # one source twice is fine
     assert call(state(span=1 << 36, src_row=1 << 36, dst_row=1 << 36, dst=1 << 45)) == ESHAPE  # 2^32 columns of 16 bytes
+
+
+def test_reorder_check_refuses_alike_and_launches_nothing(L):
+    def call(*states, bi=3, bo=3, parent=C):
+        arr = (qg._BeamState * len(states))(*states)
+        return L.qg_beam_reorder_check(ctypes.addressof(arr), len(states), parent, 2, bi, bo)
+
+    assert call(state()) == OK and call(state(), state(dst=D)) == OK  # without a device, too
+    assert call(state(), state(src=D)) == ESHAPE and call(state(dst=C - 64)) == ESHAPE
+    assert call(state(dst=A), bo=2) == ESHAPE and call(state(span=0)) == ESHAPE
+    assert call(state(src=None)) == ENULL and call(state(), parent=C + 2) == EALIGN
+    assert call(*[state(dst=B + 0x100000 * i) for i in range(57)]) == ESHAPE
+    assert b"57" in L.qg_last_error()
