@@ -432,9 +432,9 @@ qg_status lmhead_topk(const void* w_packed, const float* x, int64_t M, int64_t K
  * the pages give no format for either, so this one is the library's own:
  *   y[n, m] = x_scale[n] * w_scale[m] * sum_k xq[n, k] * wq[m, k]  (+ bias[m])
  * with int8 xq, wq and float32 scales. The sums are exact int32 (hence
- * K <= QG_I8_MAX_K); each is converted to float32, multiplied by the rounded
- * product of the two scales, the bias is added, all in float32, and the result is
- * rounded once more when Y is fp16 (beyond +-65504 infinite) or bf16. Any number
+ * K <= QG_I8_MAX_K); each is converted to float32, the two scales are multiplied in
+ * float32, and one fused float32 operation multiplies the two and adds the bias (a
+ * single rounding); the result is rounded once more when Y is fp16 (beyond +-65504 infinite) or bf16. Any number
  * of columns N >= 1: decode and verification columns, beams, prefill tokens.
  * Matrices that share their activations (Q, K and V; gate and up) are one product
  * over their rows stacked.

@@ -226,7 +226,9 @@ struct GArgs {
     int32_t total;       // tiles of Y
 };
 
-QG_DEV float scaled(int acc, float xs, float ws, float b) { return (float)acc * (xs * ws) + b; }
+// Written as one operation, which rounds the product and the bias together: left as a
+// product and a sum, their rounding would be the compiler's choice, form by form.
+QG_DEV float scaled(int acc, float xs, float ws, float b) { return __builtin_fmaf((float)acc, xs * ws, b); }
 
 template <int YT>
 QG_DEV uint32_t pack2(float lo, float hi) {

@@ -36,6 +36,21 @@ def product_tolerance(y, p, eps_out, tiny):
     return 3.01 * half * np.abs(p) + 1.01 * (half + eps_out / 2) * np.abs(y) + tiny
 
 
+def fused32(a, b, c):
+    """a * b + c of float32 arrays rounded once to float32. The product is exact in float64
+    (48 bits) and the sum's error is known exactly, so the sum is first rounded to odd: its
+    last bit stands for all that was cut off, and 53 bits rounded to 24 then give what the
+    exact sum would."""
+    p, c = a.astype(np.float64) * b.astype(np.float64), c.astype(np.float64)
+    s = p + c
+    t = s - p
+    err = (p - (s - t)) + (c - t)
+    bits = s.view(np.int64)
+    away = (err > 0) == (s > 0)  # the exact sum is farther from zero than s
+    odd = np.where((err != 0) & (bits & 1 == 0), np.where(away, bits + 1, bits - 1), bits)
+    return odd.view(np.float64).astype(np.float32)
+
+
 def beam_select(z, score, n, finished=None, length=None, eos=-1, alpha=0.0):
     """Selection over (B, W, V) float64 logits; returns a dict of (B, n) arrays."""
     B, W, V = z.shape

@@ -222,3 +222,28 @@ def test_refusals():
         qg.quantize_i8_rows(torch.zeros(3, 4, device=DEV).t())
     with pytest.raises(ValueError):
         qg.pack_i8(torch.zeros(3, 200000, dtype=torch.int8, device=DEV))
+
+
+FORMS = [("streamed", 100, 300, 5), ("streamed, 32 columns", 500, 300, 20), ("walk", 16500, 1030, 3),
+         ("walk, 32 columns", 16500, 1030, 20), ("tiles of 64", 1000, 191, 100), ("tiles of 64, split", 256, 18944, 40),
+         ("tiles of 128, three buffers", 1664, 200, 1300), ("tiles of 128, split", 300, 8200, 100),
+         ("tiles of 128, two buffers", 4700, 200, 1000), ("tiles of 256", 3300, 200, 4001),
+         ("tiles of 256, two for a workgroup", 4300, 200, 4100)]
+
+
+@pytest.mark.parametrize("form,M,K,N", FORMS)
+def test_product_and_bias_are_rounded_once(form, M, K, N):
+    """Every form bit for bit: the sum to float32, the scales' product to float32, product
+    and bias in one rounding, one more to a 16-bit output."""
+    wq, xq, ws, xs, _ = operands(M, K, N, seed=M + K + N)
+    rng = np.random.default_rng(M)
+    b = (rng.standard_normal(M) * 40 * np.sqrt(K) * ws * xs.mean()).astype(np.float32)  # as large as the products
+    acc = (torch.from_numpy(xq).double() @ torch.from_numpy(wq).double().t()).numpy().astype(np.float32)
+    scale = xs[:, None] * ws[None]
+    want = torch.from_numpy(beamref.fused32(acc, scale, np.broadcast_to(b, scale.shape)))
+    assert bool((want != torch.from_numpy(acc * scale + b)).any())  # two roundings are told apart
+    wp, dx, dw, ds, db = qg.pack_i8(to_dev(wq)), to_dev(padded(xq)), to_dev(ws), to_dev(xs), to_dev(b)
+    for t, dtype in TYPES.items():
+        case(f"qgemm_i8 {form} M={M} K={K} N={N} {t} rounded once")
+        y = qg.qgemm_i8(wp, dw, dx, ds, M, K, bias=db, dtype=dtype)[:, :M].cpu()
+        assert torch.equal(y, want.to(dtype)), (form, t, int((y != want.to(dtype)).sum()))
