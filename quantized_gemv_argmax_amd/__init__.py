@@ -202,7 +202,8 @@ class Workspace:
     needs nothing and leaves all of it undefined. One workspace may serve the first two
     in turn, cleared between them by the calls themselves, but not those and the third,
     whichever came first. Outgrown buffers are kept, as a captured graph may still hold
-    them."""
+    them; a buffer is at least twice the one before it, so that together they are smaller
+    than the current one. release_outgrown() frees them."""
 
     def __init__(self, device=None, nbytes: int = 0):
         self.device = torch.device(device if device is not None else "cuda")
@@ -216,7 +217,13 @@ class Workspace:
         if nbytes and (self.buf is None or self.buf.numel() < nbytes):
             if self.buf is not None:
                 self.outgrown.append(self.buf)
-            self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=self.device)
+            self.buf = torch.zeros(max(nbytes, 1 << 20, 2 * self.nbytes()), dtype=torch.uint8, device=self.device)
+        return self
+
+    def release_outgrown(self):
+        """Frees the buffers that growing has replaced: once no captured graph that used
+        this workspace will be replayed, and its calls on other streams have ended."""
+        self.outgrown.clear()
         return self
 
     def serve(self, nbytes: int, kind: str):

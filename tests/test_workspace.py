@@ -49,6 +49,17 @@ def test_default_workspace_is_kept_for_calls_that_need_zeros(monkeypatch):
     qg._ws(None, 64, "cpu:0")  # what the LM-head calls take
 
 
+def test_outgrown_buffers_stay_smaller_than_the_current_one():
+    ws = qg.Workspace("cpu")
+    for need in range(1 << 20, 12 << 20, 1 << 18):  # shapes that grow step by step
+        ws.serve(need, "zeros")
+        assert ws.nbytes() >= need and int(ws.buf.count_nonzero()) == 0
+        assert sum(b.numel() for b in ws.outgrown) < ws.nbytes()
+    assert 0 < len(ws.outgrown) <= 4
+    ws.buf[3] = 1
+    assert not ws.release_outgrown().outgrown and int(ws.buf[3]) == 1
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("first", ["product", "head", "topk"])
 def test_products_and_heads_share_a_workspace(first):
