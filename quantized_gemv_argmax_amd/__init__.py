@@ -672,6 +672,13 @@ def _launch(name, gpu, *args):
         _check(name, status)
 
 
+def _int32(**values):
+    """The library's 32-bit arguments would take a larger number's low 32 bits."""
+    for name, v in values.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name}={v} does not fit 32 bits")
+
+
 def _gpu(name, t, dtypes):
     """Index of the GPU that holds t, a tensor of one of `dtypes`."""
     if not isinstance(t, torch.Tensor) or t.get_device() < 0:
@@ -824,6 +831,7 @@ def logits_beam_select(logits: torch.Tensor, score: torch.Tensor, n: int, finish
         raise ValueError("score must be (batch, beams)")
     shape = score.shape
     B, W = shape
+    _int32(beams=W, n=n, eos=eos)
     _same("score", score, _F32, gpu, shape)
     _, V, ld = _rows_of("logits", logits, _TYPES, gpu, B * W, 0)
     if finished is not None:
@@ -837,8 +845,6 @@ def logits_beam_select(logits: torch.Tensor, score: torch.Tensor, n: int, finish
             t = getattr(out, name)
             if t is not None:
                 _same("out." + name, t, types, gpu, (B, n))
-    if not -(1 << 31) <= eos < 1 << 31:
-        raise ValueError(f"eos={eos} is no token")
     xt = _TYPES[logits.dtype]
     wp, wb, keep = _scratch(ws, L.logits_beam_select_workspace_bytes(xt, B, W, V, n), logits.device)
     ci = _BeamIn(logits.data_ptr(), xt, ld, B, W, V, score.data_ptr(), _ptr(finished), _ptr(length), length_penalty, eos)
@@ -907,6 +913,7 @@ def beam_reorder(states, parent: torch.Tensor, out=None):
     if not isinstance(first, torch.Tensor) or not B or not n or first.dim() < 1 or first.shape[0] % B:
         raise ValueError(f"{tuple(parent.shape)} parents do not fit the first state")
     W = first.shape[0] // B
+    _int32(beams=W, n=n)
     # states that look alike (a model's layers) are cut into pieces once
     fields, seen, moves = [], None, None
     for i, s in enumerate(states):

@@ -544,3 +544,14 @@ def test_reorder_of_many_states_refuses_before_it_moves(at, count):
     assert all(torch.equal(o, s[rows]) for o, s in zip(out, states))
     qg.beam_reorder(list(all_.unbind()), parent)
     assert torch.equal(all_, before[:, rows])
+
+
+def test_counts_beyond_32_bits_are_refused():
+    # (of 2^32 + 3 the library would see 3)
+    z, s = torch.zeros(6, 100, device=DEV), torch.zeros(2, 3, device=DEV)
+    for n in (2 ** 32 + 3, 2 ** 31, -(2 ** 32) + 3):
+        with pytest.raises(ValueError, match="does not fit 32 bits"):
+            qg.logits_beam_select(z, s, n)
+    many = torch.zeros(1, 1, dtype=torch.uint8, device=DEV).expand(2 ** 32 + 3, 1)
+    with pytest.raises(ValueError, match="does not fit 32 bits"):
+        qg.beam_reorder([many], torch.zeros(1, 3, dtype=torch.int32, device=DEV), out=[torch.zeros(3, 1, dtype=torch.uint8, device=DEV)])
