@@ -547,7 +547,7 @@ qg_status logits_beam_select(const qg_beam_in* in /* host */, int n, void* works
  * are src_row / dst_row bytes apart. dst == src moves in place (then beams_in ==
  * beams_out and equal strides): rows whose parent is themselves are not touched, and
  * every row is read before any is overwritten. Otherwise src and dst must not
- * overlap. A parent outside [0, beams_in) leaves its dst row as it was. States of one
+ * overlap, each taken from its first to its last byte. A parent outside [0, beams_in) leaves its dst row as it was. States of one
  * call must not overlap each other's; they need no alignment.
  * 1 <= count <= QG_BEAM_MAX_STATES, 1 <= beams_in, beams_out <= QG_BEAM_MAX, 1 <= batch
  * <= 65535; outer * span < 2^40, and outer * ceil(span / 16) < 2^32 - 256;

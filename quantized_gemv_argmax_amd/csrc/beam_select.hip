@@ -206,8 +206,8 @@ struct Row {
 // ---------------------------------------------------------------- stage 1
 // A segment per wavefront, SV vectors of each lane; 8 / SV lanes' make a tile. Bound by
 // its double-precision instructions, about 14 of 25 per element and at half the rate of
-// float32's: 16 x 8 rows of 152064 bf16 (39 MB) take 20 us, with the exponentials
-// replaced by a subtraction 12. (Walking wavefronts with the next segment's loads ahead
+// float32's: 16 x 8 rows of 152064 bf16 (39 MB) take 21 us (a fifth of them finished:
+// 20.7); with the exponentials replaced by a subtraction 20 became 12. (Walking wavefronts with the next segment's loads ahead
 // of the work on one: 22 us. Splitting the polynomial between float32 and double, or a
 // table of powers, trades as many instructions as it saves.)
 template <int XT, int SV>
@@ -658,7 +658,7 @@ QG_DEV void rank_item(const BArgs& a, int64_t item, const Beam& beam, ItemShared
     }
 }
 
-// Bound by latency: 9.7 us for 4 rows of 152064 fp32 and n = 8, of them about 1 us each for
+// Bound by latency: 9.6 us for 4 rows of 152064 fp32 and n = 8, of them about 1 us each for
 // reading the tile maxima, for the bound, for the listed tiles' elements and for the
 // candidates of the other rows, under 1 us for each ranking and for the arrival.
 template <int XT, int SV>

@@ -700,8 +700,9 @@ __global__ __launch_bounds__(64) void gemm_i8_join_kernel(GArgs a, int tiles, in
 // ---------------------------------------------------------------- launches
 // How a product runs: few columns stream the weights past them; else a tile form,
 // perhaps split along K. 17 to 32 columns take tiles of 64 for K beyond the walk's
-// (3584 x 18944 by 32: 18.8 us in 4 splits, streamed 26.6; 30000 x 6000 by 32: 42.6 and
-// 63.7) unless the tiles are few (2000 x 8000 by 20: 10.2 and 9.4).
+// (3584 x 18944 by 32: 19.7 us in 4 splits, streamed 26; 30000 x 6000 by 32: 42 and 61)
+// unless the tiles are few (2000 x 8000 by 20: streamed 8.3, tiles of 64 in two splits 14.4).
+// (These times and those below: calls in a graph, bf16 outputs, weights from memory.)
 enum { FORM_STREAM, FORM_64, FORM_128_DEEP, FORM_128, FORM_256 };
 struct Plan {
     int form, tiles, splits, kper;
@@ -709,17 +710,21 @@ struct Plan {
 };
 
 // The largest tile that still gives most compute units one, larger tiles reading the
-// operands less often (37888 x 3584 by 4096 columns: 534 us in tiles of 256, 1094 in
-// tiles of 64; 18944 x 3584 by 256: 36 us in 296 tiles of 128, 45 in 74 of 256 split
-// three ways; 1000 x 1000 by 1000: 6.2 us in 256 tiles of 64, 9.6 in 64 of 128), but
-// tiles of 128 where K is long (3584 x 18944 by 256: 36 us, tiles of 64 43).
+// operands less often (37888 x 3584 by 4096 columns: 485 us in tiles of 256, 548 in 128,
+// 1054 in 64; 18944 x 3584 by 256: 33 us in 296 tiles of 128, 52 in 74 of 256; 1000 x 1000
+// by 1000: 6.4 us in 256 tiles of 64, 8.3 in 64 of 128), but tiles of 128 where K is long
+// (3584 x 18944 by 256: 36 us, tiles of 64 97). The rule does not see how full the last
+// round of tiles of 256 is: in 1.1 rounds of them 4608 x 3584 by 4096 takes 86 us (tiles of
+// 128: 76), 18944 x 3584 by 1024 89 (84), 37888 x 3584 by 512 105 (89) and by 300 97 (64).
 // Tiles of 128 take three LDS buffers up to a workgroup per compute unit, two, with two
-// workgroups per unit, beyond (296 tiles: 36 us, with three buffers 45; 144 tiles of
-// 4608 x 3584 by 512: 23 us, with three 19).
+// workgroups per unit, beyond (296 tiles: 33 us, with three buffers 41; 144 tiles of
+// 4608 x 3584 by 512: 28 us, with three 20).
 // With fewer tiles than units a long K is split until about 256 workgroups share it,
 // each keeping some K tiles to repay the second launch: 3584 x 18944 by 64 columns takes
-// 21.1 us in 4 splits of tiles of 64 (3: 24.4, 8: 22.7), 4608 x 3584 by 64 9.9 unsplit
-// and 10.6 in two; in tiles of 128, 3584 x 18944 by 128 26 us in 8 and 28 in 6.
+// 20 us in 4 splits of tiles of 64 (1: 97, 3: 24, 8: 22), by 128 25 us in 8 of tiles of 128
+// (6: 27). The least K tiles of a split, 28 and 18, were chosen with weights in the caches,
+// where 4608 x 3584 by 64 takes 10.4 us whole, 10.2 in two; with weights from memory it
+// takes 21 whole, 12 in two.
 Plan plan(int64_t M, int64_t K, int64_t N) {
     Plan p{};
     const int kt = (int)qg::ceil_div(K, 2 * kKB);
