@@ -217,7 +217,8 @@ class Workspace:
         if nbytes and (self.buf is None or self.buf.numel() < nbytes):
             if self.buf is not None:
                 self.outgrown.append(self.buf)
-            self.buf = torch.zeros(max(nbytes, 1 << 20, 2 * self.nbytes()), dtype=torch.uint8, device=self.device)
+            with torch.inference_mode(False):  # (an inference tensor could not be cleared outside that mode)
+                self.buf = torch.zeros(max(nbytes, 1 << 20, 2 * self.nbytes()), dtype=torch.uint8, device=self.device)
         return self
 
     def release_outgrown(self):

@@ -60,6 +60,14 @@ def test_outgrown_buffers_stay_smaller_than_the_current_one():
     assert not ws.release_outgrown().outgrown and int(ws.buf[3]) == 1
 
 
+def test_a_buffer_made_in_inference_mode_can_be_cleared_outside():
+    ws = qg.Workspace("cpu")
+    with torch.inference_mode():
+        ws.serve(64, "counters")
+        ws.buf[0] = 1
+    assert int(ws.serve(64, "zeros").buf[0]) == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("first", ["product", "head", "topk"])
 def test_products_and_heads_share_a_workspace(first):
