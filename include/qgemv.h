@@ -60,8 +60,8 @@
  * Workspaces: the LM-head entry points (lmhead_argmax, lmhead_argmax_verify,
  * lmhead_argmax_verify_q8_1, lmhead_topk) and logits_topk take one; each reports
  * the bytes it needs through its *_workspace_bytes query (so do
- * qgemm_q4k_smalln_batch_ws, qgemm_i8 and logits_beam_select, whose rules stand at
- * their declarations). A workspace of those LM-head and top-k calls must be
+ * qgemm_q4k_smalln_batch_ws, qgemm_i8, qgemm_f8, logits_beam_select and
+ * logits_expert_select, whose rules stand at their declarations). A workspace of those LM-head and top-k calls must be
  * all-zero when first used (qg_workspace_clear, or any zero-filled allocation)
  * and every call leaves it all-zero again, so one workspace can serve every entry
  * point in turn. A call that fails on the device may leave it dirty: clear it
@@ -572,6 +572,150 @@ qg_status qg_beam_reorder(const qg_beam_state* states /* host */, int count, con
                           int beams_in, int beams_out, qg_stream_t stream);
 qg_status qg_beam_reorder_check(const qg_beam_state* states /* host */, int count, const int32_t* parent, int64_t batch,
                                 int beams_in, int beams_out);
+
+/*
+ * Products on 8-bit floating-point values with block scales, dense and grouped by
+ * expert ("Why Local LLMs Don't Need C++ or Python" decodes a mixture-of-experts model
+ * and keeps FP8 values beside FP16 ones; the dotLLM README scales blocks of quantized
+ * weights and activations; neither page gives this format, so it is the library's own):
+ *   y[n, m] = sum_b x_scale[n, b] * w_scale[m / 128, b] * S_b  (+ bias[m]),
+ *   S_b = sum over the block's k = 128 b .. 128 b + 127 of xq[n, k] * wq[m, k]
+ * with xq and wq in e4m3 (sign, 4 exponent bits of bias 7, 3 mantissa bits, no
+ * infinities, 0x7f and 0xff NaN, largest value 448), float32 scales, one per row and block of
+ * activations and one per 128 x 128 block of weights. S_b is scaled by one float32
+ * multiply-add per block; bias is added in float32, and the result rounded once more
+ * when Y is fp16 (beyond +-65504 infinite) or bf16. Where Y is float32, S_b is a float32
+ * sum of exact products. Where Y is fp16 or bf16 and there are more than a few rows, S_b
+ * comes from the 8-bit matrix cores, which align each eight products to the largest and
+ * keep 13 bits below its leading one: its error is below 2^-10 * sum |xq * wq| (measured:
+ * 1.5e-5 of the result for normally distributed values, 2^-12 of the sum of magnitudes at
+ * worst for random bytes), under the rounding of the output where the sum does
+ * not cancel. Results are deterministic; they may differ in the last bits between
+ * numbers of rows, which run in different forms.
+ *
+ * qg_pack_f8 lays the weights out once, at load time: `experts` matrices (1 for a dense
+ * product) of M rows of K bytes, rows ldw >= K bytes apart, matrices w_expert bytes apart
+ * (ignored for one). The packed buffer has qg_f8_bytes(M, K, experts) bytes: per
+ * matrix rows padded to 16 and K to 128 with zeros, and the 16 bytes k = 128 b + 64 h +
+ * 16 g .. + 15 of row 16 t + i at (((t * ceil(K / 128) + b) * 2 + h) * 64 + 16 g + i) * 16.
+ * w needs no alignment and must not overlap dst. 1 <= M <= QG_F8_MAX_ROWS, 1 <= K <=
+ * QG_F8_MAX_K, 1 <= experts <= QG_EXPERTS_MAX, at most 2^40 bytes. w_scale: row-major
+ * [experts][ceil(M / 128)][ceil(K / 128)].
+ *
+ * qg_quantize_f8_rows quantizes rows of fp32, fp16 or bf16 (row n at x + n * ldx
+ * elements): of K values x, or with gated = 1 of 2 K values g and u that enter as
+ * g / (1 + exp(-g)) * u in float32. scale[n, b] = max |.| / 448 over block b, rounded to
+ * float32; q = x / scale rounded to the nearest e4m3 value, ties to even, decided on the
+ * exact quotient and clamped to +-448 (0 where the scale is 0). Bytes K .. round_up(K,
+ * 128) - 1 of each row of q and the scales up to a multiple of 4 blocks are set to 0;
+ * ldq >= round_up(K, 128), a multiple of 16; lds >= ceil(K / 128) rounded up to 4, a
+ * multiple of 4; what lies beyond is left as it is. A block that holds an infinity or
+ * NaN gets scale NaN and zeros. count: NULL, or a device int32 (offsets + experts of a
+ * selection below, say): only rows below *count are read and written.
+ * ldx >= K (2 K); x needs the alignment of its elements only. 1 <= N <= QG_F8_MAX_ROWS;
+ * N * ldx, N * ldq and N * lds at most 2^40.
+ *
+ * qgemm_f8: xq has rows of ldx bytes, round_up(K, 128) <= ldx <= 2^22, a multiple of 16,
+ * zero from K to round_up(K, 128); x_scale rows of ldxs floats, a multiple of 4 >=
+ * ceil(K / 128), at most 2^20 (what lies beyond ceil(K / 128) may be anything); Y rows of
+ * ldy >= M elements of y_type, ldy a multiple of 4. Only Y[n, 0..M) is written. bias may
+ * be NULL. 1 <= N <= QG_F8_MAX_ROWS, M * N <= 2^32. w_packed, xq, x_scale and Y 16-byte
+ * aligned, the others 4. Workspace: qgemm_f8_workspace_bytes(M, K, N, y_type) bytes (0:
+ * none needed; 0 too for an invalid shape), for the partial sums of products split along K;
+ * no preparation needed, contents undefined afterwards; calls that overlap must not
+ * share it.
+ *
+ * qgemm_f8_grouped: rows offsets[e] .. offsets[e + 1] - 1 of Y are products with expert
+ * e's matrix (and bias[e], row-major [experts][M], or NULL). offsets (device int32,
+ * experts + 1 of them) ascend within 0 .. rows; they need not start at 0 nor end at
+ * `rows`, and rows of Y outside them are left as they are. Row r of Y comes from row
+ * row[r] of xq (device int32, in [0, x_rows)), or from row r where `row` is NULL (then
+ * x_rows >= rows). Nothing is read or written out of bounds whatever offsets and row
+ * hold, but what rows get from indices out of range, or from offsets that descend, is undefined.
+ * 1 <= rows, x_rows <= QG_F8_MAX_ROWS, M * rows <= 2^32; with `row`, xq and x_scale
+ * below 2^32 bytes; the rest as for qgemm_f8. No workspace. The host does not
+ * read offsets: a call can be captured and replayed with others.
+ */
+#define QG_F8_BLOCK 128
+#define QG_F8_MAX_K 131072
+#define QG_F8_MAX_ROWS 4194303
+#define QG_EXPERTS_MAX 1024
+typedef struct {
+    const void* w_packed;
+    const float* w_scale;
+    const void* xq;
+    int64_t ldx;
+    const float* x_scale;
+    int64_t ldxs;
+    int64_t x_rows;
+    const int32_t* row; /* or NULL */
+    const int32_t* offsets;
+    const float* bias; /* or NULL */
+    void* Y;
+    int y_type;
+    int64_t ldy;
+    int64_t M;
+    int64_t K;
+    int64_t experts;
+    int64_t rows;
+} qg_f8_grouped;
+size_t qg_f8_bytes(int64_t M, int64_t K, int64_t experts);
+qg_status qg_pack_f8(const void* w, int64_t ldw, int64_t w_expert, void* dst, int64_t M, int64_t K, int64_t experts,
+                     qg_stream_t stream);
+qg_status qg_quantize_f8_rows(const void* x, int x_type, int64_t ldx, int gated, const int32_t* count, int64_t N, int64_t K,
+                              void* q, int64_t ldq, float* scale, int64_t lds, qg_stream_t stream);
+size_t qgemm_f8_workspace_bytes(int64_t M, int64_t K, int64_t N, int y_type);
+qg_status qgemm_f8(const void* w_packed, const float* w_scale, const void* xq, int64_t ldx, const float* x_scale,
+                   int64_t ldxs, const float* bias, void* Y, int y_type, int64_t ldy, int64_t M, int64_t K, int64_t N,
+                   void* workspace, size_t workspace_bytes, qg_stream_t stream);
+qg_status qgemm_f8_grouped(const qg_f8_grouped* problem /* host */, qg_stream_t stream);
+
+/*
+ * Selection of experts and the weighted sum of their outputs, around qgemm_f8_grouped
+ * (a mixture-of-experts layer, as in the model that "Why Local LLMs Don't Need C++ or
+ * Python" measures; the ranking is logits_topk's, row by row: dotLLM README, top-k and softmax).
+ *
+ * logits_expert_select ranks each of N rows of E logits (logits_type, rows ld elements
+ * apart) and takes the k best, best first, equal logits by lower expert:
+ *   expert[n, j]   the expert
+ *   weight[n, j]   scale * exp(z_j - z_max) / sum, the sum over all E experts, or with
+ *                  normalize = 1 over the k that are taken; float32
+ *   offsets[e]     how many (n, j) chose an expert below e; offsets[E] of all (E + 1)
+ *   row[r]         the rows n in the order of the experts, and for one expert of n:
+ *                  expert e has r = offsets[e] .. offsets[e + 1] - 1; -1 from offsets[E] on
+ *   position[n, j] the r of (n, j)
+ * An expert whose logit is -inf or NaN (switched off) is not taken; where a row has
+ * fewer than k, the remaining entries are expert -1, weight 0, position -1, so a row of
+ * -inf (padding) asks for nothing. A logit of +inf counts as the largest finite float.
+ * offsets and row are what qgemm_f8_grouped takes (rows = N * k, x_rows = N).
+ * 1 <= E <= QG_EXPERTS_MAX, 1 <= k <= min(E, QG_EXPERTS_MAX_K), 1 <= N, N * k <=
+ * QG_F8_MAX_ROWS, ld in [E, 2^40 / N]. logits need the alignment of their elements, the others 4
+ * bytes. Workspace: logits_expert_select_workspace_bytes(N, E, k) bytes, 16-byte aligned (0: none), no
+ * preparation needed, contents undefined afterwards; calls that overlap must not share it.
+ *
+ * qg_expert_combine: out[n, 0..M) = (add ? add[n, ..] : 0) + sum_j weight[n, j] *
+ * Y[position[n, j], ..], j ascending, in float32, rounded once; entries whose position is
+ * not in [0, rows) are skipped whatever their weight. Y: `rows` rows of M of y_type, ldy elements apart; add
+ * and out: N rows of out_type, ldadd and ldo apart; add may be out itself (then equal strides), otherwise
+ * out must not overlap an input. All need the alignment of their elements only. 1 <= k <=
+ * QG_EXPERTS_MAX_K; 1 <= N, rows <= QG_F8_MAX_ROWS, N * ceil(M / 8) < 2^32 - 256; strides >= M, times their
+ * rows at most 2^40.
+ */
+#define QG_EXPERTS_MAX_K 32
+typedef struct {
+    int32_t* expert;
+    float* weight;
+    int32_t* position;
+    int32_t* row;
+    int32_t* offsets;
+} qg_experts_out;
+size_t logits_expert_select_workspace_bytes(int64_t N, int E, int k);
+qg_status logits_expert_select(const void* logits, int logits_type, int64_t ld, int64_t N, int E, int k, int normalize,
+                               float scale, void* workspace, size_t workspace_bytes, const qg_experts_out* out /* host */,
+                               qg_stream_t stream);
+qg_status qg_expert_combine(const void* Y, int y_type, int64_t ldy, int64_t rows, const int32_t* position,
+                            const float* weight, int k, const void* add /* or NULL */, int64_t ldadd, void* out,
+                            int out_type, int64_t ldo, int64_t N, int64_t M, qg_stream_t stream);
 
 /*
  * Launch override, for tests and measurements only (not needed for correct

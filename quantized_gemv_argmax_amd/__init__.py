@@ -23,6 +23,10 @@ I8_MAX_K = 131071
 BEAM_MAX = 32
 BEAM_MAX_SELECT = 64
 BEAM_MAX_STATES = 56
+F8_BLOCK = 128
+F8_MAX_K = 131072
+EXPERTS_MAX = 1024
+EXPERTS_MAX_K = 32
 
 _lib = None
 
@@ -88,6 +92,18 @@ class _BeamState(ctypes.Structure):
                 ("outer", ctypes.c_int64), ("span", ctypes.c_int64)]
 
 
+class _F8Grouped(ctypes.Structure):
+    _fields_ = [("w_packed", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("xq", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("x_scale", ctypes.c_void_p), ("ldxs", ctypes.c_int64), ("x_rows", ctypes.c_int64), ("row", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("y_type", ctypes.c_int),
+                ("ldy", ctypes.c_int64), ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("experts", ctypes.c_int64),
+                ("rows", ctypes.c_int64)]
+
+
+class _ExpertsOut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("expert", "weight", "position", "row", "offsets")]
+
+
 _P, _I64, _SZ, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
 
 _SIGS = {
@@ -139,6 +155,15 @@ _SIGS = {
     "logits_beam_select": (_I, [ctypes.POINTER(_BeamIn), _I, _P, _SZ, ctypes.POINTER(_BeamOut), _P]),
     "qg_beam_reorder": (_I, [_P, _I, _P, _I64, _I, _I, _P]),
     "qg_beam_reorder_check": (_I, [_P, _I, _P, _I64, _I, _I]),
+    "qg_f8_bytes": (_SZ, [_I64, _I64, _I64]),
+    "qg_pack_f8": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I64, _P]),
+    "qg_quantize_f8_rows": (_I, [_P, _I, _I64, _I, _P, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "qgemm_f8_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I]),
+    "qgemm_f8": (_I, [_P, _P, _P, _I64, _P, _I64, _P, _P, _I, _I64, _I64, _I64, _I64, _P, _SZ, _P]),
+    "qgemm_f8_grouped": (_I, [ctypes.POINTER(_F8Grouped), _P]),
+    "logits_expert_select_workspace_bytes": (_SZ, [_I64, _I, _I]),
+    "logits_expert_select": (_I, [_P, _I, _I64, _I64, _I, _I, _I, ctypes.c_float, _P, _SZ, ctypes.POINTER(_ExpertsOut), _P]),
+    "qg_expert_combine": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _P, _I64, _P, _I, _I64, _I64, _I64, _P]),
 }
 
 
@@ -198,8 +223,8 @@ class Workspace:
     """A device scratch buffer reused across calls on one stream (grown on demand).
     It starts all-zero. Three kinds of calls use one: "zeros" (the LM-head and top-k
     calls) needs it so and leaves it so; "counters" (qgemm_q4k_smalln_batch_ws) needs its
-    counters zero and leaves the rest undefined; "scratch" (qgemm_i8, logits_beam_select)
-    needs nothing and leaves all of it undefined. One workspace may serve the first two
+    counters zero and leaves the rest undefined; "scratch" (qgemm_i8, qgemm_f8,
+    logits_beam_select, logits_expert_select) needs nothing and leaves all of it undefined. One workspace may serve the first two
     in turn, cleared between them by the calls themselves, but not those and the third,
     whichever came first. Outgrown buffers are kept, as a captured graph may still hold
     them; a buffer is at least twice the one before it, so that together they are smaller
@@ -231,8 +256,8 @@ class Workspace:
         """ensure(nbytes) for a call of `kind`, zeros where it needs them."""
         if kind not in self.kinds:
             if self.kinds and "scratch" in (kind, *self.kinds):
-                raise ValueError("a workspace of qgemm_i8 or logits_beam_select, which leave it undefined, cannot serve "
-                                 "a call that needs zeros, nor the other way round: give each kind its own")
+                raise ValueError("a workspace of qgemm_i8, qgemm_f8, logits_beam_select or logits_expert_select, which leave it "
+                                 "undefined, cannot serve a call that needs zeros, nor the other way round: give each kind its own")
             self.kinds.add(kind)
         self.ensure(nbytes)
         # A captured "counters" call may have run since, so this is not done once. (A
@@ -945,3 +970,208 @@ def beam_reorder(states, parent: torch.Tensor, out=None):
     for k in groups:
         _launch("qg_beam_reorder", gpu, at + k * 64, min(BEAM_MAX_STATES, count - k), parent.data_ptr(), B, W, n)
     return results
+
+
+# ------------------------------------------------------------------ 8-bit floating-point rows and products
+_F8 = (torch.float8_e4m3fn,)
+
+
+def f8_bytes(M: int, K: int, experts: int = 1) -> int:
+    return int(lib().qg_f8_bytes(M, K, experts))
+
+
+def pack_f8(w: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Lay out e4m3 weights (float8_e4m3fn) for qgemm_f8, one matrix (M, K), or for
+    qgemm_f8_grouped, one per expert (experts, M, K); rows contiguous, at any strides.
+    Returns a uint8 buffer of f8_bytes(M, K, experts) bytes."""
+    gpu = _gpu("w", w, _F8)
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be (M, K) or (experts, M, K)")
+    E = w.shape[0] if w.dim() == 3 else 1
+    M, K = w.shape[-2:]
+    n = f8_bytes(M, K, E)
+    if n == 0:
+        raise ValueError(f"no e4m3 layout for {E} matrices of {M} x {K}")
+    if K > 1 and w.stride(-1) != 1:
+        raise ValueError("w must have contiguous rows")
+    ldw = max(w.stride(-2), K) if M > 1 else K
+    each = w.stride(0) if E > 1 else 0
+    if M > 1 and w.stride(-2) < K or E > 1 and each < (M - 1) * ldw + K:
+        raise ValueError(f"the rows or matrices of w overlap (strides {w.stride()})")
+    if out is None:
+        out = torch.empty(n, dtype=torch.uint8, device=w.device)
+    _same("out", out, _U8, gpu, (n,))
+    _launch("qg_pack_f8", gpu, w.data_ptr(), ldw, each, out.data_ptr(), M, K, E)
+    return out
+
+
+def quantize_f8_rows(x: torch.Tensor, gated: bool = False, count: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """E4m3 rows of x in fp32, fp16 or bf16 with a float32 scale per 128 values (max / 448):
+    of x (N, K), or with `gated` of silu(g) * u for x (N, 2 K) = g beside u. Returns
+    (q float8_e4m3fn (N, ldq), scale (N, lds)), ldq = K rounded up to 128 and lds = blocks
+    rounded up to 4, zeros beyond K. count: an int32 tensor of one element on the GPU; only the
+    first `count` rows are done."""
+    gpu = _gpu("x", x, _TYPES)
+    N, W, ldx = _rows_of("x", x, _TYPES, gpu, None, 0)
+    if gated and W % 2:
+        raise ValueError(f"x has {W} columns, not two halves")
+    K = W // 2 if gated else W
+    nb = (K + 127) // 128
+    kp, sp = nb * 128, (nb + 3) // 4 * 4
+    if count is not None:
+        _same("count", count, _I32, gpu, (1,))
+    if out is None:
+        out, ldq = torch.empty_strided((N, kp), (kp, 1), dtype=torch.float8_e4m3fn, device=x.device), kp
+    else:
+        ldq = _rows_of("out", out, _F8, gpu, N, kp)[2]
+    if scale is None:
+        scale, lds = torch.empty_strided((N, sp), (sp, 1), dtype=torch.float32, device=x.device), sp
+    else:
+        lds = _rows_of("scale", scale, _F32, gpu, N, sp)[2]
+    _launch("qg_quantize_f8_rows", gpu, x.data_ptr(), _TYPES[x.dtype], ldx, 1 if gated else 0,
+            None if count is None else count.data_ptr(), N, K, out.data_ptr(), ldq, scale.data_ptr(), lds)
+    return out, scale
+
+
+def qgemm_f8_workspace_bytes(M: int, K: int, N: int, dtype: torch.dtype = torch.float32) -> int:
+    return int(lib().qgemm_f8_workspace_bytes(M, K, N, _TYPES[dtype]))
+
+
+def _f8_operands(L, w, w_scale, xq, x_scale, M, K, experts, bias, shape):
+    """(gpu, rows of xq, ldx, ldxs) of a product's checked inputs; shape: () or (experts,)."""
+    gpu = _gpu("w", w, _U8)
+    if w.numel() != L.qg_f8_bytes(M, K, experts) or not w.is_contiguous():
+        raise ValueError(f"w is not {experts} packed {M} x {K} matrices" if shape else f"w is not a packed {M} x {K} matrix")
+    nb = (K + 127) // 128
+    X, _, ldx = _rows_of("xq", xq, _F8, gpu, None, nb * 128)
+    ldxs = _rows_of("x_scale", x_scale, _F32, gpu, X, (nb + 3) // 4 * 4)[2]
+    _same("w_scale", w_scale, _F32, gpu, shape + ((M + 127) // 128, nb))
+    if bias is not None:
+        _same("bias", bias, _F32, gpu, shape + (M,))
+    return gpu, X, ldx, ldxs
+
+
+def _product_rows(Y, dtype, gpu, N, M, device):
+    """(Y, type, ldy) of a product's result, allocated if need be."""
+    if Y is not None:
+        return Y, _TYPES[Y.dtype] if Y.dtype in _TYPES else -1, _rows_of("Y", Y, _TYPES, gpu, N, M)[2]
+    if dtype not in _TYPES:
+        raise ValueError(f"no output of type {dtype}")
+    ldy = (M + 3) // 4 * 4
+    return torch.empty_strided((N, ldy), (ldy, 1), dtype=dtype, device=device), _TYPES[dtype], ldy
+
+
+def qgemm_f8(w: torch.Tensor, w_scale: torch.Tensor, xq: torch.Tensor, x_scale: torch.Tensor, M: int, K: int,
+             bias: torch.Tensor | None = None, Y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+             ws: Workspace | None = None) -> torch.Tensor:
+    """Y[n, m] = sum_b x_scale[n, b] w_scale[m // 128, b] sum_{k in b} xq[n, k] wq[m, k] (+ bias[m])
+    over blocks b of 128, for weights packed by pack_f8 (w_scale (ceil(M / 128), ceil(K /
+    128))) and rows quantized by quantize_f8_rows. Returns Y (N, ldy) of `dtype` (fp32, fp16 or
+    bf16) with Y[:, :M] written. Without ws, a call that needs a workspace (products split
+    along K) allocates its own."""
+    L = lib()
+    gpu, N, ldx, ldxs = _f8_operands(L, w, w_scale, xq, x_scale, M, K, 1, bias, ())
+    Y, yt, ldy = _product_rows(Y, dtype, gpu, N, M, w.device)
+    need = L.qgemm_f8_workspace_bytes(M, K, N, yt)
+    wp, wb, keep = _scratch(ws, need, w.device) if need else (None, 0, None)
+    _launch("qgemm_f8", gpu, w.data_ptr(), w_scale.data_ptr(), xq.data_ptr(), ldx, x_scale.data_ptr(), ldxs,
+            None if bias is None else bias.data_ptr(), Y.data_ptr(), yt, ldy, M, K, N, wp, wb)
+    return Y
+
+
+def qgemm_f8_grouped(w: torch.Tensor, w_scale: torch.Tensor, xq: torch.Tensor, x_scale: torch.Tensor, M: int, K: int,
+                     offsets: torch.Tensor, row: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                     Y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """Products grouped by expert: rows offsets[e] .. offsets[e + 1] of Y (int32, ascending)
+    are those of qgemm_f8 with expert e's matrix (w of pack_f8 with experts, w_scale (experts,
+    ceil(M / 128), ceil(K / 128)), bias (experts, M)). Row r of Y comes from row row[r] of xq (int32), or
+    from row r. Returns Y (rows, ldy) with Y[offsets[0]:offsets[-1], :M] written; `rows` is
+    that of `row`, or of xq."""
+    L = lib()
+    gpu = _gpu("offsets", offsets, _I32)
+    if offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous, one more than there are experts")
+    E = offsets.numel() - 1
+    on, X, ldx, ldxs = _f8_operands(L, w, w_scale, xq, x_scale, M, K, E, bias, (E,))
+    if on != gpu:
+        raise ValueError(f"offsets is on GPU {gpu}, the other operands on GPU {on}")
+    N = X
+    if row is not None:
+        N = row.numel()
+        _same("row", row, _I32, gpu, (N,))
+    Y, yt, ldy = _product_rows(Y, dtype, gpu, N, M, w.device)
+    p = _F8Grouped(w.data_ptr(), w_scale.data_ptr(), xq.data_ptr(), ldx, x_scale.data_ptr(), ldxs, X, _ptr(row),
+                   offsets.data_ptr(), _ptr(bias), Y.data_ptr(), yt, ldy, M, K, E, N)
+    _launch("qgemm_f8_grouped", gpu, ctypes.byref(p))
+    return Y
+
+
+# ------------------------------------------------------------------ experts
+class ExpertSelection:
+    """Device outputs of logits_expert_select: expert (int32), weight (float32) and position
+    (int32), (N, k) each, row (int32, N * k) and offsets (int32, experts + 1)."""
+
+    def __init__(self, N: int, E: int, k: int, device):
+        whole = torch.empty_strided((4 * N * k + E + 1,), (1,), dtype=torch.int32, device=device)
+        n = N * k
+        self.expert, self.position = whole[:n].view(N, k), whole[n:2 * n].view(N, k)
+        self.weight = whole[2 * n:3 * n].view(torch.float32).view(N, k)
+        self.row, self.offsets = whole[3 * n:4 * n], whole[4 * n:]
+
+
+def logits_expert_select(logits: torch.Tensor, k: int, normalize: bool = False, scale: float = 1.0,
+                         out: ExpertSelection | None = None, ws: Workspace | None = None) -> ExpertSelection:
+    """The k best of each row's expert logits (N, E) in fp32, fp16 or bf16, rows at any
+    stride, their softmax weights (over all experts, or with `normalize` over the k taken, times
+    `scale`), and the rows in the experts' order: what qgemm_f8_grouped (offsets, row) and
+    expert_combine (position, weight) take. Ranking and special values as include/qgemv.h states."""
+    L = lib()
+    gpu = _gpu("logits", logits, _TYPES)
+    N, E, ld = _rows_of("logits", logits, _TYPES, gpu, None, 0)
+    _int32(experts=E, k=k)
+    if out is None:
+        if not (1 <= k <= min(E, EXPERTS_MAX_K) and N >= 1):
+            raise ValueError(f"k={k} for logits of shape {tuple(logits.shape)}: it is at most the experts and {EXPERTS_MAX_K}")
+        out = ExpertSelection(N, E, k, logits.device)
+    else:
+        for name, types, shape in (("expert", _I32, (N, k)), ("weight", _F32, (N, k)), ("position", _I32, (N, k)),
+                                   ("row", _I32, (N * k,)), ("offsets", _I32, (E + 1,))):
+            _same("out." + name, getattr(out, name), types, gpu, shape)
+    need = L.logits_expert_select_workspace_bytes(N, E, k)
+    wp, wb, keep = _scratch(ws, need, logits.device) if need else (None, 0, None)
+    co = _ExpertsOut(out.expert.data_ptr(), out.weight.data_ptr(), out.position.data_ptr(), out.row.data_ptr(),
+                     out.offsets.data_ptr())
+    _launch("logits_expert_select", gpu, logits.data_ptr(), _TYPES[logits.dtype], ld, N, E, k, 1 if normalize else 0, scale, wp,
+            wb, ctypes.byref(co))
+    return out
+
+
+def expert_combine(Y: torch.Tensor, position: torch.Tensor, weight: torch.Tensor, add: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, dtype: torch.dtype | None = None, M: int | None = None) -> torch.Tensor:
+    """out[n] = (add[n] +) sum_j weight[n, j] Y[position[n, j]] over the first M (default all) columns of
+    Y, in float32, rounded once to `dtype` (default: that of add, or of Y). position int32 and
+    weight float32 (N, k); positions outside Y are skipped. out may be add itself."""
+    gpu = _gpu("Y", Y, _TYPES)
+    R, W, ldy = _rows_of("Y", Y, _TYPES, gpu, None, M or 0)
+    M = W if M is None else M
+    if position.dim() != 2:
+        raise ValueError("position must be (N, k)")
+    N, k = position.shape
+    _int32(k=k)
+    _same("position", position, _I32, gpu, (N, k))
+    _same("weight", weight, _F32, gpu, (N, k))
+    if out is not None:
+        dtype = out.dtype
+    elif dtype is None:
+        dtype = Y.dtype if add is None else add.dtype
+    if dtype not in _TYPES:
+        raise ValueError(f"no output of type {dtype}")
+    ldadd = 0 if add is None else _rows_of("add", add, (dtype,), gpu, N, M)[2]
+    if out is None:
+        out, ldo = torch.empty_strided((N, M), (M, 1), dtype=dtype, device=Y.device), M
+    else:
+        ldo = _rows_of("out", out, _TYPES, gpu, N, M)[2]
+    _launch("qg_expert_combine", gpu, Y.data_ptr(), _TYPES[Y.dtype], ldy, R, position.data_ptr(), weight.data_ptr(), k,
+            _ptr(add), ldadd, out.data_ptr(), _TYPES[dtype], ldo, N, M)
+    return out

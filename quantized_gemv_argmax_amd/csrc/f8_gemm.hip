@@ -1,0 +1,966 @@
+// Products on 8-bit floating-point (e4m3) weights and activations with block scales, for
+// gfx950: the load-time layout of the weights, the row quantizer, the product and the
+// product grouped by expert.
+//
+//   y[n, m] = sum_b x_scale[n, b] * w_scale[m / 128, b] * sum_{k in b} xq[n, k] * wq[m, k]  (+ bias[m])
+//
+// over blocks b of 128 values of K. A block is one matrix-core operand (16 x 16 x 128),
+// whose sum is scaled once, by one multiply-add per output.
+#include <algorithm>
+#include <climits>
+
+#include "qg_device.h"
+#include "qg_host.h"
+#include "qg_rows.h"
+
+namespace {
+
+using namespace qg;
+
+constexpr int T = QG_TILE_ROWS;
+constexpr int kB = QG_F8_BLOCK;
+constexpr int kUnit = T * kB;  // bytes of one operand: 16 rows x 128 k
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------------- weight layout
+__global__ __launch_bounds__(256) void pack_f8_kernel(const uint8_t* __restrict__ src, int64_t ldw, int64_t w_expert,
+                                                      uint4* __restrict__ dst, int64_t M, int K, int nb,
+                                                      int64_t mtiles, int64_t units) {
+    const int64_t stride = (int64_t)gridDim.x * 256;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += stride) {
+        const int l = (int)(u & 63);
+        const int64_t th = u >> 6;  // (expert, tile, half of a block)
+        const int64_t t = th / (2 * nb);
+        const int64_t row = t % mtiles * T + (l & 15);
+        const int k0 = (int)(th % (2 * nb)) * (kB / 2) + (l >> 4) * 16;
+        union {
+            uint4 v;
+            uint8_t b[16];
+        } o;
+        o.v = make_uint4(0, 0, 0, 0);
+        if (row < M) {
+            typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(1)));  // rows start anywhere
+            const uint8_t* p = src + t / mtiles * w_expert + row * ldw + k0;
+            if (k0 + 16 <= K) {
+                const vec v = *reinterpret_cast<const vec*>(p);
+                o.v = make_uint4(v.x, v.y, v.z, v.w);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (k0 + e < K) o.b[e] = p[e];
+            }
+        }
+        dst[u] = o.v;
+    }
+}
+
+// ---------------------------------------------------------------- row quantizer
+// The largest of a value's 16 lanes, in all of them (DPP: within quads, then across them).
+QG_DEV uint32_t row_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));   // quad_perm [1, 0, 3, 2]
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));   // quad_perm [2, 3, 0, 1]
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));  // row_half_mirror
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));  // row_mirror
+}
+
+// x / d rounded to e4m3's three bits after the leading one (from 2^-6 on; multiples of
+// 2^-9 below), ties to even, decided on the exact quotient: in double precision the
+// quotient of two floats is never rounded onto a border that it does not meet.
+QG_DEV float round_exact(float x, float d) {
+    const double v = (double)x / (double)d, a = fabs(v);
+    const int e = a < 0x1p-6 ? -6 : ilogb(a);
+    return (float)ldexp(rint(ldexp(v, 3 - e)), e - 3);
+}
+
+// Eight values divided by d, as e4m3 bytes. x * inv is off by two units in the last place
+// at most; where it lies within four of a border between two results, the exact quotient
+// decides.
+QG_DEV uint2 quant8(const float (&x)[8], float d, float inv) {
+    float t[8];
+    bool near = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        t[e] = x[e] * inv;
+        float a = fabsf(t[e]);
+        if (a < 0x1p-6f) a += 0x1p-6f;  // (below 2^-6 the borders are those of the next octave, shifted)
+        near |= ((__builtin_bit_cast(uint32_t, a) + 4u - 0x80000u) & 0xfffffu) <= 8u;
+    }
+    if (near) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = round_exact(x[e], d);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = fminf(fmaxf(t[e], -448.f), 448.f);  // (over it where the scale is subnormal)
+    uint2 o;
+    o.x = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+    o.x = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], o.x, true);
+    o.y = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
+    o.y = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], o.y, true);
+    return o;
+}
+
+struct QArgs {
+    const void* x;
+    int64_t ldx;
+    const int32_t* count;  // rows to do, or NULL
+    uint8_t* q;
+    int64_t ldq;
+    float* scale;
+    int64_t lds;
+    int32_t N, K;
+    uint32_t quads;  // quads: groups of four blocks of a row
+};
+
+// Sixteen lanes per block of 128, a wavefront per four blocks, U of them at a time.
+template <int XT, bool GATED, int U>
+__global__ __launch_bounds__(256) void quantize_f8_kernel(QArgs a) {
+    typedef typename XVec<XT>::E E;
+    constexpr int VN = XVec<XT>::N, V = 8 / VN;  // vectors of a lane's eight values
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t rows = a.count ? min(max(*a.count, 0), a.N) : a.N;
+    const uint32_t total = rows * a.quads;  // below 2^31
+    for (uint32_t first = (blockIdx.x * 4 + wave) * U; first < total; first += gridDim.x * 4 * U) {
+    uint4 v[U][V], g[GATED ? U : 1][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t at = first + u;
+        if (at < total) {
+            const uint32_t n = at / a.quads;
+            const int k = (int)(at - n * a.quads) * 4 * kB + lane * 8;
+            const E* p = reinterpret_cast<const E*>(a.x) + n * a.ldx;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[u][i] = row_vec<XT>(p, a.K, k / VN + i);
+                if constexpr (GATED) {
+                    g[u][i] = v[u][i];
+                    v[u][i] = row_vec<XT>(p + a.K, a.K, k / VN + i);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t at = first + u;
+        if (at >= total) return;
+        const uint32_t n = at / a.quads;
+        const int b = (int)(at - n * a.quads) * 4 + (lane >> 4);
+        float x[8];
+        uint32_t mx = 0;  // the largest |x| by its bits: above every finite value an infinity, above it a NaN
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = XVec<XT>::get(v[u][e / VN], e % VN);
+            if constexpr (GATED) {
+                const float z = XVec<XT>::get(g[u][e / VN], e % VN);
+                x[e] *= z / (1.f + expf(-z));
+            }
+            mx = max(mx, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
+        }
+        mx = row_max(mx);
+        const bool finite = mx < 0x7f800000u;
+        const float d0 = finite ? __builtin_bit_cast(float, mx) / 448.f : __builtin_nanf("");
+        const bool ok = d0 > 0.f;
+        // tiny scales: x and d scaled alike (exactly), so that 1/d stays finite
+        const float s = d0 < 0x1p-90f ? 0x1p60f : 1.f;
+        const float d = ok ? d0 * s : 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = ok ? x[e] * s : 0.f;
+        const uint2 o = quant8(x, d, 1.f / d);
+        const bool in = b * kB < a.K;
+        if (in) *reinterpret_cast<uint2*>(a.q + n * a.ldq + b * kB + (lane & 15) * 8) = o;
+        if ((lane & 15) == 0) a.scale[n * a.lds + b] = in ? d0 : 0.f;
+    }
+    }
+}
+
+// ---------------------------------------------------------------- product
+struct GArgs {
+    const uint8_t* w;
+    const float* ws;
+    const uint8_t* x;
+    int64_t ldx;
+    const float* xs;
+    int64_t ldxs;
+    const float* bias;
+    void* Y;
+    int64_t ldy;
+    const int32_t* offsets;  // grouped: rows offsets[e] .. offsets[e + 1] of Y meet expert e
+    const int32_t* row;      // grouped: rows of x that rows of Y come from, or NULL: the same
+    qg_f4* part;             // partial sums of a product split along K
+    int32_t M, N, X;         // N: rows of Y, X: rows of x
+    int32_t E, nb, mb;       // experts, blocks of 128 along K and M
+    int32_t mtiles;          // 16-row tiles of an expert's weights
+    int32_t kper;            // blocks of a split
+    int32_t total;           // tiles of Y
+};
+
+// Rows of Y that meet one expert.
+struct Group {
+    int e, r0, r1;
+};
+
+QG_DEV void group_range(const GArgs& a, int e, int& r0, int& r1) {
+    r0 = r1 = 0;
+    if (e < a.E) {
+        r0 = min(max(a.offsets[e], 0), a.N);
+        r1 = min(max(a.offsets[e + 1], r0), a.N);
+    }
+}
+
+// The slot-th expert that has rows; false if there are fewer. By every wavefront alike.
+QG_DEV bool used_group(const GArgs& a, int slot, Group& g) {
+    const int lane = threadIdx.x & 63;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        int r0, r1;
+        group_range(a, e0 + lane, r0, r1);
+        const uint64_t used = __ballot(r1 > r0);
+        const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(used >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)used, 0));
+        const uint64_t hit = __ballot(r1 > r0 && before == slot);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            g = {e0 + l, __builtin_amdgcn_readlane(r0, l), __builtin_amdgcn_readlane(r1, l)};
+            return true;
+        }
+        slot -= __builtin_popcountll(used);
+    }
+    return false;
+}
+
+QG_DEV int source_row(const GArgs& a, int r) { return a.row ? min(max(a.row[r], 0), a.X - 1) : r; }
+
+// Eight e4m3 values as fp16, exactly.
+QG_DEV h8 to_half(uint32_t lo, uint32_t hi) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    union {
+        h2 p[4];
+        h8 v;
+    } o;
+    o.p[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
+    o.p[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
+    o.p[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
+    o.p[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+    return o.v;
+}
+
+// A 16 x 128 operand in a lane: row lane % 16, k = 16 (lane / 16) .. + 15 of each half.
+union Op8 {
+    v8i v;
+    qi4 h[2];
+};
+struct Op16 {
+    h8 v[4];
+    QG_DEV void set(const Op8& o) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = to_half((uint32_t)o.v[2 * i], (uint32_t)o.v[2 * i + 1]);
+    }
+};
+// The 16 x 16 sums of one block. On the 8-bit matrix cores, which align each eight
+// products to the largest and keep 13 bits below its leading one (measured with single
+// products: one of 2^-13 of the largest counts, of 2^-14 it does not), so that a block's
+// sum is off by 1.5e-5 for normally distributed values: for outputs that are rounded to
+// 2^-9 or 2^-12 in the end ...
+QG_DEV qg_f4 block_sum(const Op8& a, const Op8& b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, qg_f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+// ... and on the fp16 ones at half the rate, exactly but for the float32 additions.
+QG_DEV qg_f4 block_sum(const Op16& a, const Op16& b) {
+    qg_f4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], s, 0, 0, 0);
+    return s;
+}
+QG_DEV void add_scaled(qg_f4& acc, const qg_f4& s, float scale) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(s[e], scale, acc[e]);
+}
+
+// The biases of C consecutive weight rows from m on, rows beyond M repeating the last one.
+template <int C>
+QG_DEV void row_bias(const GArgs& a, int e, int m, float (&sb)[C]) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) sb[i] = a.bias ? a.bias[(int64_t)e * a.M + min(m + i, a.M - 1)] : 0.f;
+}
+
+// ---------------------------------------------------------------- few rows
+// One 16-row tile of an expert's weights and NB blocks of 16 rows of Y per workgroup; its
+// KW wavefronts take blocks of K in turn, and their sums meet in LDS, in order. The
+// weights go from memory straight to registers, in the packed order.
+template <int YT, int NB, int KW>
+__global__ __launch_bounds__(64 * KW) void gemm_f8_stream_kernel(GArgs a) {
+    __shared__ qg_f4 part[KW][NB][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = blockIdx.x, slot = blockIdx.y;
+    Group g = {0, 0, a.N};
+    if (a.offsets && !used_group(a, slot, g)) return;
+    const uint8_t* w = a.w + ((size_t)g.e * a.mtiles + t) * a.nb * kUnit + lane * 16;
+    const float* ws = a.ws + ((size_t)g.e * a.mb + t * T / kB) * a.nb;
+    for (int c0 = g.r0; c0 < g.r1; c0 += 16 * NB) {
+        const uint8_t* xr[NB];
+        const float* sr[NB];
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {  // rows beyond the last repeat it; their sums are not stored
+            const int64_t r = source_row(a, min(c0 + 16 * c + (lane & 15), g.r1 - 1));
+            xr[c] = a.x + r * a.ldx + (lane >> 4) * 16;
+            sr[c] = a.xs + r * a.ldxs;
+        }
+        qg_f4 acc[NB];
+#pragma unroll
+        for (int c = 0; c < NB; ++c) acc[c] = qg_f4{0.f, 0.f, 0.f, 0.f};
+        Op8 wv[2], xv[2][NB];
+        float sv[2][NB];
+        auto load = [&](int p, int b) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                wv[p].h[h] = __builtin_nontemporal_load(reinterpret_cast<const qi4*>(w + (size_t)b * kUnit + h * 1024));
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) xv[p][c].h[h] = *reinterpret_cast<const qi4*>(xr[c] + b * kB + h * 64);
+                sv[p][c] = sr[c][b] * ws[b];
+            }
+        };
+        auto mma = [&](int p) {
+            Op16 wh, xh;
+            wh.set(wv[p]);
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+                xh.set(xv[p][c]);
+                add_scaled(acc[c], block_sum(wh, xh), sv[p][c]);
+            }
+        };
+        int b = wave;
+        for (; b + KW < a.nb; b += 2 * KW) {
+            load(0, b);
+            load(1, b + KW);
+            mma(0);
+            mma(1);
+        }
+        if (b < a.nb) {
+            load(0, b);
+            mma(0);
+        }
+#pragma unroll
+        for (int c = 0; c < NB; ++c) part[wave][c][lane] = acc[c];
+        __syncthreads();
+        if (wave < NB) {
+            const int c = wave, n = c0 + 16 * c + (lane & 15), m = t * T + (lane >> 4) * 4;
+            qg_f4 s = part[0][c][lane];
+#pragma unroll
+            for (int k = 1; k < KW; ++k) s += part[k][c][lane];
+            if (n < g.r1 && m < a.M) {
+                float sb[4], y[4];
+                row_bias(a, g.e, m, sb);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = s[e] + sb[e];
+                store_row<YT>(a.Y, n * a.ldy + m, y, a.M - m);
+            }
+        }
+        __syncthreads();  // (the next rows' sums go to the same places)
+    }
+}
+
+// ---------------------------------------------------------------- many rows
+// Tiles of Y (Tile in qg_rows.h: a K tile of 128 bytes is one block). Beside a tile's
+// stages LDS holds the row scales of eight blocks, twice.
+template <int BM, int BN, int WM, int WN, int NS>
+struct F8Tile : Tile<BM, BN, WM, WN, NS> {
+    typedef Tile<BM, BN, WM, WN, NS> P;
+    static constexpr int SB = 2 * BN * 16;       // bytes of the scales of eight blocks
+    static constexpr int SU = 2 * BN / 64;       // 1 KB loads of them
+    static constexpr int LDS = P::LDS + 2 * SB;
+    static_assert(BM / WM <= kB && kB % (BM / WM) == 0 && BN % 64 == 0, "a wavefront's rows share a weight scale");
+};
+
+// Outputs of a wavefront's accumulators. Product i of a pair (2c, 2c + 1) holds in its
+// row 4 q + e the weight row 32 c + 8 q + 4 (i % 2) + e, so a lane's pair is eight
+// consecutive outputs and four lanes' pairs are 32.
+template <int YT, int CT>
+QG_DEV void store_pair(const GArgs& a, const qg_f4 (&lo)[CT], const qg_f4 (&hi)[CT], const float (&sb)[8], int m, int n0,
+                       int n1) {
+    const int count = a.M - m;
+    if (count <= 0) return;
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+        const int n = n0 + 16 * j;
+        if (n < n1) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[e] = lo[j][e] + sb[e];
+                y[4 + e] = hi[j][e] + sb[4 + e];
+            }
+            store_row<YT>(a.Y, n * a.ldy + m, y, count);
+        }
+    }
+}
+
+// The bound of a buffer's loads, whose offsets are 32 bits.
+QG_DEV int buffer_bytes(int64_t n) { return (int)(uint32_t)min(n, (int64_t)0xffffffffll); }
+
+// Tile of a grouped product: the experts' tiles of BN rows in order, each with all of its
+// weight tiles; the XCDs take contiguous runs. False beyond the last one.
+struct GroupTile {
+    Group g;
+    int t0, n0;  // first 16-row weight tile, first row of Y
+};
+template <int BM, int BN>
+QG_DEV bool group_tile_at(const GArgs& a, int id, GroupTile& o) {
+    const int lane = threadIdx.x & 63;
+    const int mts = (a.mtiles * 16 + BM - 1) / BM;
+    int all = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        int r0, r1;
+        group_range(a, e0 + lane, r0, r1);
+        int n = (r1 - r0 + BN - 1) / BN;
+#pragma unroll
+        for (int m = 32; m; m >>= 1) n += __shfl_xor(n, m);
+        all += n;
+    }
+    const int total = all * mts, q = total / 8, r = total % 8, x = id % 8;
+    if (id / 8 >= q + (x < r)) return false;
+    id = x * q + min(x, r) + id / 8;
+    int left = id / mts;
+    o.t0 = (id - left * mts) * (BM / 16);
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        int r0, r1;
+        group_range(a, e0 + lane, r0, r1);
+        const int n = (r1 - r0 + BN - 1) / BN;
+        int upto = n;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int v = __shfl_up(upto, m);
+            if (lane >= m) upto += v;
+        }
+        const uint64_t hit = __ballot(left < upto);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            o.g = {e0 + l, __builtin_amdgcn_readlane(r0, l), __builtin_amdgcn_readlane(r1, l)};
+            o.n0 = o.g.r0 + (left - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l))) * BN;
+            return true;
+        }
+        left -= __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+
+template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
+    typedef F8Tile<BM, BN, WM, WN, NS> G;
+    // float32 outputs take the exact block sums, 16-bit ones the faster 8-bit matrix cores
+    typedef typename std::conditional<YT == QG_F32, Op16, Op8>::type Op;
+    extern __shared__ __align__(1024) uint8_t lds[];
+    uint8_t* const sl = lds + G::P::LDS;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int k0 = SPLIT ? blockIdx.y * a.kper : 0;
+    const int k1 = SPLIT ? min(a.nb, k0 + a.kper) : a.nb;
+
+    // Loads: rows and tiles beyond the operands repeat the last ones (their sums are
+    // not stored). Weights arrive in the packed order. Activations: eight lanes per row
+    // of 128 bytes, the 16-byte chunk c of row r at place c ^ (r % 8), which spreads
+    // the operand reads over the banks.
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    const int wm = wave % WM, wn = wave / WM;
+    __amdgpu_buffer_rsrc_t wr, xr, sr;
+    uint32_t woff[G::AU], xoff[G::XU], soff;
+    const float* ws;
+    int t0, n0, n1, e = 0;
+    auto aim = [&](int id) {
+        int64_t xbase = 0;
+        if constexpr (GROUPED) {
+            GroupTile at;
+            if (!group_tile_at<BM, BN>(a, id, at)) return false;
+            e = at.g.e;
+            t0 = at.t0;
+            n0 = at.n0;
+            n1 = at.g.r1;
+        } else {
+            const TileAt at = tile_at<BM, BN>(a.mtiles, a.N, id);
+            t0 = at.t0;
+            n0 = at.n0;
+            n1 = a.N;
+        }
+        if (!GROUPED || !a.row) xbase = n0;
+        const int64_t rows = GROUPED && a.row ? a.X : n1 - n0;
+        wr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + ((size_t)e * a.mtiles + t0) * a.nb * kUnit), (short)0,
+                                               buffer_bytes((int64_t)(a.mtiles - t0) * a.nb * kUnit),
+                                               kQgRawBufferFlags);
+        xr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.x + xbase * a.ldx), (short)0,
+                                               buffer_bytes((rows - 1) * a.ldx + a.nb * kB),
+                                               kQgRawBufferFlags);
+        sr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.xs + xbase * a.ldxs), (short)0,
+                                               buffer_bytes(((rows - 1) * a.ldxs + ((a.nb + 3) & ~3)) * 4),
+                                               kQgRawBufferFlags);
+        ws = a.ws + ((size_t)e * a.mb + min((t0 * T + wm * (BM / WM)) / kB, a.mb - 1)) * a.nb;
+        auto from = [&](int c) {  // the row, from xbase on, that column c of the tile comes from
+            const int n = min(n0 + c, n1 - 1);
+            return (uint32_t)(GROUPED && a.row ? source_row(a, n) : n - n0);
+        };
+#pragma unroll
+        for (int u = 0; u < G::AU; ++u)
+            woff[u] = (uint32_t)min((wave * G::AU + u) >> 1, a.mtiles - 1 - t0) * (uint32_t)a.nb * kUnit + lane * 16u;
+#pragma unroll
+        for (int u = 0; u < G::XU; ++u)
+            xoff[u] = from((wave * G::XU + u) * 8 + (lane >> 3)) * (uint32_t)a.ldx + chunk * 16u;
+        soff = from(wave % (BN / 64) * 64 + lane) * (uint32_t)a.ldxs * 4u;
+        return true;
+    };
+    auto fetch = [&](int t, int buf) {
+        uint8_t* A = lds + buf * G::STAGE;
+        uint8_t* X = A + G::AB;
+        if (t == k0 || (t & 7) == 0) {
+            // scales of the blocks 8 (t / 8) .. + 7, four to a load (wavefronts beyond the units repeat some)
+            const int unit = wave % G::SU, c = min((t >> 3) * 2 + unit / (BN / 64), (a.nb - 1) >> 2);
+            lds_load(sr, sl + ((t >> 3) & 1) * G::SB + unit * 1024, soff, c * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < G::AU; ++u) {
+            const int unit = wave * G::AU + u;
+            lds_load(wr, A + unit * 1024, woff[u], (2 * t + (unit & 1)) * 1024);
+        }
+#pragma unroll
+        for (int u = 0; u < G::XU; ++u) lds_load(xr, X + (wave * G::XU + u) * 1024, xoff[u], t * kB);
+    };
+    auto start = [&]() {
+#pragma unroll
+        for (int i = 0; i < NS - 1; ++i)
+            if (k0 + i < k1) fetch(k0 + i, i);
+    };
+
+    const int r = lane & 15, q = lane >> 4;
+    qg_f4 acc[G::MT][G::CT];
+    const int arow = (wm * G::MT + (r >> 3)) * kUnit + (q * 16 + ((r >> 2) & 1) * 8 + (r & 3)) * 16;
+    const int xrow = (wn * G::CT * 16 + r) * 128;
+    auto read = [](Op& o, const uint8_t* p0, const uint8_t* p1) {
+        Op8 v;
+        v.h[0] = *reinterpret_cast<const qi4*>(p0);
+        v.h[1] = *reinterpret_cast<const qi4*>(p1);
+        if constexpr (YT == QG_F32)
+            o.set(v);
+        else
+            o = v;
+    };
+    constexpr int U = G::AU + G::XU;
+    int id = blockIdx.x;
+    if (!aim(id)) return;
+    start();
+    while (true) {
+#pragma unroll
+        for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j) acc[i][j] = qg_f4{0.f, 0.f, 0.f, 0.f};
+        int buf = 0;
+        float wsn = ws[k0];
+        for (int t = k0; t < k1; ++t) {
+            // tile t has arrived, and the buffer of tile t - 1 has been read by all
+            const float wsv = wsn;
+            if (t + NS - 1 <= k1)
+                tile_sync<(NS - 2) * U>();
+            else
+                tile_sync<0>();
+            wsn = ws[min(t + 1, k1 - 1)];
+            if (t + NS - 1 < k1) fetch(t + NS - 1, buf ? buf - 1 : NS - 1);
+            const uint8_t* A = lds + buf * G::STAGE + arow;
+            const uint8_t* X = lds + buf * G::STAGE + G::AB + xrow;
+            const uint8_t* S = sl + ((t >> 3) & 1) * G::SB + ((t >> 2) & 1) * (BN * 16) + (wn * G::CT * 16 + r) * 16 + (t & 3) * 4;
+            Op fx[G::CT];
+            float sc[G::CT];
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j) {
+                read(fx[j], X + j * 2048 + ((q ^ (r & 7)) * 16), X + j * 2048 + (((4 + q) ^ (r & 7)) * 16));
+                sc[j] = *reinterpret_cast<const float*>(S + j * 256) * wsv;
+            }
+#pragma unroll
+            for (int i = 0; i < G::MT; ++i) {
+                Op fa;
+                const uint8_t* p = A + (i >> 1) * (2 * kUnit) + (i & 1) * 64;
+                read(fa, p, p + 1024);
+#pragma unroll
+                for (int j = 0; j < G::CT; ++j) add_scaled(acc[i][j], block_sum(fa, fx[j]), sc[j]);
+            }
+            buf = buf + 1 == NS ? 0 : buf + 1;
+        }
+        const int m0 = (t0 + wm * G::MT) * 16 + q * 8, c0 = n0 + wn * G::CT * 16 + r;
+        if constexpr (SPLIT) {
+            qg_f4* p = a.part + ((((size_t)blockIdx.y * gridDim.x + blockIdx.x) * G::W + wave) * (G::MT * G::CT)) * 64 + lane;
+#pragma unroll
+            for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < G::CT; ++j) p[(i * G::CT + j) * 64] = acc[i][j];
+            return;
+        } else {
+            const int last = n1, eb = e;
+            id += gridDim.x;
+            bool more = id < a.total;
+            if (more) {
+                tile_sync<0>();  // the last tile's buffer has been read by all
+                more = aim(id);
+                if (more) start();
+            }
+#pragma unroll
+            for (int c = 0; c < G::MT / 2; ++c) {
+                float sb[8];
+                row_bias(a, eb, m0 + 32 * c, sb);
+                store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb, m0 + 32 * c, c0, last);
+            }
+            if (!more) return;
+        }
+    }
+}
+
+// The partial sums of a split product added in order and stored: one wavefront per pair
+// of a tile wavefront's products.
+template <int YT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64) void gemm_f8_join_kernel(GArgs a, int tiles, int splits) {
+    typedef Tile<BM, BN, WM, WN, 2> G;
+    const int lane = threadIdx.x;
+    const int c = blockIdx.x % (G::MT / 2), wave = blockIdx.x / (G::MT / 2) % G::W;
+    const int id = blockIdx.x / (G::MT / 2 * G::W);
+    const TileAt at = tile_at<BM, BN>(a.mtiles, a.N, id);
+    const int wm = wave % WM, wn = wave / WM, r = lane & 15, q = lane >> 4;
+    const qg_f4* p = a.part + (((size_t)id * G::W + wave) * (G::MT * G::CT) + 2 * c * G::CT) * 64 + lane;
+    const size_t step = (size_t)tiles * G::W * (G::MT * G::CT) * 64;
+    const int m = (at.t0 + wm * G::MT + 2 * c) * 16 + q * 8, n = at.n0 + wn * G::CT * 16 + r;
+    float sb[8];
+    row_bias(a, 0, m, sb);
+    qg_f4 lo[G::CT], hi[G::CT];
+#pragma unroll
+    for (int j = 0; j < G::CT; ++j) lo[j] = hi[j] = qg_f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s, p += step)
+#pragma unroll
+        for (int j = 0; j < G::CT; ++j) {
+            lo[j] += p[j * 64];
+            hi[j] += p[(G::CT + j) * 64];
+        }
+    store_pair<YT, G::CT>(a, lo, hi, sb, m, n, a.N);
+}
+
+// ---------------------------------------------------------------- launches
+enum { FORM_STREAM, FORM_64, FORM_128, FORM_256 };
+struct Plan {
+    int form, tiles, splits, kper;
+    size_t ws;
+};
+
+Plan plan(int64_t M, int64_t K, int64_t N, int y_type) {
+    Plan p{};
+    const int kt = (int)qg::ceil_div(K, kB);
+    p.splits = 1;
+    p.kper = kt;
+    auto tiles = [&](int b) { return qg::ceil_div(M, b) * qg::ceil_div(N, b); };
+    if (N <= 32) {
+        p.form = FORM_STREAM;
+        p.tiles = (int)qg::ceil_div(M, T);
+        return p;
+    }
+    int side = 64;
+    if (N > 64 && tiles(256) >= 192 && y_type != QG_F32)
+        side = 256;
+    else if (N > 64 && (tiles(128) >= 128 || kt >= 64))
+        side = 128;
+    p.tiles = (int)tiles(side);
+    p.form = side == 256 ? FORM_256 : side == 64 ? FORM_64 : FORM_128;
+    const int s = side == 256 ? 1 : std::min(256 / p.tiles, kt / (side == 128 ? 18 : 28));
+    if (s > 1) {
+        p.kper = (int)qg::ceil_div(kt, s);
+        p.splits = (int)qg::ceil_div(kt, p.kper);
+        p.ws = (size_t)p.splits * p.tiles * side * side * 4;
+    }
+    return p;
+}
+
+template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
+qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
+    typedef F8Tile<BM, BN, WM, WN, NS> G;
+    const int groups = BM == 256 ? std::min(p.tiles, qg::device_cus()) : p.tiles;
+    if constexpr (G::LDS > 65536) {
+        static std::atomic<bool> done[64];
+        const qg_status st = allow_lds(
+            reinterpret_cast<const void*>(&gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, SPLIT, GROUPED>), G::LDS, done);
+        if (st) return st;
+    }
+    hipLaunchKernelGGL((gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, SPLIT, GROUPED>), dim3(groups, p.splits),
+                       dim3(64 * G::W), G::LDS, s, a);
+    qg_status st = qg::launch_status("qgemm_f8");
+    if constexpr (SPLIT) {
+        if (st) return st;
+        hipLaunchKernelGGL((gemm_f8_join_kernel<YT, BM, BN, WM, WN>), dim3(p.tiles * G::W * (G::MT / 2)), dim3(64), 0, s,
+                           a, p.tiles, p.splits);
+        st = qg::launch_status("qgemm_f8 (join)");
+    }
+    return st;
+}
+
+template <int YT>
+qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
+    const bool split = p.splits > 1;
+    switch (p.form) {
+        case FORM_64:
+            return split ? launch_tiles<YT, 64, 64, 2, 2, 4, true, false>(a, p, s)
+                         : launch_tiles<YT, 64, 64, 2, 2, 4, false, false>(a, p, s);
+        case FORM_128:
+            return split ? launch_tiles<YT, 128, 128, 2, 4, 3, true, false>(a, p, s)
+                         : launch_tiles<YT, 128, 128, 2, 4, 3, false, false>(a, p, s);
+        case FORM_256:
+            if constexpr (YT != QG_F32) return launch_tiles<YT, 256, 256, 2, 4, 2, false, false>(a, p, s);
+    }
+    if (a.N <= 16)
+        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
+    else
+        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 2, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
+    return qg::launch_status("qgemm_f8");
+}
+
+template <int YT>
+qg_status launch_grouped(const GArgs& a, hipStream_t s) {
+    const int64_t used = std::min(a.E, a.N);  // experts that can have rows
+    const int64_t each = qg::ceil_div(a.N, used);
+    Plan p{};
+    p.splits = 1;
+    p.kper = a.nb;
+    auto tiles = [&](int bm, int bn) {
+        return (int)((std::min<int64_t>(a.N, a.N / bn + used)) * qg::ceil_div(a.mtiles * 16, bm));
+    };
+    GArgs b = a;
+    if (each <= 32) {
+        const dim3 g(a.mtiles, (unsigned)used);
+        if (each <= 12)
+            hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), g, dim3(512), 0, s, a);
+        else
+            hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 2, 8>), g, dim3(512), 0, s, a);
+        return qg::launch_status("qgemm_f8_grouped");
+    }
+    if (each <= 96) {
+        b.total = p.tiles = tiles(64, 64);
+        return launch_tiles<YT, 64, 64, 2, 2, 4, false, true>(b, p, s);
+    }
+    b.total = p.tiles = tiles(128, 128);
+    return launch_tiles<YT, 128, 128, 2, 4, 3, false, true>(b, p, s);
+}
+
+qg_status check_mk(int64_t M, int64_t K) {
+    if (M < 1 || M > QG_F8_MAX_ROWS)
+        return qg::fail(QG_ERR_SHAPE, "M=%lld not in [1, %d]", (long long)M, QG_F8_MAX_ROWS);
+    if (K < 1 || K > QG_F8_MAX_K)
+        return qg::fail(QG_ERR_SHAPE, "K=%lld not in [1, %d]", (long long)K, QG_F8_MAX_K);
+    return QG_OK;
+}
+
+constexpr int64_t kMost = (int64_t)1 << 40;
+
+template <int XT, bool GATED>
+void launch_quantize(const QArgs& a, hipStream_t s) {
+    const int64_t quads = (int64_t)a.N * a.quads;
+    if (quads >= 16384)
+        hipLaunchKernelGGL((quantize_f8_kernel<XT, GATED, 4>), dim3((unsigned)std::min<int64_t>(qg::ceil_div(quads, 16), 1 << 22)), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((quantize_f8_kernel<XT, GATED, 1>), dim3((unsigned)qg::ceil_div(quads, 4)), dim3(256), 0, s, a);
+}
+
+// What the dense and the grouped product check alike. rows: rows of x.
+qg_status check_operands(const void* w, const float* ws, const void* xq, int64_t ldx, const float* xs, int64_t ldxs,
+                         const float* bias, const void* Y, int y_type, int64_t ldy, int64_t M, int64_t K, int64_t N,
+                         int64_t rows, int64_t experts) {
+    if (!w || !ws || !xq || !xs || !Y) return qg::fail(QG_ERR_NULL, "NULL pointer (w_packed, w_scale, xq, x_scale, Y)");
+    if (!known_type(y_type)) return qg::fail(QG_ERR_SHAPE, "y_type=%d unknown", y_type);
+    const qg_status st = check_mk(M, K);
+    if (st) return st;
+    if (experts < 1 || experts > QG_EXPERTS_MAX)
+        return qg::fail(QG_ERR_SHAPE, "experts=%lld not in [1, %d]", (long long)experts, QG_EXPERTS_MAX);
+    const int64_t nb = qg::ceil_div(K, kB), kp = nb * kB;
+    if (N < 1 || N > QG_F8_MAX_ROWS || M * N > (int64_t)1 << 32)
+        return qg::fail(QG_ERR_SHAPE, "%lld rows not in [1, %d], or times M over 2^32", (long long)N, QG_F8_MAX_ROWS);
+    if (rows < 1 || rows > QG_F8_MAX_ROWS)
+        return qg::fail(QG_ERR_SHAPE, "%lld rows of xq not in [1, %d]", (long long)rows, QG_F8_MAX_ROWS);
+    if (ldx < kp || ldx > (1 << 22) || ldx % 16)  // 256 rows stay within 32-bit offsets
+        return qg::fail(QG_ERR_SHAPE, "ldx=%lld not a multiple of 16 in [%lld, 2^22]", (long long)ldx, (long long)kp);
+    if (ldxs < nb || ldxs > (1 << 20) || ldxs % 4)
+        return qg::fail(QG_ERR_SHAPE, "ldxs=%lld not a multiple of 4 in [%lld, 2^20]", (long long)ldxs, (long long)nb);
+    if (ldy < M || ldy > kMost / N || ldy % 4)
+        return qg::fail(QG_ERR_SHAPE, "ldy=%lld not a multiple of 4 in [M, 2^40 / N]", (long long)ldy);
+    if (!qg::aligned16(w) || !qg::aligned16(xq) || !qg::aligned16(xs) || !qg::aligned16(Y))
+        return qg::fail(QG_ERR_ALIGN, "w_packed, xq, x_scale and Y must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(ws) | reinterpret_cast<uintptr_t>(bias)) & 3)
+        return qg::fail(QG_ERR_ALIGN, "w_scale and bias must be 4-byte aligned");
+    return QG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qg_f8_bytes(int64_t M, int64_t K, int64_t experts) {
+    if (M < 1 || M > QG_F8_MAX_ROWS || K < 1 || K > QG_F8_MAX_K || experts < 1 || experts > QG_EXPERTS_MAX) return 0;
+    const int64_t one = qg::ceil_div(M, T) * qg::ceil_div(K, kB) * kUnit;
+    return one > kMost / experts ? 0 : (size_t)(one * experts);
+}
+
+qg_status qg_pack_f8(const void* w, int64_t ldw, int64_t w_expert, void* dst, int64_t M, int64_t K, int64_t experts,
+                     qg_stream_t stream) {
+    qg::clear_error();
+    if (!w || !dst) return qg::fail(QG_ERR_NULL, "NULL pointer (w, dst)");
+    qg_status st = check_mk(M, K);
+    if (st) return st;
+    const size_t n = qg_f8_bytes(M, K, experts);
+    if (!n) return qg::fail(QG_ERR_SHAPE, "experts=%lld not in [1, %d], or over 2^40 bytes", (long long)experts, QG_EXPERTS_MAX);
+    if (ldw < K || ldw > kMost / M) return qg::fail(QG_ERR_SHAPE, "ldw=%lld not in [K, 2^40 / M]", (long long)ldw);
+    if (experts > 1 && (w_expert < (M - 1) * ldw + K || w_expert > kMost / experts))
+        return qg::fail(QG_ERR_SHAPE, "w_expert=%lld: experts overlap, or over 2^40 bytes", (long long)w_expert);
+    if (!qg::aligned16(dst)) return qg::fail(QG_ERR_ALIGN, "dst not 16-byte aligned");
+    const size_t src = (size_t)(experts > 1 ? (experts - 1) * w_expert : 0) + (M - 1) * ldw + K;
+    if (overlap(w, src, dst, n)) return qg::fail(QG_ERR_SHAPE, "w and dst overlap");
+    st = qg::check_device();
+    if (st) return st;
+    const int64_t units = (int64_t)(n / 16);
+    const unsigned g = (unsigned)std::min<int64_t>(qg::ceil_div(units, 256), 65536);
+    hipLaunchKernelGGL(pack_f8_kernel, dim3(g), dim3(256), 0, (hipStream_t)stream, (const uint8_t*)w, ldw, w_expert,
+                       (uint4*)dst, M, (int)K, (int)qg::ceil_div(K, kB), qg::ceil_div(M, T), units);
+    return qg::launch_status("qg_pack_f8");
+}
+
+qg_status qg_quantize_f8_rows(const void* x, int x_type, int64_t ldx, int gated, const int32_t* count, int64_t N, int64_t K,
+                              void* q, int64_t ldq, float* scale, int64_t lds, qg_stream_t stream) {
+    qg::clear_error();
+    if (!x || !q || !scale) return qg::fail(QG_ERR_NULL, "NULL pointer (x, q, scale)");
+    if (!known_type(x_type)) return qg::fail(QG_ERR_SHAPE, "x_type=%d unknown", x_type);
+    if (gated != 0 && gated != 1) return qg::fail(QG_ERR_SHAPE, "gated=%d not 0 or 1", gated);
+    if (N < 1 || N > QG_F8_MAX_ROWS)
+        return qg::fail(QG_ERR_SHAPE, "N=%lld not in [1, %d]", (long long)N, QG_F8_MAX_ROWS);
+    if (K < 1 || K > QG_F8_MAX_K) return qg::fail(QG_ERR_SHAPE, "K=%lld not in [1, %d]", (long long)K, QG_F8_MAX_K);
+    const int64_t nb = qg::ceil_div(K, kB), width = gated ? 2 * K : K, most = kMost / N;
+    const int64_t sp = qg::ceil_div(nb, 4) * 4;
+    if (ldx < width || ldx > most)
+        return qg::fail(QG_ERR_SHAPE, "ldx=%lld not in [%lld, 2^40 / N]", (long long)ldx, (long long)width);
+    if (ldq < nb * kB || ldq > most || ldq % 16)
+        return qg::fail(QG_ERR_SHAPE, "ldq=%lld not a multiple of 16 in [%lld, 2^40 / N]", (long long)ldq, (long long)(nb * kB));
+    if (lds < sp || lds > most || lds % 4)
+        return qg::fail(QG_ERR_SHAPE, "lds=%lld not a multiple of 4 in [%lld, 2^40 / N]", (long long)lds, (long long)sp);
+    const int eb = elem_bytes(x_type);
+    if (reinterpret_cast<uintptr_t>(x) % eb) return qg::fail(QG_ERR_ALIGN, "x not aligned to its elements");
+    if (!qg::aligned16(q) || !qg::aligned16(scale)) return qg::fail(QG_ERR_ALIGN, "q and scale must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(count) & 3) return qg::fail(QG_ERR_ALIGN, "count not 4-byte aligned");
+    const size_t xb = ((size_t)(N - 1) * ldx + width) * eb, qb = (size_t)(N - 1) * ldq + nb * kB;
+    const size_t sb = ((size_t)(N - 1) * lds + sp) * 4;
+    if (overlap(x, xb, q, qb) || overlap(x, xb, scale, sb) || overlap(q, qb, scale, sb) ||
+        (count && (overlap(count, 4, q, qb) || overlap(count, 4, scale, sb))))
+        return qg::fail(QG_ERR_SHAPE, "x, count, q and scale overlap");
+    qg_status st = qg::check_device();
+    if (st) return st;
+    QArgs a{x, ldx, count, (uint8_t*)q, ldq, scale, lds, (int32_t)N, (int32_t)K, (uint32_t)(sp / 4)};
+    hipStream_t s = (hipStream_t)stream;
+    if (x_type == QG_F32)
+        gated ? launch_quantize<QG_F32, true>(a, s) : launch_quantize<QG_F32, false>(a, s);
+    else if (x_type == QG_F16)
+        gated ? launch_quantize<QG_F16, true>(a, s) : launch_quantize<QG_F16, false>(a, s);
+    else
+        gated ? launch_quantize<QG_BF16, true>(a, s) : launch_quantize<QG_BF16, false>(a, s);
+    return qg::launch_status("qg_quantize_f8_rows");
+}
+
+size_t qgemm_f8_workspace_bytes(int64_t M, int64_t K, int64_t N, int y_type) {
+    if (!qg_f8_bytes(M, K, 1) || N < 1 || N > QG_F8_MAX_ROWS || M * N > (int64_t)1 << 32 || !known_type(y_type)) return 0;
+    return plan(M, K, N, y_type).ws;
+}
+
+qg_status qgemm_f8(const void* w, const float* ws, const void* xq, int64_t ldx, const float* xs, int64_t ldxs,
+                   const float* bias, void* Y, int y_type, int64_t ldy, int64_t M, int64_t K, int64_t N,
+                   void* workspace, size_t workspace_bytes, qg_stream_t stream) {
+    qg::clear_error();
+    qg_status st = check_operands(w, ws, xq, ldx, xs, ldxs, bias, Y, y_type, ldy, M, K, N, N, 1);
+    if (st) return st;
+    const int64_t nb = qg::ceil_div(K, kB), mb = qg::ceil_div(M, kB);
+    const size_t yb = ((size_t)(N - 1) * ldy + M) * elem_bytes(y_type), xb = (size_t)(N - 1) * ldx + nb * kB;
+    const size_t sb = ((size_t)(N - 1) * ldxs + qg::ceil_div(nb, 4) * 4) * 4, wb = qg_f8_bytes(M, K, 1), wsb = (size_t)mb * nb * 4;
+    auto over = [&](const void* p, size_t n) {
+        return overlap(p, n, xq, xb) || overlap(p, n, w, wb) || overlap(p, n, ws, wsb) || overlap(p, n, xs, sb) ||
+               (bias && overlap(p, n, bias, (size_t)M * 4));
+    };
+    if (over(Y, yb)) return qg::fail(QG_ERR_SHAPE, "Y overlaps an input");
+    const Plan p = plan(M, K, N, y_type);
+    if (p.ws) {
+        if (!workspace || workspace_bytes < p.ws)
+            return qg::fail(QG_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", p.ws, workspace ? workspace_bytes : 0);
+        if (!qg::aligned16(workspace)) return qg::fail(QG_ERR_ALIGN, "workspace not 16-byte aligned");
+        if (over(workspace, p.ws) || overlap(workspace, p.ws, Y, yb))
+            return qg::fail(QG_ERR_SHAPE, "the workspace overlaps an operand");
+    }
+    st = qg::check_device();
+    if (st) return st;
+    GArgs a{};
+    a.w = (const uint8_t*)w;
+    a.ws = ws;
+    a.x = (const uint8_t*)xq;
+    a.ldx = ldx;
+    a.xs = xs;
+    a.ldxs = ldxs;
+    a.bias = bias;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.part = (qg_f4*)workspace;
+    a.M = (int32_t)M;
+    a.N = a.X = (int32_t)N;
+    a.E = 1;
+    a.nb = (int32_t)nb;
+    a.mb = (int32_t)mb;
+    a.mtiles = (int32_t)qg::ceil_div(M, T);
+    a.kper = p.kper;
+    a.total = p.tiles;
+    hipStream_t s = (hipStream_t)stream;
+    if (y_type == QG_F32) return launch_gemm<QG_F32>(a, p, s);
+    if (y_type == QG_F16) return launch_gemm<QG_F16>(a, p, s);
+    return launch_gemm<QG_BF16>(a, p, s);
+}
+
+qg_status qgemm_f8_grouped(const qg_f8_grouped* g, qg_stream_t stream) {
+    qg::clear_error();
+    if (!g) return qg::fail(QG_ERR_NULL, "NULL pointer (problem)");
+    qg_status st = check_operands(g->w_packed, g->w_scale, g->xq, g->ldx, g->x_scale, g->ldxs, g->bias, g->Y, g->y_type,
+                                  g->ldy, g->M, g->K, g->rows, g->x_rows, g->experts);
+    if (st) return st;
+    if (!g->offsets) return qg::fail(QG_ERR_NULL, "NULL pointer (offsets)");
+    if ((reinterpret_cast<uintptr_t>(g->offsets) | reinterpret_cast<uintptr_t>(g->row)) & 3)
+        return qg::fail(QG_ERR_ALIGN, "offsets and row must be 4-byte aligned");
+    if (!g->row && g->x_rows < g->rows)
+        return qg::fail(QG_ERR_SHAPE, "x_rows=%lld below rows=%lld without `row`", (long long)g->x_rows, (long long)g->rows);
+    const int64_t nb = qg::ceil_div(g->K, kB), mb = qg::ceil_div(g->M, kB);
+    const size_t xb = (size_t)(g->x_rows - 1) * g->ldx + nb * kB, sb = ((size_t)(g->x_rows - 1) * g->ldxs + qg::ceil_div(nb, 4) * 4) * 4;
+    if (g->row && (xb > UINT32_MAX || sb > UINT32_MAX))
+        return qg::fail(QG_ERR_SHAPE, "xq or x_scale of 2^32 bytes or more with `row`");
+    const size_t wb = qg_f8_bytes(g->M, g->K, g->experts);
+    if (!wb) return qg::fail(QG_ERR_SHAPE, "weights of over 2^40 bytes");
+    const size_t yb = ((size_t)(g->rows - 1) * g->ldy + g->M) * elem_bytes(g->y_type);
+    if (overlap(g->Y, yb, g->xq, xb) || overlap(g->Y, yb, g->w_packed, wb) || overlap(g->Y, yb, g->x_scale, sb) ||
+        overlap(g->Y, yb, g->w_scale, (size_t)g->experts * mb * nb * 4) ||
+        overlap(g->Y, yb, g->offsets, (size_t)(g->experts + 1) * 4) || (g->row && overlap(g->Y, yb, g->row, (size_t)g->rows * 4)) ||
+        (g->bias && overlap(g->Y, yb, g->bias, (size_t)g->experts * g->M * 4)))
+        return qg::fail(QG_ERR_SHAPE, "Y overlaps an input");
+    st = qg::check_device();
+    if (st) return st;
+    GArgs a{};
+    a.w = (const uint8_t*)g->w_packed;
+    a.ws = g->w_scale;
+    a.x = (const uint8_t*)g->xq;
+    a.ldx = g->ldx;
+    a.xs = g->x_scale;
+    a.ldxs = g->ldxs;
+    a.bias = g->bias;
+    a.Y = g->Y;
+    a.ldy = g->ldy;
+    a.offsets = g->offsets;
+    a.row = g->row;
+    a.M = (int32_t)g->M;
+    a.N = (int32_t)g->rows;
+    a.X = (int32_t)g->x_rows;
+    a.E = (int32_t)g->experts;
+    a.nb = (int32_t)nb;
+    a.mb = (int32_t)mb;
+    a.mtiles = (int32_t)qg::ceil_div(g->M, T);
+    hipStream_t s = (hipStream_t)stream;
+    if (g->y_type == QG_F32) return launch_grouped<QG_F32>(a, s);
+    if (g->y_type == QG_F16) return launch_grouped<QG_F16>(a, s);
+    return launch_grouped<QG_BF16>(a, s);
+}
+
+}  // extern "C"
