@@ -362,14 +362,17 @@ __global__ __launch_bounds__(64 * KW) void gemm_f8_stream_kernel(GArgs a) {
 
 // ---------------------------------------------------------------- many rows
 // Tiles of Y (Tile in qg_rows.h: a K tile of 128 bytes is one block). Beside a tile's
-// stages LDS holds the row scales of eight blocks, twice.
+// stages LDS holds the row scales and each wavefront's weight scales of eight blocks,
+// twice, and of a grouped product the experts' first tiles.
 template <int BM, int BN, int WM, int WN, int NS>
 struct F8Tile : Tile<BM, BN, WM, WN, NS> {
     typedef Tile<BM, BN, WM, WN, NS> P;
-    static constexpr int SB = 2 * BN * 16;       // bytes of the scales of eight blocks
-    static constexpr int SU = 2 * BN / 64;       // 1 KB loads of them
+    static constexpr int SU = 2 * BN / 64;            // 1 KB loads of the row scales of eight blocks
+    static constexpr int SB = SU * 1024 + P::W * 256;  // bytes of all scales of eight blocks
     static constexpr int LDS = P::LDS + 2 * SB;
+    static constexpr int NP = P::MT / 2;              // pairs of 16-row weight operands
     static_assert(BM / WM <= kB && kB % (BM / WM) == 0 && BN % 64 == 0, "a wavefront's rows share a weight scale");
+    static_assert(NP % 2 == 0, "the pairs alternate between two sets of registers");
 };
 
 // Outputs of a wavefront's accumulators. Product i of a pair (2c, 2c + 1) holds in its
@@ -398,30 +401,12 @@ QG_DEV void store_pair(const GArgs& a, const qg_f4 (&lo)[CT], const qg_f4 (&hi)[
 // The bound of a buffer's loads, whose offsets are 32 bits.
 QG_DEV int buffer_bytes(int64_t n) { return (int)(uint32_t)min(n, (int64_t)0xffffffffll); }
 
-// Tile of a grouped product: the experts' tiles of BN rows in order, each with all of its
-// weight tiles; the XCDs take contiguous runs. False beyond the last one.
-struct GroupTile {
-    Group g;
-    int t0, n0;  // first 16-row weight tile, first row of Y
-};
-template <int BM, int BN>
-QG_DEV bool group_tile_at(const GArgs& a, int id, GroupTile& o) {
+// The tiles of BN rows before each expert's, in LDS, by the first wavefront; returns the
+// number of all of them to it.
+template <int BN>
+QG_DEV int first_tiles(const GArgs& a, int* first) {
     const int lane = threadIdx.x & 63;
-    const int mts = (a.mtiles * 16 + BM - 1) / BM;
     int all = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        int r0, r1;
-        group_range(a, e0 + lane, r0, r1);
-        int n = (r1 - r0 + BN - 1) / BN;
-#pragma unroll
-        for (int m = 32; m; m >>= 1) n += __shfl_xor(n, m);
-        all += n;
-    }
-    const int total = all * mts, q = total / 8, r = total % 8, x = id % 8;
-    if (id / 8 >= q + (x < r)) return false;
-    id = x * q + min(x, r) + id / 8;
-    int left = id / mts;
-    o.t0 = (id - left * mts) * (BM / 16);
     for (int e0 = 0; e0 < a.E; e0 += 64) {
         int r0, r1;
         group_range(a, e0 + lane, r0, r1);
@@ -432,16 +417,41 @@ QG_DEV bool group_tile_at(const GArgs& a, int id, GroupTile& o) {
             const int v = __shfl_up(upto, m);
             if (lane >= m) upto += v;
         }
-        const uint64_t hit = __ballot(left < upto);
-        if (hit) {
-            const int l = __builtin_ctzll(hit);
-            o.g = {e0 + l, __builtin_amdgcn_readlane(r0, l), __builtin_amdgcn_readlane(r1, l)};
-            o.n0 = o.g.r0 + (left - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l))) * BN;
-            return true;
-        }
-        left -= __builtin_amdgcn_readlane(upto, 63);
+        first[e0 + lane] = all + upto - n;
+        all += __builtin_amdgcn_readlane(upto, 63);
     }
-    return false;
+    return all;
+}
+
+// Tile of a grouped product: the experts' tiles of BN rows in order, each with all of its
+// weight tiles; the XCDs take contiguous runs. False beyond the last one.
+struct GroupTile {
+    Group g;
+    int t0, n0;  // first 16-row weight tile, first row of Y
+};
+template <int BM, int BN>
+QG_DEV bool group_tile_at(const GArgs& a, const int* first, int all, int id, GroupTile& o) {
+    const int lane = threadIdx.x & 63;
+    const int mts = (a.mtiles * 16 + BM - 1) / BM;
+    const int total = all * mts, q = total / 8, r = total % 8, x = id % 8;
+    if (id / 8 >= q + (x < r)) return false;
+    id = x * q + min(x, r) + id / 8;
+    const int at = id / mts;
+    o.t0 = (id - at * mts) * (BM / 16);
+    // the last expert whose first tile is not beyond this one (it has rows: one without would share
+    // its first tile with the next)
+    int e = -1;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        const int c = __builtin_popcountll(__ballot(e0 + lane < a.E && first[e0 + lane] <= at));
+        e += c;
+        if (c < 64) break;
+    }
+    o.g.e = e;
+    const int r0 = min(max(a.offsets[e], 0), a.N);
+    o.g.r0 = __builtin_amdgcn_readfirstlane(r0);
+    o.g.r1 = __builtin_amdgcn_readfirstlane(min(max(a.offsets[e + 1], r0), a.N));
+    o.n0 = o.g.r0 + (at - __builtin_amdgcn_readfirstlane(first[e])) * BN;
+    return true;
 }
 
 template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
@@ -451,10 +461,20 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
     typedef typename std::conditional<YT == QG_F32, Op16, Op8>::type Op;
     extern __shared__ __align__(1024) uint8_t lds[];
     uint8_t* const sl = lds + G::P::LDS;
+    int* const first = reinterpret_cast<int*>(lds + G::LDS);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int k0 = SPLIT ? blockIdx.y * a.kper : 0;
     const int k1 = SPLIT ? min(a.nb, k0 + a.kper) : a.nb;
+    int all = 0;
+    if constexpr (GROUPED) {
+        if (wave == 0) {
+            all = first_tiles<BN>(a, first + 1);
+            if (lane == 0) first[0] = all;
+        }
+        __syncthreads();
+        all = __builtin_amdgcn_readfirstlane(first[0]);
+    }
 
     // Loads: rows and tiles beyond the operands repeat the last ones (their sums are
     // not stored). Weights arrive in the packed order. Activations: eight lanes per row
@@ -462,15 +482,16 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
     // the operand reads over the banks.
     const int chunk = (lane & 7) ^ (lane >> 3);
     const int wm = wave % WM, wn = wave / WM;
-    __amdgpu_buffer_rsrc_t wr, xr, sr;
+    const uint8_t *wp, *xp;
+    int wbytes, xbytes;
+    __amdgpu_buffer_rsrc_t sr, vr;
     uint32_t woff[G::AU], xoff[G::XU], soff;
-    const float* ws;
     int t0, n0, n1, e = 0;
     auto aim = [&](int id) {
         int64_t xbase = 0;
         if constexpr (GROUPED) {
             GroupTile at;
-            if (!group_tile_at<BM, BN>(a, id, at)) return false;
+            if (!group_tile_at<BM, BN>(a, first + 1, all, id, at)) return false;
             e = at.g.e;
             t0 = at.t0;
             n0 = at.n0;
@@ -483,16 +504,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         }
         if (!GROUPED || !a.row) xbase = n0;
         const int64_t rows = GROUPED && a.row ? a.X : n1 - n0;
-        wr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + ((size_t)e * a.mtiles + t0) * a.nb * kUnit), (short)0,
-                                               buffer_bytes((int64_t)(a.mtiles - t0) * a.nb * kUnit),
-                                               kQgRawBufferFlags);
-        xr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.x + xbase * a.ldx), (short)0,
-                                               buffer_bytes((rows - 1) * a.ldx + a.nb * kB),
-                                               kQgRawBufferFlags);
+        wp = a.w + ((size_t)e * a.mtiles + t0) * a.nb * kUnit;
+        wbytes = buffer_bytes((int64_t)(a.mtiles - t0) * a.nb * kUnit);
+        xp = a.x + xbase * a.ldx;
+        xbytes = buffer_bytes((rows - 1) * a.ldx + a.nb * kB);
         sr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.xs + xbase * a.ldxs), (short)0,
-                                               buffer_bytes(((rows - 1) * a.ldxs + ((a.nb + 3) & ~3)) * 4),
+                                               buffer_bytes(((rows - 1) * a.ldxs + ((a.nb + 3) & ~3)) * 4), kQgRawBufferFlags);
+        const int mblock = min((t0 * T + wm * (BM / WM)) / kB, a.mb - 1);
+        vr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.ws + ((size_t)e * a.mb + mblock) * a.nb), (short)0, a.nb * 4,
                                                kQgRawBufferFlags);
-        ws = a.ws + ((size_t)e * a.mb + min((t0 * T + wm * (BM / WM)) / kB, a.mb - 1)) * a.nb;
         auto from = [&](int c) {  // the row, from xbase on, that column c of the tile comes from
             const int n = min(n0 + c, n1 - 1);
             return (uint32_t)(GROUPED && a.row ? source_row(a, n) : n - n0);
@@ -506,42 +526,140 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         soff = from(wave % (BN / 64) * 64 + lane) * (uint32_t)a.ldxs * 4u;
         return true;
     };
-    auto fetch = [&](int t, int buf) {
+    // Scales of the blocks 8 g .. + 7: the row scales four blocks to a load (wavefronts beyond
+    // the units repeat some), and eight weight scales.
+    auto fetch_scales = [&](int g) {
+        uint8_t* S = sl + (g & 1) * G::SB;
+        const int unit = wave % G::SU, c = min(g * 2 + unit / (BN / 64), (a.nb - 1) >> 2);
+        lds_load(sr, S + unit * 1024, soff, c * 16);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_ptr)(S + G::SU * 1024 + wave * 256), 4, (lane & 7) * 4, g * 32, 0, 0);
+    };
+    // Part `part` of `parts` of the stage of K tile t. Beyond the last one every load is out of
+    // its buffer's bounds and reads nothing, so that the loop needs no branch.
+    constexpr int U = G::AU + G::XU;
+    auto fetch = [&](int t, int buf, int part, int parts) {
         uint8_t* A = lds + buf * G::STAGE;
         uint8_t* X = A + G::AB;
-        if (t == k0 || (t & 7) == 0) {
-            // scales of the blocks 8 (t / 8) .. + 7, four to a load (wavefronts beyond the units repeat some)
-            const int unit = wave % G::SU, c = min((t >> 3) * 2 + unit / (BN / 64), (a.nb - 1) >> 2);
-            lds_load(sr, sl + ((t >> 3) & 1) * G::SB + unit * 1024, soff, c * 16);
-        }
+        const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wp, (short)0, t < k1 ? wbytes : 0, kQgRawBufferFlags);
+        const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)xp, (short)0, t < k1 ? xbytes : 0, kQgRawBufferFlags);
 #pragma unroll
-        for (int u = 0; u < G::AU; ++u) {
-            const int unit = wave * G::AU + u;
-            lds_load(wr, A + unit * 1024, woff[u], (2 * t + (unit & 1)) * 1024);
+        for (int u = part * U / parts; u < (part + 1) * U / parts; ++u) {
+            if (u < G::AU) {
+                const int unit = wave * G::AU + u;
+                lds_load(wr, A + unit * 1024, woff[u], (2 * t + (unit & 1)) * 1024);
+            } else {
+                lds_load(xr, X + (wave * G::XU + u - G::AU) * 1024, xoff[u - G::AU], t * kB);
+            }
         }
-#pragma unroll
-        for (int u = 0; u < G::XU; ++u) lds_load(xr, X + (wave * G::XU + u) * 1024, xoff[u], t * kB);
     };
     auto start = [&]() {
+        fetch_scales(k0 >> 3);
+        fetch(k0, 0, 0, 1);
 #pragma unroll
-        for (int i = 0; i < NS - 1; ++i)
-            if (k0 + i < k1) fetch(k0 + i, i);
+        for (int i = 1; i < NS; ++i) {
+            if (((k0 + i) & 7) == 0 && k0 + i < k1) fetch_scales((k0 + i) >> 3);
+            fetch(k0 + i, i, 0, 1);
+        }
     };
 
     const int r = lane & 15, q = lane >> 4;
     qg_f4 acc[G::MT][G::CT];
     const int arow = (wm * G::MT + (r >> 3)) * kUnit + (q * 16 + ((r >> 2) & 1) * 8 + (r & 3)) * 16;
-    const int xrow = (wn * G::CT * 16 + r) * 128;
-    auto read = [](Op& o, const uint8_t* p0, const uint8_t* p1) {
-        Op8 v;
-        v.h[0] = *reinterpret_cast<const qi4*>(p0);
-        v.h[1] = *reinterpret_cast<const qi4*>(p1);
-        if constexpr (YT == QG_F32)
-            o.set(v);
-        else
-            o = v;
+    const int xrow = G::AB + (wn * G::CT * 16 + r) * 128;
+    const int x0 = xrow + ((q ^ (r & 7)) * 16), x1 = xrow + (((4 + q) ^ (r & 7)) * 16);
+    const int srow = (wn * G::CT * 16 + r) * 16;
+    auto get = [](Op8& o, const uint8_t* p0, const uint8_t* p1) {
+        o.h[0] = *reinterpret_cast<const qi4*>(p0);
+        o.h[1] = *reinterpret_cast<const qi4*>(p1);
     };
-    constexpr int U = G::AU + G::XU;
+    auto get_pair = [&](Op8(&o)[2], int buf, int p) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint8_t* A = lds + buf * G::STAGE + arow + p * (2 * kUnit) + i * 64;
+            get(o[i], A, A + 1024);
+        }
+    };
+    auto get_col = [&](Op8& o, int buf, int j) { get(o, lds + buf * G::STAGE + x0 + j * 2048, lds + buf * G::STAGE + x1 + j * 2048); };
+    struct Scales {
+        float x[G::CT], w;
+    };
+    auto get_scales = [&](Scales& s, int t) {
+        const uint8_t* S = sl + ((t >> 3) & 1) * G::SB;
+        const uint8_t* X = S + ((t >> 2) & 1) * (BN * 16) + srow + (t & 3) * 4;
+#pragma unroll
+        for (int j = 0; j < G::CT; ++j) s.x[j] = *reinterpret_cast<const float*>(X + j * 256);
+        s.w = *reinterpret_cast<const float*>(S + G::SU * 1024 + wave * 256 + (t & 7) * 4);
+    };
+    auto as = [](const Op8& o) {
+        Op v;
+        if constexpr (YT == QG_F32)
+            v.set(o);
+        else
+            v = o;
+        return v;
+    };
+
+    // A tile's products run pair by pair of weight operands, each pair over the columns, and
+    // the sums of a step are scaled and added during the next one. The operands of a pair
+    // are read during the pair before; before the last pair, whose operands are then in registers, a barrier: the
+    // tile's buffer can be refilled, with the tile NS later, and the next tile has arrived, whose
+    // operands and scales are read as the last pair frees their registers.
+    Op8 fa[2][2], fx[G::CT];
+    Op cx[G::CT];
+    Scales sc;
+    float sx[G::CT], sl1;
+    qg_f4 sum[2];
+    auto tile = [&](auto last, int t, int buf, int nbuf) {
+        constexpr bool LAST = decltype(last)::value;
+#pragma unroll
+        for (int j = 0; j < G::CT; ++j) {
+            sx[j] = sc.x[j] * sc.w;
+            if constexpr (YT == QG_F32) cx[j] = as(fx[j]);
+        }
+#pragma unroll
+        for (int p = 0; p < G::NP; ++p) {
+            if (p == G::NP - 1 && !LAST) {
+                tile_sync<(NS - 2) * U>();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            Op ca[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ca[i] = as(fa[p & 1][i]);
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j) {
+                qg_f4 now[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (YT == QG_F32)
+                        now[i] = block_sum(ca[i], cx[j]);
+                    else
+                        now[i] = block_sum(ca[i], fx[j]);
+                }
+                // the step before
+                const int pj = j ? j - 1 : G::CT - 1, pp = j ? p : p ? p - 1 : G::NP - 1;
+                const float s = j || p ? sx[pj] : sl1;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    add_scaled(acc[2 * pp + i][pj], sum[i], s);
+                    // (left free, the last tile's additions move behind it and its sums to scratch memory)
+                    if constexpr (LAST) asm volatile("" : "+v"(acc[2 * pp + i][pj]));
+                    sum[i] = now[i];
+                }
+                if (p + 1 < G::NP) {
+                    if (j == 0) get_pair(fa[(p + 1) & 1], buf, p + 1);
+                } else if constexpr (!LAST) {
+                    if (j == 0) {
+                        get_scales(sc, t + 1);
+                        get_pair(fa[0], nbuf, 0);
+                    }
+                    get_col(fx[j], nbuf, j);
+                    fetch(t + NS, buf, j, G::CT);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        sl1 = sx[G::CT - 1];
+    };
     int id = blockIdx.x;
     if (!aim(id)) return;
     start();
@@ -550,39 +668,26 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         for (int i = 0; i < G::MT; ++i)
 #pragma unroll
             for (int j = 0; j < G::CT; ++j) acc[i][j] = qg_f4{0.f, 0.f, 0.f, 0.f};
-        int buf = 0;
-        float wsn = ws[k0];
-        for (int t = k0; t < k1; ++t) {
-            // tile t has arrived, and the buffer of tile t - 1 has been read by all
-            const float wsv = wsn;
-            if (t + NS - 1 <= k1)
-                tile_sync<(NS - 2) * U>();
-            else
-                tile_sync<0>();
-            wsn = ws[min(t + 1, k1 - 1)];
-            if (t + NS - 1 < k1) fetch(t + NS - 1, buf ? buf - 1 : NS - 1);
-            const uint8_t* A = lds + buf * G::STAGE + arow;
-            const uint8_t* X = lds + buf * G::STAGE + G::AB + xrow;
-            const uint8_t* S = sl + ((t >> 3) & 1) * G::SB + ((t >> 2) & 1) * (BN * 16) + (wn * G::CT * 16 + r) * 16 + (t & 3) * 4;
-            Op fx[G::CT];
-            float sc[G::CT];
+        sum[0] = sum[1] = qg_f4{0.f, 0.f, 0.f, 0.f};
+        sl1 = 0.f;
+        tile_sync<(NS - 1) * U>();
+        get_scales(sc, k0);
+        get_pair(fa[0], 0, 0);
 #pragma unroll
-            for (int j = 0; j < G::CT; ++j) {
-                read(fx[j], X + j * 2048 + ((q ^ (r & 7)) * 16), X + j * 2048 + (((4 + q) ^ (r & 7)) * 16));
-                sc[j] = *reinterpret_cast<const float*>(S + j * 256) * wsv;
-            }
-#pragma unroll
-            for (int i = 0; i < G::MT; ++i) {
-                Op fa;
-                const uint8_t* p = A + (i >> 1) * (2 * kUnit) + (i & 1) * 64;
-                read(fa, p, p + 1024);
-#pragma unroll
-                for (int j = 0; j < G::CT; ++j) add_scaled(acc[i][j], block_sum(fa, fx[j]), sc[j]);
-            }
-            buf = buf + 1 == NS ? 0 : buf + 1;
+        for (int j = 0; j < G::CT; ++j) get_col(fx[j], 0, j);
+        int t = k0, buf = 0;
+        for (; t + 1 < k1; ++t) {
+            const int nbuf = buf + 1 == NS ? 0 : buf + 1;
+            if (((t + NS) & 7) == 0 && t + NS < k1) fetch_scales((t + NS) >> 3);
+            tile(std::false_type{}, t, buf, nbuf);
+            buf = nbuf;
         }
+        tile(std::true_type{}, t, buf, buf);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) add_scaled(acc[G::MT - 2 + i][G::CT - 1], sum[i], sl1);
         const int m0 = (t0 + wm * G::MT) * 16 + q * 8, c0 = n0 + wn * G::CT * 16 + r;
         if constexpr (SPLIT) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (loads beyond the last tile)
             qg_f4* p = a.part + ((((size_t)blockIdx.y * gridDim.x + blockIdx.x) * G::W + wave) * (G::MT * G::CT)) * 64 + lane;
 #pragma unroll
             for (int i = 0; i < G::MT; ++i)
@@ -590,19 +695,18 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
                 for (int j = 0; j < G::CT; ++j) p[(i * G::CT + j) * 64] = acc[i][j];
             return;
         } else {
-            const int last = n1, eb = e;
+            // A workgroup with another tile to do sends that tile's first loads before it
+            // stores this one's outputs.
+            const int rows = n1, expert = e;
             id += gridDim.x;
-            bool more = id < a.total;
-            if (more) {
-                tile_sync<0>();  // the last tile's buffer has been read by all
-                more = aim(id);
-                if (more) start();
-            }
+            tile_sync<0>();  // the last tile's buffer has been read by all (and loads beyond it are done)
+            const bool more = id < a.total && aim(id);
+            if (more) start();
 #pragma unroll
-            for (int c = 0; c < G::MT / 2; ++c) {
+            for (int c = 0; c < G::NP; ++c) {
                 float sb[8];
-                row_bias(a, eb, m0 + 32 * c, sb);
-                store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb, m0 + 32 * c, c0, last);
+                row_bias(a, expert, m0 + 32 * c, sb);
+                store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb, m0 + 32 * c, c0, rows);
             }
             if (!more) return;
         }
@@ -674,15 +778,17 @@ Plan plan(int64_t M, int64_t K, int64_t N, int y_type) {
 template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
 qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
     typedef F8Tile<BM, BN, WM, WN, NS> G;
-    const int groups = BM == 256 ? std::min(p.tiles, qg::device_cus()) : p.tiles;
-    if constexpr (G::LDS > 65536) {
-        static std::atomic<bool> done[64];
-        const qg_status st = allow_lds(
-            reinterpret_cast<const void*>(&gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, SPLIT, GROUPED>), G::LDS, done);
-        if (st) return st;
-    }
+    constexpr int most = G::LDS + (GROUPED ? (QG_EXPERTS_MAX + 64) * 4 : 0);  // (one number, and whole 64s of experts)
+    static_assert(most <= 160 * 1024, "LDS of a compute unit");
+    const int lds = G::LDS + (GROUPED ? (1 + (a.E + 63) / 64 * 64) * 4 : 0);
+    // a workgroup takes tile after tile, as many of them at a time as there is LDS for
+    const int groups = SPLIT ? p.tiles : std::min(p.tiles, qg::device_cus() * (160 * 1024 / lds));
+    static std::atomic<bool> done[64];
+    const qg_status lst =
+        allow_lds(reinterpret_cast<const void*>(&gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, SPLIT, GROUPED>), most, done);
+    if (lst) return lst;
     hipLaunchKernelGGL((gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, SPLIT, GROUPED>), dim3(groups, p.splits),
-                       dim3(64 * G::W), G::LDS, s, a);
+                       dim3(64 * G::W), lds, s, a);
     qg_status st = qg::launch_status("qgemm_f8");
     if constexpr (SPLIT) {
         if (st) return st;
@@ -698,11 +804,11 @@ qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
     const bool split = p.splits > 1;
     switch (p.form) {
         case FORM_64:
-            return split ? launch_tiles<YT, 64, 64, 2, 2, 4, true, false>(a, p, s)
-                         : launch_tiles<YT, 64, 64, 2, 2, 4, false, false>(a, p, s);
+            return split ? launch_tiles<YT, 64, 64, 1, 4, 4, true, false>(a, p, s)
+                         : launch_tiles<YT, 64, 64, 1, 4, 4, false, false>(a, p, s);
         case FORM_128:
-            return split ? launch_tiles<YT, 128, 128, 2, 4, 3, true, false>(a, p, s)
-                         : launch_tiles<YT, 128, 128, 2, 4, 3, false, false>(a, p, s);
+            return split ? launch_tiles<YT, 128, 128, 2, 2, 2, true, false>(a, p, s)
+                         : launch_tiles<YT, 128, 128, 2, 2, 2, false, false>(a, p, s);
         case FORM_256:
             if constexpr (YT != QG_F32) return launch_tiles<YT, 256, 256, 2, 4, 2, false, false>(a, p, s);
     }
@@ -734,10 +840,10 @@ qg_status launch_grouped(const GArgs& a, hipStream_t s) {
     }
     if (each <= 96) {
         b.total = p.tiles = tiles(64, 64);
-        return launch_tiles<YT, 64, 64, 2, 2, 4, false, true>(b, p, s);
+        return launch_tiles<YT, 64, 64, 1, 4, 4, false, true>(b, p, s);
     }
     b.total = p.tiles = tiles(128, 128);
-    return launch_tiles<YT, 128, 128, 2, 4, 3, false, true>(b, p, s);
+    return launch_tiles<YT, 128, 128, 2, 2, 2, false, true>(b, p, s);
 }
 
 qg_status check_mk(int64_t M, int64_t K) {
