@@ -596,8 +596,9 @@ qg_status qg_beam_reorder_check(const qg_beam_state* states /* host */, int coun
  * qg_pack_f8 lays the weights out once, at load time: `experts` matrices (1 for a dense
  * product) of M rows of K bytes, rows ldw >= K bytes apart, matrices w_expert bytes apart
  * (ignored for one). The packed buffer has qg_f8_bytes(M, K, experts) bytes: per
- * matrix rows padded to 16 and K to 128 with zeros, and the 16 bytes k = 128 b + 64 h +
- * 16 g .. + 15 of row 16 t + i at (((t * ceil(K / 128) + b) * 2 + h) * 64 + 16 g + i) * 16.
+ * matrix rows padded to 32 and K to 128 with zeros, and the 16 bytes k = 128 b + 64 h +
+ * 16 g .. + 15 of row 32 t + 8 j + 4 i + l (l, i, j below 4, 2, 4) at
+ * ((((2 t + i) * ceil(K / 128) + b) * 2 + h) * 64 + 16 g + 4 j + l) * 16.
  * w needs no alignment and must not overlap dst. 1 <= M <= QG_F8_MAX_ROWS, 1 <= K <=
  * QG_F8_MAX_K, 1 <= experts <= QG_EXPERTS_MAX, at most 2^40 bytes. w_scale: row-major
  * [experts][ceil(M / 128)][ceil(K / 128)].

@@ -18,6 +18,7 @@ namespace {
 using namespace qg;
 
 constexpr int T = QG_TILE_ROWS;
+constexpr int kPair = 2 * T;  // weight rows of two operands, which share them in fours
 constexpr int kB = QG_F8_BLOCK;
 constexpr int kUnit = T * kB;  // bytes of one operand: 16 rows x 128 k
 
@@ -25,6 +26,9 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------- weight layout
+// Operands in pairs of 32 weight rows: row r of operand i of a pair is the weight row 8 (r /
+// 4) + 4 i + r % 4, so that a lane, which gets four rows of a product, gets eight
+// consecutive ones of a pair's.
 __global__ __launch_bounds__(256) void pack_f8_kernel(const uint8_t* __restrict__ src, int64_t ldw, int64_t w_expert,
                                                       uint4* __restrict__ dst, int64_t M, int K, int nb,
                                                       int64_t mtiles, int64_t units) {
@@ -32,8 +36,8 @@ __global__ __launch_bounds__(256) void pack_f8_kernel(const uint8_t* __restrict_
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += stride) {
         const int l = (int)(u & 63);
         const int64_t th = u >> 6;  // (expert, tile, half of a block)
-        const int64_t t = th / (2 * nb);
-        const int64_t row = t % mtiles * T + (l & 15);
+        const int64_t t = th / (2 * nb), m = t % mtiles;
+        const int64_t row = m / 2 * kPair + (l >> 2 & 3) * 8 + (m & 1) * 4 + (l & 3);
         const int k0 = (int)(th % (2 * nb)) * (kB / 2) + (l >> 4) * 16;
         union {
             uint4 v;
@@ -344,7 +348,7 @@ __global__ __launch_bounds__(64 * KW) void gemm_f8_stream_kernel(GArgs a) {
         for (int c = 0; c < NB; ++c) part[wave][c][lane] = acc[c];
         __syncthreads();
         if (wave < NB) {
-            const int c = wave, n = c0 + 16 * c + (lane & 15), m = t * T + (lane >> 4) * 4;
+            const int c = wave, n = c0 + 16 * c + (lane & 15), m = (t >> 1) * kPair + (lane >> 4) * 8 + (t & 1) * 4;
             qg_f4 s = part[0][c][lane];
 #pragma unroll
             for (int k = 1; k < KW; ++k) s += part[k][c][lane];
@@ -362,22 +366,23 @@ __global__ __launch_bounds__(64 * KW) void gemm_f8_stream_kernel(GArgs a) {
 
 // ---------------------------------------------------------------- many rows
 // Tiles of Y (Tile in qg_rows.h: a K tile of 128 bytes is one block). Beside a tile's
-// stages LDS holds the row scales and each wavefront's weight scales of eight blocks,
-// twice, and of a grouped product the experts' first tiles.
-template <int BM, int BN, int WM, int WN, int NS>
+// stages LDS holds the row scales and the weight scales of eight blocks, twice, and of a
+// grouped product the experts' first tiles.
+template <int BM, int BN, int WM, int WN, int NS, int H>
 struct F8Tile : Tile<BM, BN, WM, WN, NS> {
     typedef Tile<BM, BN, WM, WN, NS> P;
     static constexpr int SU = 2 * BN / 64;            // 1 KB loads of the row scales of eight blocks
-    static constexpr int SB = SU * 1024 + P::W * 256;  // bytes of all scales of eight blocks
+    static constexpr int MB = (BM + kB - 1) / kB;      // blocks of weight rows
+    static constexpr int SB = SU * 1024 + MB * 256;    // bytes of all scales of eight blocks
     static constexpr int LDS = P::LDS + 2 * SB;
-    static constexpr int NP = P::MT / 2;              // pairs of 16-row weight operands
+    static constexpr int MH = P::MT / H;               // weight operands of a part of a K tile
+    static constexpr int AH = P::AU / H;               // loads of them
+    static_assert(P::W == 8 && MH * H == P::MT && AH * H == P::AU && (H == 1 || (H == 2 && NS == 2)), "parts of a K tile");
     static_assert(BM / WM <= kB && kB % (BM / WM) == 0 && BN % 64 == 0, "a wavefront's rows share a weight scale");
-    static_assert(NP % 2 == 0, "the pairs alternate between two sets of registers");
 };
 
-// Outputs of a wavefront's accumulators. Product i of a pair (2c, 2c + 1) holds in its
-// row 4 q + e the weight row 32 c + 8 q + 4 (i % 2) + e, so a lane's pair is eight
-// consecutive outputs and four lanes' pairs are 32.
+// Outputs of a wavefront's accumulators: a lane's pair is eight consecutive outputs, four
+// lanes' pairs are 32.
 template <int YT, int CT>
 QG_DEV void store_pair(const GArgs& a, const qg_f4 (&lo)[CT], const qg_f4 (&hi)[CT], const float (&sb)[8], int m, int n0,
                        int n1) {
@@ -454,9 +459,9 @@ QG_DEV bool group_tile_at(const GArgs& a, const int* first, int all, int id, Gro
     return true;
 }
 
-template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
+template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool SPLIT, bool GROUPED>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
-    typedef F8Tile<BM, BN, WM, WN, NS> G;
+    typedef F8Tile<BM, BN, WM, WN, NS, H> G;
     // float32 outputs take the exact block sums, 16-bit ones the faster 8-bit matrix cores
     typedef typename std::conditional<YT == QG_F32, Op16, Op8>::type Op;
     extern __shared__ __align__(1024) uint8_t lds[];
@@ -481,12 +486,18 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
     // of 128 bytes, the 16-byte chunk c of row r at place c ^ (r % 8), which spreads
     // the operand reads over the banks.
     const int chunk = (lane & 7) ^ (lane >> 3);
-    const int wm = wave % WM, wn = wave / WM;
+    const int wm = wave % WM, wn = wave / WM, mine = wm * (BM / WM) / kB;  // (wavefronts of one block of rows load its scales alike)
     const uint8_t *wp, *xp;
     int wbytes, xbytes;
     __amdgpu_buffer_rsrc_t sr, vr;
     uint32_t woff[G::AU], xoff[G::XU], soff;
     int t0, n0, n1, e = 0;
+    // 1 KB of weights in a stage that load u of this wavefront brings: the operands of the
+    // first part of every wavefront's rows come first.
+    auto unit_of = [&](int u) {
+        const int h = u / G::AH, g = wave * G::AH + u % G::AH, o = g >> 1;
+        return (o / G::MH * G::MT + h * G::MH + o % G::MH) * 2 + (g & 1);
+    };
     auto aim = [&](int id) {
         int64_t xbase = 0;
         if constexpr (GROUPED) {
@@ -519,7 +530,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         };
 #pragma unroll
         for (int u = 0; u < G::AU; ++u)
-            woff[u] = (uint32_t)min((wave * G::AU + u) >> 1, a.mtiles - 1 - t0) * (uint32_t)a.nb * kUnit + lane * 16u;
+            woff[u] = (uint32_t)min(unit_of(u) >> 1, a.mtiles - 1 - t0) * (uint32_t)a.nb * kUnit + lane * 16u;
 #pragma unroll
         for (int u = 0; u < G::XU; ++u)
             xoff[u] = from((wave * G::XU + u) * 8 + (lane >> 3)) * (uint32_t)a.ldx + chunk * 16u;
@@ -532,39 +543,40 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         uint8_t* S = sl + (g & 1) * G::SB;
         const int unit = wave % G::SU, c = min(g * 2 + unit / (BN / 64), (a.nb - 1) >> 2);
         lds_load(sr, S + unit * 1024, soff, c * 16);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_ptr)(S + G::SU * 1024 + wave * 256), 4, (lane & 7) * 4, g * 32, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_ptr)(S + G::SU * 1024 + mine * 256), 4, (lane & 7) * 4, g * 32, 0, 0);
     };
-    // Part `part` of `parts` of the stage of K tile t. Beyond the last one every load is out of
-    // its buffer's bounds and reads nothing, so that the loop needs no branch.
-    constexpr int U = G::AU + G::XU;
-    auto fetch = [&](int t, int buf, int part, int parts) {
+    // Load u of part `part` of K tile t: its share of the weights, of the first part the
+    // activations too. Beyond the last tile every load is out of its buffer's bounds and reads
+    // nothing, so that the loop needs no branch.
+    constexpr int FIRST = G::AH + G::XU;  // loads of the first part
+    auto fetch = [&](int t, int buf, int part, int u) {
         uint8_t* A = lds + buf * G::STAGE;
-        uint8_t* X = A + G::AB;
-        const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wp, (short)0, t < k1 ? wbytes : 0, kQgRawBufferFlags);
-        const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)xp, (short)0, t < k1 ? xbytes : 0, kQgRawBufferFlags);
-#pragma unroll
-        for (int u = part * U / parts; u < (part + 1) * U / parts; ++u) {
-            if (u < G::AU) {
-                const int unit = wave * G::AU + u;
-                lds_load(wr, A + unit * 1024, woff[u], (2 * t + (unit & 1)) * 1024);
-            } else {
-                lds_load(xr, X + (wave * G::XU + u - G::AU) * 1024, xoff[u - G::AU], t * kB);
-            }
+        if (u < G::AH) {
+            const int v = part * G::AH + u;
+            const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wp, (short)0, t < k1 ? wbytes : 0, kQgRawBufferFlags);
+            lds_load(wr, A + unit_of(v) * 1024, woff[v], (2 * t + (unit_of(v) & 1)) * 1024);
+        } else {
+            const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)xp, (short)0, t < k1 ? xbytes : 0, kQgRawBufferFlags);
+            lds_load(xr, A + G::AB + (wave * G::XU + u - G::AH) * 1024, xoff[u - G::AH], t * kB);
         }
     };
-    auto start = [&]() {
-        fetch_scales(k0 >> 3);
-        fetch(k0, 0, 0, 1);
+    auto fetch_part = [&](int t, int buf, int part) {
 #pragma unroll
-        for (int i = 1; i < NS; ++i) {
-            if (((k0 + i) & 7) == 0 && k0 + i < k1) fetch_scales((k0 + i) >> 3);
-            fetch(k0 + i, i, 0, 1);
+        for (int u = 0; u < (part ? G::AH : FIRST); ++u) fetch(t, buf, part, u);
+    };
+    // What the first turns need.
+    auto start = [&]() {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            if (i == 0 || (((k0 + i) & 7) == 0 && k0 + i < k1)) fetch_scales((k0 + i) >> 3);
+            if (H == 2 || i < NS - 1 || wave >= 4) fetch_part(k0 + i, i, 0);
+            if (H == 2 && (i < NS - 1 || wave >= 4)) fetch_part(k0 + i, i, 1);
         }
     };
 
     const int r = lane & 15, q = lane >> 4;
     qg_f4 acc[G::MT][G::CT];
-    const int arow = (wm * G::MT + (r >> 3)) * kUnit + (q * 16 + ((r >> 2) & 1) * 8 + (r & 3)) * 16;
+    const int arow = wm * G::MT * kUnit + lane * 16;
     const int xrow = G::AB + (wn * G::CT * 16 + r) * 128;
     const int x0 = xrow + ((q ^ (r & 7)) * 16), x1 = xrow + (((4 + q) ^ (r & 7)) * 16);
     const int srow = (wn * G::CT * 16 + r) * 16;
@@ -572,24 +584,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         o.h[0] = *reinterpret_cast<const qi4*>(p0);
         o.h[1] = *reinterpret_cast<const qi4*>(p1);
     };
-    auto get_pair = [&](Op8(&o)[2], int buf, int p) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint8_t* A = lds + buf * G::STAGE + arow + p * (2 * kUnit) + i * 64;
-            get(o[i], A, A + 1024);
-        }
+    auto get_row = [&](Op8& o, int buf, int i) {
+        const uint8_t* A = lds + buf * G::STAGE + arow + i * kUnit;
+        get(o, A, A + 1024);
     };
     auto get_col = [&](Op8& o, int buf, int j) { get(o, lds + buf * G::STAGE + x0 + j * 2048, lds + buf * G::STAGE + x1 + j * 2048); };
-    struct Scales {
-        float x[G::CT], w;
-    };
-    auto get_scales = [&](Scales& s, int t) {
-        const uint8_t* S = sl + ((t >> 3) & 1) * G::SB;
-        const uint8_t* X = S + ((t >> 2) & 1) * (BN * 16) + srow + (t & 3) * 4;
-#pragma unroll
-        for (int j = 0; j < G::CT; ++j) s.x[j] = *reinterpret_cast<const float*>(X + j * 256);
-        s.w = *reinterpret_cast<const float*>(S + G::SU * 1024 + wave * 256 + (t & 7) * 4);
-    };
     auto as = [](const Op8& o) {
         Op v;
         if constexpr (YT == QG_F32)
@@ -599,66 +598,82 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         return v;
     };
 
-    // A tile's products run pair by pair of weight operands, each pair over the columns, and
-    // the sums of a step are scaled and added during the next one. The operands of a pair
-    // are read during the pair before; before the last pair, whose operands are then in registers, a barrier: the
-    // tile's buffer can be refilled, with the tile NS later, and the next tile has arrived, whose
-    // operands and scales are read as the last pair frees their registers.
-    Op8 fa[2][2], fx[G::CT];
-    Op cx[G::CT];
-    Scales sc;
-    float sx[G::CT], sl1;
-    qg_f4 sum[2];
-    auto tile = [&](auto last, int t, int buf, int nbuf) {
-        constexpr bool LAST = decltype(last)::value;
+    // The wavefronts work in two groups of four, one of each on every SIMD, that take turns:
+    // while one multiplies a part of a K tile (its operands are in registers), the other reads
+    // the operands of its next part from LDS and sends loads. A barrier ends each turn.
+    // The second group is a turn behind. A part's place in its buffer has been read by both
+    // groups when the second one's turn on it ends; the loads of the part NS tiles later go there from the
+    // first group's next reading turn on, and have arrived by the barrier before its next turn on that place:
+    // when LATER loads that were sent after them may still be on their way.
+    constexpr int U = G::AU + G::XU, LATER = H == 2 ? U : (NS - 2) * U;
+    Op fa[G::MH], fx[G::CT];
+    float sx[G::CT];
+    // sums of the last products, not added yet
+    constexpr int PRODUCTS = G::MH * G::CT, D = PRODUCTS < 3 ? PRODUCTS : 3;
+    qg_f4 sum[D];
+    auto turn_end = [&](auto wait_lds, auto wait_loads) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(wait_lds)::value) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if constexpr (decltype(wait_loads)::value) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory");
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Adds the sums of the products that the part h before left over.
+    auto flush = [&](int h) {
 #pragma unroll
-        for (int j = 0; j < G::CT; ++j) {
-            sx[j] = sc.x[j] * sc.w;
-            if constexpr (YT == QG_F32) cx[j] = as(fx[j]);
+        for (int d = 0; d < D; ++d) {
+            const int at = PRODUCTS - D + d;
+            add_scaled(acc[h * G::MH + at / G::CT][at % G::CT], sum[at % D], sx[at % G::CT]);
+        }
+    };
+    auto read = [&](int t, int buf, int h) {
+        Op8 ra[G::MH], rx[G::CT];
+        float s[G::CT], w;
+        if (h == 0) {
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j) get_col(rx[j], buf, j);
         }
 #pragma unroll
-        for (int p = 0; p < G::NP; ++p) {
-            if (p == G::NP - 1 && !LAST) {
-                tile_sync<(NS - 2) * U>();
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            Op ca[2];
+        for (int i = 0; i < G::MH; ++i) get_row(ra[i], buf, h * G::MH + i);
+        if (h == 0) {
+            const uint8_t* S = sl + ((t >> 3) & 1) * G::SB;
+            const uint8_t* X = S + ((t >> 2) & 1) * (BN * 16) + srow + (t & 3) * 4;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) ca[i] = as(fa[p & 1][i]);
+            for (int j = 0; j < G::CT; ++j) s[j] = *reinterpret_cast<const float*>(X + j * 256);
+            w = *reinterpret_cast<const float*>(S + G::SU * 1024 + mine * 256 + (t & 7) * 4);
+        }
+        flush(H - 1 - h);
+        if (h == 0) {
 #pragma unroll
             for (int j = 0; j < G::CT; ++j) {
-                qg_f4 now[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if constexpr (YT == QG_F32)
-                        now[i] = block_sum(ca[i], cx[j]);
-                    else
-                        now[i] = block_sum(ca[i], fx[j]);
-                }
-                // the step before
-                const int pj = j ? j - 1 : G::CT - 1, pp = j ? p : p ? p - 1 : G::NP - 1;
-                const float s = j || p ? sx[pj] : sl1;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    add_scaled(acc[2 * pp + i][pj], sum[i], s);
-                    // (left free, the last tile's additions move behind it and its sums to scratch memory)
-                    if constexpr (LAST) asm volatile("" : "+v"(acc[2 * pp + i][pj]));
-                    sum[i] = now[i];
-                }
-                if (p + 1 < G::NP) {
-                    if (j == 0) get_pair(fa[(p + 1) & 1], buf, p + 1);
-                } else if constexpr (!LAST) {
-                    if (j == 0) {
-                        get_scales(sc, t + 1);
-                        get_pair(fa[0], nbuf, 0);
-                    }
-                    get_col(fx[j], nbuf, j);
-                    fetch(t + NS, buf, j, G::CT);
-                }
-                __builtin_amdgcn_sched_barrier(0);
+                sx[j] = s[j] * w;
+                fx[j] = as(rx[j]);
             }
         }
-        sl1 = sx[G::CT - 1];
+#pragma unroll
+        for (int i = 0; i < G::MH; ++i) fa[i] = as(ra[i]);
+    };
+    // The products of part h, and between them the loads that may go now (BEHIND: the wavefront
+    // is of the second group).
+    auto multiply = [&](auto behind, int t, int buf, int h) {
+        constexpr bool BEHIND = decltype(behind)::value;
+        const int before = buf ? buf - 1 : NS - 1;
+        const int part = H == 1 ? 0 : BEHIND ? h : 1 - h;
+        const int count = part ? G::AH : FIRST;
+        const bool next = BEHIND || (H == 2 && h == 1);  // to this tile's own buffer, or to the one before
+#pragma unroll
+        for (int at = 0; at < PRODUCTS; ++at) {
+            const qg_f4 now = block_sum(fa[at / G::CT], fx[at % G::CT]);
+            if (at >= D) {
+                const int b = at - D;
+                add_scaled(acc[h * G::MH + b / G::CT][b % G::CT], sum[b % D], sx[b % G::CT]);
+            }
+            sum[at % D] = now;
+#pragma unroll
+            for (int u = at * count / PRODUCTS; u < (at + 1) * count / PRODUCTS; ++u)
+                fetch(next ? t + NS : t - 1 + NS, next ? buf : before, part, u);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     int id = blockIdx.x;
     if (!aim(id)) return;
@@ -668,23 +683,34 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         for (int i = 0; i < G::MT; ++i)
 #pragma unroll
             for (int j = 0; j < G::CT; ++j) acc[i][j] = qg_f4{0.f, 0.f, 0.f, 0.f};
-        sum[0] = sum[1] = qg_f4{0.f, 0.f, 0.f, 0.f};
-        sl1 = 0.f;
-        tile_sync<(NS - 1) * U>();
-        get_scales(sc, k0);
-        get_pair(fa[0], 0, 0);
 #pragma unroll
-        for (int j = 0; j < G::CT; ++j) get_col(fx[j], 0, j);
-        int t = k0, buf = 0;
-        for (; t + 1 < k1; ++t) {
-            const int nbuf = buf + 1 == NS ? 0 : buf + 1;
-            if (((t + NS) & 7) == 0 && t + NS < k1) fetch_scales((t + NS) >> 3);
-            tile(std::false_type{}, t, buf, nbuf);
-            buf = nbuf;
+        for (int d = 0; d < D; ++d) sum[d] = qg_f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < G::CT; ++j) sx[j] = 0.f;
+        tile_sync<H == 2 ? FIRST : (NS - 2) * U>();
+        auto turns = [&](auto behind) {
+            constexpr auto other = std::integral_constant<bool, !decltype(behind)::value>{};
+            int buf = 0;
+            for (int t = k0; t < k1; ++t) {
+                if (((t + NS) & 7) == 0 && t + NS < k1) fetch_scales((t + NS) >> 3);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    read(t, buf, h);
+                    turn_end(std::true_type{}, behind);
+                    multiply(behind, t, buf, h);
+                    turn_end(std::false_type{}, other);
+                }
+                buf = buf + 1 == NS ? 0 : buf + 1;
+            }
+        };
+        if (wave >= 4) {
+            asm volatile("s_barrier" ::: "memory");
+            turns(std::true_type{});
+        } else {
+            turns(std::false_type{});
+            asm volatile("s_barrier" ::: "memory");
         }
-        tile(std::true_type{}, t, buf, buf);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) add_scaled(acc[G::MT - 2 + i][G::CT - 1], sum[i], sl1);
+        flush(H - 1);
         const int m0 = (t0 + wm * G::MT) * 16 + q * 8, c0 = n0 + wn * G::CT * 16 + r;
         if constexpr (SPLIT) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (loads beyond the last tile)
@@ -696,18 +722,23 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
             return;
         } else {
             // A workgroup with another tile to do sends that tile's first loads before it
-            // stores this one's outputs.
-            const int rows = n1, expert = e;
+            // stores this one's outputs. (The biases have arrived before: a wait for them in the
+            // next tile's turns would be one for its loads.)
+            float sb[G::MT / 2][8];
+#pragma unroll
+            for (int c = 0; c < G::MT / 2; ++c) {
+                row_bias(a, e, m0 + 32 * c, sb[c]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sb[c][i]));
+            }
+            const int rows = n1;
             id += gridDim.x;
             tile_sync<0>();  // the last tile's buffer has been read by all (and loads beyond it are done)
             const bool more = id < a.total && aim(id);
             if (more) start();
 #pragma unroll
-            for (int c = 0; c < G::NP; ++c) {
-                float sb[8];
-                row_bias(a, expert, m0 + 32 * c, sb);
-                store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb, m0 + 32 * c, c0, rows);
-            }
+            for (int c = 0; c < G::MT / 2; ++c)
+                store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb[c], m0 + 32 * c, c0, rows);
             if (!more) return;
         }
     }
@@ -748,6 +779,8 @@ struct Plan {
     size_t ws;
 };
 
+int64_t weight_tiles(int64_t M) { return qg::ceil_div(M, kPair) * 2; }
+
 Plan plan(int64_t M, int64_t K, int64_t N, int y_type) {
     Plan p{};
     const int kt = (int)qg::ceil_div(K, kB);
@@ -756,7 +789,7 @@ Plan plan(int64_t M, int64_t K, int64_t N, int y_type) {
     auto tiles = [&](int b) { return qg::ceil_div(M, b) * qg::ceil_div(N, b); };
     if (N <= 32) {
         p.form = FORM_STREAM;
-        p.tiles = (int)qg::ceil_div(M, T);
+        p.tiles = (int)weight_tiles(M);
         return p;
     }
     int side = 64;
@@ -775,9 +808,9 @@ Plan plan(int64_t M, int64_t K, int64_t N, int y_type) {
     return p;
 }
 
-template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
+template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool SPLIT, bool GROUPED>
 qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
-    typedef F8Tile<BM, BN, WM, WN, NS> G;
+    typedef F8Tile<BM, BN, WM, WN, NS, H> G;
     constexpr int most = G::LDS + (GROUPED ? (QG_EXPERTS_MAX + 64) * 4 : 0);  // (one number, and whole 64s of experts)
     static_assert(most <= 160 * 1024, "LDS of a compute unit");
     const int lds = G::LDS + (GROUPED ? (1 + (a.E + 63) / 64 * 64) * 4 : 0);
@@ -785,9 +818,9 @@ qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
     const int groups = SPLIT ? p.tiles : std::min(p.tiles, qg::device_cus() * (160 * 1024 / lds));
     static std::atomic<bool> done[64];
     const qg_status lst =
-        allow_lds(reinterpret_cast<const void*>(&gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, SPLIT, GROUPED>), most, done);
+        allow_lds(reinterpret_cast<const void*>(&gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, H, SPLIT, GROUPED>), most, done);
     if (lst) return lst;
-    hipLaunchKernelGGL((gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, SPLIT, GROUPED>), dim3(groups, p.splits),
+    hipLaunchKernelGGL((gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, H, SPLIT, GROUPED>), dim3(groups, p.splits),
                        dim3(64 * G::W), lds, s, a);
     qg_status st = qg::launch_status("qgemm_f8");
     if constexpr (SPLIT) {
@@ -804,13 +837,13 @@ qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
     const bool split = p.splits > 1;
     switch (p.form) {
         case FORM_64:
-            return split ? launch_tiles<YT, 64, 64, 1, 4, 4, true, false>(a, p, s)
-                         : launch_tiles<YT, 64, 64, 1, 4, 4, false, false>(a, p, s);
+            return split ? launch_tiles<YT, 64, 64, 2, 4, 4, 1, true, false>(a, p, s)
+                         : launch_tiles<YT, 64, 64, 2, 4, 4, 1, false, false>(a, p, s);
         case FORM_128:
-            return split ? launch_tiles<YT, 128, 128, 2, 2, 2, true, false>(a, p, s)
-                         : launch_tiles<YT, 128, 128, 2, 2, 2, false, false>(a, p, s);
+            return split ? launch_tiles<YT, 128, 128, 2, 4, 4, 1, true, false>(a, p, s)
+                         : launch_tiles<YT, 128, 128, 2, 4, 4, 1, false, false>(a, p, s);
         case FORM_256:
-            if constexpr (YT != QG_F32) return launch_tiles<YT, 256, 256, 2, 4, 2, false, false>(a, p, s);
+            if constexpr (YT != QG_F32) return launch_tiles<YT, 256, 256, 2, 4, 2, 2, false, false>(a, p, s);
     }
     if (a.N <= 16)
         hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
@@ -840,10 +873,10 @@ qg_status launch_grouped(const GArgs& a, hipStream_t s) {
     }
     if (each <= 96) {
         b.total = p.tiles = tiles(64, 64);
-        return launch_tiles<YT, 64, 64, 1, 4, 4, false, true>(b, p, s);
+        return launch_tiles<YT, 64, 64, 2, 4, 4, 1, false, true>(b, p, s);
     }
     b.total = p.tiles = tiles(128, 128);
-    return launch_tiles<YT, 128, 128, 2, 2, 2, false, true>(b, p, s);
+    return launch_tiles<YT, 128, 128, 2, 4, 4, 1, false, true>(b, p, s);
 }
 
 qg_status check_mk(int64_t M, int64_t K) {
@@ -899,7 +932,7 @@ extern "C" {
 
 size_t qg_f8_bytes(int64_t M, int64_t K, int64_t experts) {
     if (M < 1 || M > QG_F8_MAX_ROWS || K < 1 || K > QG_F8_MAX_K || experts < 1 || experts > QG_EXPERTS_MAX) return 0;
-    const int64_t one = qg::ceil_div(M, T) * qg::ceil_div(K, kB) * kUnit;
+    const int64_t one = weight_tiles(M) * qg::ceil_div(K, kB) * kUnit;
     return one > kMost / experts ? 0 : (size_t)(one * experts);
 }
 
@@ -922,7 +955,7 @@ qg_status qg_pack_f8(const void* w, int64_t ldw, int64_t w_expert, void* dst, in
     const int64_t units = (int64_t)(n / 16);
     const unsigned g = (unsigned)std::min<int64_t>(qg::ceil_div(units, 256), 65536);
     hipLaunchKernelGGL(pack_f8_kernel, dim3(g), dim3(256), 0, (hipStream_t)stream, (const uint8_t*)w, ldw, w_expert,
-                       (uint4*)dst, M, (int)K, (int)qg::ceil_div(K, kB), qg::ceil_div(M, T), units);
+                       (uint4*)dst, M, (int)K, (int)qg::ceil_div(K, kB), weight_tiles(M), units);
     return qg::launch_status("qg_pack_f8");
 }
 
@@ -1010,7 +1043,7 @@ qg_status qgemm_f8(const void* w, const float* ws, const void* xq, int64_t ldx, 
     a.E = 1;
     a.nb = (int32_t)nb;
     a.mb = (int32_t)mb;
-    a.mtiles = (int32_t)qg::ceil_div(M, T);
+    a.mtiles = (int32_t)weight_tiles(M);
     a.kper = p.kper;
     a.total = p.tiles;
     hipStream_t s = (hipStream_t)stream;
@@ -1062,7 +1095,7 @@ qg_status qgemm_f8_grouped(const qg_f8_grouped* g, qg_stream_t stream) {
     a.E = (int32_t)g->experts;
     a.nb = (int32_t)nb;
     a.mb = (int32_t)mb;
-    a.mtiles = (int32_t)qg::ceil_div(g->M, T);
+    a.mtiles = (int32_t)weight_tiles(g->M);
     hipStream_t s = (hipStream_t)stream;
     if (g->y_type == QG_F32) return launch_grouped<QG_F32>(a, s);
     if (g->y_type == QG_F16) return launch_grouped<QG_F16>(a, s);

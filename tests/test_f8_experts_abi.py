@@ -21,8 +21,8 @@ def no_gpu():
 
 
 def test_sizes(L):
-    assert L.qg_f8_bytes(16, 128, 1) == 2048
-    assert L.qg_f8_bytes(17, 129, 3) == 3 * 2 * 2 * 2048
+    assert L.qg_f8_bytes(16, 128, 1) == 4096
+    assert L.qg_f8_bytes(33, 129, 3) == 3 * 2 * 2 * 4096
     assert L.qg_f8_bytes(152064, 3584, 1) == 152064 * 3584
     for m, k, e in [(0, 64, 1), (16, 0, 1), (4194304, 64, 1), (16, 131073, 1), (16, 64, 0), (16, 64, 1025), (4194303, 131072, 1024)]:
         assert L.qg_f8_bytes(m, k, e) == 0
@@ -187,8 +187,8 @@ def test_binding_refuses_host_tensors_and_other_types():
     f8 = torch.float8_e4m3fn
     q, s = torch.zeros(4, 128).to(f8), torch.zeros(4, 4)
     for call in (lambda: qg.pack_f8(q), lambda: qg.quantize_f8_rows(torch.zeros(4, 128)), lambda: qg.expert_combine(s, s, s),
-                 lambda: qg.qgemm_f8(torch.zeros(2048, dtype=torch.uint8), s, q, s, 16, 128),
-                 lambda: qg.qgemm_f8_grouped(torch.zeros(2048, dtype=torch.uint8), s, q, s, 16, 128, torch.zeros(2, dtype=torch.int32)),
+                 lambda: qg.qgemm_f8(torch.zeros(4096, dtype=torch.uint8), s, q, s, 16, 128),
+                 lambda: qg.qgemm_f8_grouped(torch.zeros(4096, dtype=torch.uint8), s, q, s, 16, 128, torch.zeros(2, dtype=torch.int32)),
                  lambda: qg.logits_expert_select(s, 2)):
         with pytest.raises(ValueError, match="on the GPU"):
             call()

@@ -261,11 +261,11 @@ def test_pack_takes_strided_weights():
         case(f"pack_f8 {tuple(cut.shape)} strides {cut.stride()}")
         whole = cut.view(torch.uint8).contiguous().view(F8)
         assert torch.equal(qg.pack_f8(cut), qg.pack_f8(whole))
-    # the layout: byte (t, b, h, g, i) is row 16 t + i, k = 128 b + 64 h + 16 g ..
+    # the layout: (t, i, b, h, g, j, l) is row 32 t + 8 j + 4 i + l, k = 128 b + 64 h + 16 g ..
     w = base[0, :37, :260]
-    want = np.zeros((48, 384), np.uint8)
+    want = np.zeros((64, 384), np.uint8)
     want[:37, :260] = w
-    want = want.reshape(3, 16, 3, 2, 4, 16).transpose(0, 2, 3, 4, 1, 5).reshape(-1)
+    want = want.reshape(2, 4, 2, 4, 3, 2, 4, 16).transpose(0, 2, 4, 5, 6, 1, 3, 7).reshape(-1)
     np.testing.assert_array_equal(qg.pack_f8(f8(w)).cpu().numpy(), want)
 
 
