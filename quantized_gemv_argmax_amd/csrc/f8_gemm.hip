@@ -377,7 +377,7 @@ struct F8Tile : Tile<BM, BN, WM, WN, NS> {
     static constexpr int LDS = P::LDS + 2 * SB;
     static constexpr int MH = P::MT / H;               // weight operands of a part of a K tile
     static constexpr int AH = P::AU / H;               // loads of them
-    static_assert(P::W == 8 && MH * H == P::MT && AH * H == P::AU && (H == 1 || (H == 2 && NS == 2)), "parts of a K tile");
+    static_assert(P::W == 8 && MH * H == P::MT && AH * H == P::AU && ((H == 1 && NS >= 3) || (H == 2 && NS == 2)), "parts of a K tile");
     static_assert(BM / WM <= kB && kB % (BM / WM) == 0 && BN % 64 == 0, "a wavefront's rows share a weight scale");
 };
 
@@ -405,6 +405,9 @@ QG_DEV void store_pair(const GArgs& a, const qg_f4 (&lo)[CT], const qg_f4 (&hi)[
 
 // The bound of a buffer's loads, whose offsets are 32 bits.
 QG_DEV int buffer_bytes(int64_t n) { return (int)(uint32_t)min(n, (int64_t)0xffffffffll); }
+
+template <int N>
+using number = std::integral_constant<int, N>;
 
 // The tiles of BN rows before each expert's, in LDS, by the first wavefront; returns the
 // number of all of them to it.
@@ -569,8 +572,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             if (i == 0 || (((k0 + i) & 7) == 0 && k0 + i < k1)) fetch_scales((k0 + i) >> 3);
-            if (H == 2 || i < NS - 1 || wave >= 4) fetch_part(k0 + i, i, 0);
-            if (H == 2 && (i < NS - 1 || wave >= 4)) fetch_part(k0 + i, i, 1);
+            if (H == 2 || i < NS - 1) fetch_part(k0 + i, i, 0);
+            if (H == 2 && i < NS - 1) fetch_part(k0 + i, i, 1);
         }
     };
 
@@ -599,22 +602,26 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
     };
 
     // The wavefronts work in two groups of four, one of each on every SIMD, that take turns:
-    // while one multiplies a part of a K tile (its operands are in registers), the other reads
-    // the operands of its next part from LDS and sends loads. A barrier ends each turn.
-    // The second group is a turn behind. A part's place in its buffer has been read by both
-    // groups when the second one's turn on it ends; the loads of the part NS tiles later go there from the
-    // first group's next reading turn on, and have arrived by the barrier before its next turn on that place:
-    // when LATER loads that were sent after them may still be on their way.
-    constexpr int U = G::AU + G::XU, LATER = H == 2 ? U : (NS - 2) * U;
+    // while one multiplies a part of a K tile (its operands are in registers, but for the last
+    // few, which are on their way), the other reads the operands of its next part from LDS. A
+    // barrier ends each turn; the second group is a turn behind. So turn 2 H t + 2 h of the
+    // first group reads part h of K tile t, the next one multiplies it, and the second group's
+    // are one later. A part's place in its buffer is free when the second group has multiplied
+    // it. The next loads to it go between the products of the first group one turn later, of
+    // the second two. They have to be there before the first group's turn that reads them: at
+    // the end of a turn before one, the first group has just multiplied and the second read, and each lets only
+    // the loads sent after those be on their way.
+    constexpr int U = G::AU + G::XU;
     Op fa[G::MH], fx[G::CT];
-    float sx[G::CT];
+    float sx[G::CT], s[G::CT], w;
     // sums of the last products, not added yet
+    constexpr int LATE = G::MH >= 4 ? 4 : 0;  // reads that may be on their way when a part's products begin
     constexpr int PRODUCTS = G::MH * G::CT, D = PRODUCTS < 3 ? PRODUCTS : 3;
     qg_f4 sum[D];
-    auto turn_end = [&](auto wait_lds, auto wait_loads) {
+    auto turn_end = [&](auto reads, auto loads) {
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (decltype(wait_lds)::value) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if constexpr (decltype(wait_loads)::value) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory");
+        if constexpr (decltype(reads)::value >= 0) asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(decltype(reads)::value) : "memory");
+        if constexpr (decltype(loads)::value >= 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(loads)::value) : "memory");
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -628,39 +635,33 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
     };
     auto read = [&](int t, int buf, int h) {
         Op8 ra[G::MH], rx[G::CT];
-        float s[G::CT], w;
         if (h == 0) {
 #pragma unroll
             for (int j = 0; j < G::CT; ++j) get_col(rx[j], buf, j);
-        }
-#pragma unroll
-        for (int i = 0; i < G::MH; ++i) get_row(ra[i], buf, h * G::MH + i);
-        if (h == 0) {
             const uint8_t* S = sl + ((t >> 3) & 1) * G::SB;
             const uint8_t* X = S + ((t >> 2) & 1) * (BN * 16) + srow + (t & 3) * 4;
 #pragma unroll
             for (int j = 0; j < G::CT; ++j) s[j] = *reinterpret_cast<const float*>(X + j * 256);
             w = *reinterpret_cast<const float*>(S + G::SU * 1024 + mine * 256 + (t & 7) * 4);
         }
+#pragma unroll
+        for (int i = 0; i < G::MH; ++i) {
+            if (2 * (G::MH - i) == LATE) __builtin_amdgcn_sched_barrier(0);
+            get_row(ra[i], buf, h * G::MH + i);
+        }
         flush(H - 1 - h);
         if (h == 0) {
 #pragma unroll
-            for (int j = 0; j < G::CT; ++j) {
-                sx[j] = s[j] * w;
-                fx[j] = as(rx[j]);
-            }
+            for (int j = 0; j < G::CT; ++j) fx[j] = as(rx[j]);
         }
 #pragma unroll
         for (int i = 0; i < G::MH; ++i) fa[i] = as(ra[i]);
     };
-    // The products of part h, and between them the loads that may go now (BEHIND: the wavefront
-    // is of the second group).
-    auto multiply = [&](auto behind, int t, int buf, int h) {
-        constexpr bool BEHIND = decltype(behind)::value;
-        const int before = buf ? buf - 1 : NS - 1;
-        const int part = H == 1 ? 0 : BEHIND ? h : 1 - h;
-        const int count = part ? G::AH : FIRST;
-        const bool next = BEHIND || (H == 2 && h == 1);  // to this tile's own buffer, or to the one before
+    // The products of part h of tile t, and between them the loads that may go now.
+    auto multiply = [&](int t, int buf, int h) {
+        const bool here = H == 2 && h == 1;  // to this tile's first part, or to the last part of the one before
+        const int to = here ? t + NS : t - 1 + NS, at_buf = here ? buf : buf ? buf - 1 : NS - 1;
+        const int part = H == 2 ? 1 - h : 0, count = part ? G::AH : FIRST;
 #pragma unroll
         for (int at = 0; at < PRODUCTS; ++at) {
             const qg_f4 now = block_sum(fa[at / G::CT], fx[at % G::CT]);
@@ -669,9 +670,13 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
                 add_scaled(acc[h * G::MH + b / G::CT][b % G::CT], sum[b % D], sx[b % G::CT]);
             }
             sum[at % D] = now;
+            if (h == 0 && at == 0) {
+#pragma unroll
+                for (int j = 0; j < G::CT; ++j) sx[j] = s[j] * w;
+            }
 #pragma unroll
             for (int u = at * count / PRODUCTS; u < (at + 1) * count / PRODUCTS; ++u)
-                fetch(next ? t + NS : t - 1 + NS, next ? buf : before, part, u);
+                fetch(to, at_buf, part, u);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -689,17 +694,21 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         for (int j = 0; j < G::CT; ++j) sx[j] = 0.f;
         tile_sync<H == 2 ? FIRST : (NS - 2) * U>();
         auto turns = [&](auto behind) {
-            constexpr auto other = std::integral_constant<bool, !decltype(behind)::value>{};
+            constexpr bool BEHIND = decltype(behind)::value;
             int buf = 0;
             for (int t = k0; t < k1; ++t) {
                 if (((t + NS) & 7) == 0 && t + NS < k1) fetch_scales((t + NS) >> 3);
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
+                auto part = [&](auto which) {
+                    constexpr int h = decltype(which)::value;
+                    // loads sent after those that the next reading turn of the first group needs
+                    constexpr int first = H == 2 ? U : (NS - 2) * U, second = H == 1 ? (NS - 3) * U : h ? G::AH : FIRST;
                     read(t, buf, h);
-                    turn_end(std::true_type{}, behind);
-                    multiply(behind, t, buf, h);
-                    turn_end(std::false_type{}, other);
-                }
+                    turn_end(number<LATE>{}, number<BEHIND ? second : -1>{});
+                    multiply(t, buf, h);
+                    turn_end(number<-1>{}, number<BEHIND ? -1 : first>{});
+                };
+                part(number<0>{});
+                if constexpr (H == 2) part(number<1>{});
                 buf = buf + 1 == NS ? 0 : buf + 1;
             }
         };
