@@ -8,6 +8,7 @@
 // whose sum is scaled once, by one multiply-add per output.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "qg_device.h"
 #include "qg_host.h"
@@ -365,21 +366,27 @@ __global__ __launch_bounds__(64 * KW) void gemm_f8_stream_kernel(GArgs a) {
 }
 
 // ---------------------------------------------------------------- many rows
-// Tiles of Y (Tile in qg_rows.h: a K tile of 128 bytes is one block). Beside a tile's
-// stages LDS holds the row scales and the weight scales of eight blocks, twice, and of a
-// grouped product the experts' first tiles.
-template <int BM, int BN, int WM, int WN, int NS, int H>
+// Tiles of Y (Tile in qg_rows.h: a K tile of 128 bytes is one block), one after the other
+// per workgroup. Beside a tile's stages LDS holds the row scales and the weight scales of
+// GB blocks, in GS places. H: parts of a K tile that are loaded apart (of two, the first has
+// half of each wavefront's weights and all activations).
+template <int BM, int BN, int WM, int WN, int NS, int H_, int GB_, int GS_>
 struct F8Tile : Tile<BM, BN, WM, WN, NS> {
     typedef Tile<BM, BN, WM, WN, NS> P;
-    static constexpr int SU = 2 * BN / 64;            // 1 KB loads of the row scales of eight blocks
-    static constexpr int MB = (BM + kB - 1) / kB;      // blocks of weight rows
-    static constexpr int SB = SU * 1024 + MB * 256;    // bytes of all scales of eight blocks
-    static constexpr int LDS = P::LDS + 2 * SB;
-    static constexpr int MH = P::MT / H;               // weight operands of a part of a K tile
-    static constexpr int AH = P::AU / H;               // loads of them
-    static_assert(P::W == 8 && MH * H == P::MT && AH * H == P::AU && ((H == 1 && NS >= 3) || (H == 2 && NS == 2)), "parts of a K tile");
+    static constexpr int H = H_, GB = GB_, GS = GS_;
+    static constexpr int SU = GB / 4 * BN / 64;         // 1 KB loads of the row scales of GB blocks
+    static constexpr int MB = (BM + kB - 1) / kB;       // blocks of weight rows
+    static constexpr int SB = SU * 1024 + MB * 256;     // bytes of all scales of GB blocks
+    static constexpr int LDS = P::LDS + GS * SB;
+    static_assert(SU <= P::W && GB <= 64, "a wavefront loads row scales and weight scales once");
+    static constexpr int MH = P::MT / H, AH = P::AU / H;  // weight operands and loads of a part
+    static constexpr int FIRST = AH + P::XU;            // loads of the first part
+    static_assert(MH * H == P::MT && AH * H == P::AU, "parts of a K tile");
     static_assert(BM / WM <= kB && kB % (BM / WM) == 0 && BN % 64 == 0, "a wavefront's rows share a weight scale");
 };
+
+template <int N>
+using number = std::integral_constant<int, N>;
 
 // Outputs of a wavefront's accumulators: a lane's pair is eight consecutive outputs, four
 // lanes' pairs are 32.
@@ -406,279 +413,299 @@ QG_DEV void store_pair(const GArgs& a, const qg_f4 (&lo)[CT], const qg_f4 (&hi)[
 // The bound of a buffer's loads, whose offsets are 32 bits.
 QG_DEV int buffer_bytes(int64_t n) { return (int)(uint32_t)min(n, (int64_t)0xffffffffll); }
 
-template <int N>
-using number = std::integral_constant<int, N>;
-
-// The tiles of BN rows before each expert's, in LDS, by the first wavefront; returns the
-// number of all of them to it.
-template <int BN>
-QG_DEV int first_tiles(const GArgs& a, int* first) {
-    const int lane = threadIdx.x & 63;
-    int all = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        int r0, r1;
-        group_range(a, e0 + lane, r0, r1);
-        const int n = (r1 - r0 + BN - 1) / BN;
-        int upto = n;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const int v = __shfl_up(upto, m);
-            if (lane >= m) upto += v;
-        }
-        first[e0 + lane] = all + upto - n;
-        all += __builtin_amdgcn_readlane(upto, 63);
-    }
-    return all;
-}
-
-// Tile of a grouped product: the experts' tiles of BN rows in order, each with all of its
-// weight tiles; the XCDs take contiguous runs. False beyond the last one.
-struct GroupTile {
-    Group g;
-    int t0, n0;  // first 16-row weight tile, first row of Y
+// A tile of Y: the expert, its first 16-row weight tile, first row and end of the expert's rows.
+struct TileOf {
+    int e, t0, n0, n1;
 };
-template <int BM, int BN>
-QG_DEV bool group_tile_at(const GArgs& a, const int* first, int all, int id, GroupTile& o) {
-    const int lane = threadIdx.x & 63;
-    const int mts = (a.mtiles * 16 + BM - 1) / BM;
-    const int total = all * mts, q = total / 8, r = total % 8, x = id % 8;
-    if (id / 8 >= q + (x < r)) return false;
-    id = x * q + min(x, r) + id / 8;
-    const int at = id / mts;
-    o.t0 = (id - at * mts) * (BM / 16);
-    // the last expert whose first tile is not beyond this one (it has rows: one without would share
-    // its first tile with the next)
-    int e = -1;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        const int c = __builtin_popcountll(__ballot(e0 + lane < a.E && first[e0 + lane] <= at));
-        e += c;
-        if (c < 64) break;
-    }
-    o.g.e = e;
-    const int r0 = min(max(a.offsets[e], 0), a.N);
-    o.g.r0 = __builtin_amdgcn_readfirstlane(r0);
-    o.g.r1 = __builtin_amdgcn_readfirstlane(min(max(a.offsets[e + 1], r0), a.N));
-    o.n0 = o.g.r0 + (at - __builtin_amdgcn_readfirstlane(first[e])) * BN;
-    return true;
-}
 
-template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool SPLIT, bool GROUPED>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
-    typedef F8Tile<BM, BN, WM, WN, NS, H> G;
-    // float32 outputs take the exact block sums, 16-bit ones the faster 8-bit matrix cores
-    typedef typename std::conditional<YT == QG_F32, Op16, Op8>::type Op;
-    extern __shared__ __align__(1024) uint8_t lds[];
-    uint8_t* const sl = lds + G::P::LDS;
-    int* const first = reinterpret_cast<int*>(lds + G::LDS);
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int k0 = SPLIT ? blockIdx.y * a.kper : 0;
-    const int k1 = SPLIT ? min(a.nb, k0 + a.kper) : a.nb;
-    int all = 0;
-    if constexpr (GROUPED) {
-        if (wave == 0) {
-            all = first_tiles<BN>(a, first + 1);
-            if (lane == 0) first[0] = all;
+// What a grouped product's workgroups know of the experts, in LDS: how many tiles of BN
+// rows come before each one's, and its first row.
+struct Experts {
+    int* all;    // tiles of all
+    int* first;  // [experts rounded up to 64]
+    int* from;   // [the same and one more]
+    __host__ QG_DEV static int bytes(int E) { return (2 + 2 * ((E + 63) & ~63)) * 4; }
+    QG_DEV Experts(uint8_t* lds, int E)
+        : all(reinterpret_cast<int*>(lds)), first(all + 1), from(first + ((E + 63) & ~63)) {}
+    // By one wavefront.
+    template <int BN>
+    QG_DEV void fill(const GArgs& a) {
+        const int lane = threadIdx.x & 63;
+        int sum = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 64) {
+            int r0, r1;
+            group_range(a, e0 + lane, r0, r1);
+            const int n = (r1 - r0 + BN - 1) / BN;
+            int upto = n;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const int v = __shfl_up(upto, m);
+                if (lane >= m) upto += v;
+            }
+            first[e0 + lane] = sum + upto - n;
+            from[e0 + lane] = r0;
+            sum += __builtin_amdgcn_readlane(upto, 63);
         }
-        __syncthreads();
-        all = __builtin_amdgcn_readfirstlane(first[0]);
+        if (lane == 0) {
+            from[a.E] = min(max(a.offsets[a.E], 0), a.N);
+            *all = sum;
+        }
     }
+    // Tile `id`: the experts' tiles in order, each with all of its weight tiles; the XCDs take
+    // contiguous runs. False beyond the last one.
+    template <int BM, int BN>
+    QG_DEV bool tile(const GArgs& a, int id, TileOf& o) const {
+        const int lane = threadIdx.x & 63;
+        const int mts = (a.mtiles * 16 + BM - 1) / BM;
+        const int total = __builtin_amdgcn_readfirstlane(*all) * mts, q = total / 8, r = total % 8, x = id % 8;
+        if (id / 8 >= q + (x < r)) return false;
+        id = x * q + min(x, r) + id / 8;
+        const int at = id / mts;
+        // the last expert whose first tile is not beyond this one (it has rows: one without would
+        // share its first tile with the next)
+        int e = -1;
+        for (int e0 = 0; e0 < a.E; e0 += 64) {
+            const int c = __builtin_popcountll(__ballot(e0 + lane < a.E && first[e0 + lane] <= at));
+            e += c;
+            if (c < 64) break;
+        }
+        const int r0 = __builtin_amdgcn_readfirstlane(from[e]);
+        o.e = e;
+        o.t0 = (id - at * mts) * (BM / 16);
+        o.n0 = r0 + (at - __builtin_amdgcn_readfirstlane(first[e])) * BN;
+        o.n1 = max(r0, __builtin_amdgcn_readfirstlane(from[e + 1]));
+        return true;
+    }
+};
 
-    // Loads: rows and tiles beyond the operands repeat the last ones (their sums are
-    // not stored). Weights arrive in the packed order. Activations: eight lanes per row
-    // of 128 bytes, the 16-byte chunk c of row r at place c ^ (r % 8), which spreads
-    // the operand reads over the banks.
-    const int chunk = (lane & 7) ^ (lane >> 3);
-    const int wm = wave % WM, wn = wave / WM, mine = wm * (BM / WM) / kB;  // (wavefronts of one block of rows load its scales alike)
-    const uint8_t *wp, *xp;
-    int wbytes, xbytes;
+// A wavefront's loads of a tile's stages and scales. What lies beyond the operands is out
+// of its buffer's bounds and reads as zeros (and its sums are not stored). Weights arrive in
+// the packed order. Activations: eight lanes per row of 128 bytes, the 16-byte chunk c of row
+// r at place c ^ (r % 8), which spreads the operand reads over the banks.
+template <class G, int BM, int BN, bool GROUPED>
+struct Loads {
+    const GArgs& a;
+    uint8_t* const lds;
+    const int lane, wave, mine;  // mine: the block of weight rows whose scales this wavefront takes
+    const uint8_t* xp;
+    int xbytes;
     __amdgpu_buffer_rsrc_t sr, vr;
     uint32_t woff[G::AU], xoff[G::XU], soff;
-    int t0, n0, n1, e = 0;
-    // 1 KB of weights in a stage that load u of this wavefront brings: the operands of the
-    // first part of every wavefront's rows come first.
-    auto unit_of = [&](int u) {
+
+    QG_DEV Loads(const GArgs& args, uint8_t* l, int ln, int wv, int block) : a(args), lds(l), lane(ln), wave(wv), mine(block) {
+#pragma unroll
+        for (int u = 0; u < G::AU; ++u) woff[u] = (uint32_t)(unit_of(u) >> 1) * (uint32_t)a.nb * kUnit + lane * 16u;
+        rows([](int c) { return (uint32_t)c; });
+    }
+    QG_DEV bool gathers() const { return GROUPED && a.row; }
+    // 1 KB of weights in a stage that load u brings: the operands of the first part of every
+    // wavefront's rows come first.
+    QG_DEV int unit_of(int u) const {
         const int h = u / G::AH, g = wave * G::AH + u % G::AH, o = g >> 1;
         return (o / G::MH * G::MT + h * G::MH + o % G::MH) * 2 + (g & 1);
-    };
-    auto aim = [&](int id) {
-        int64_t xbase = 0;
-        if constexpr (GROUPED) {
-            GroupTile at;
-            if (!group_tile_at<BM, BN>(a, first + 1, all, id, at)) return false;
-            e = at.g.e;
-            t0 = at.t0;
-            n0 = at.n0;
-            n1 = at.g.r1;
-        } else {
-            const TileAt at = tile_at<BM, BN>(a.mtiles, a.N, id);
-            t0 = at.t0;
-            n0 = at.n0;
-            n1 = a.N;
-        }
-        if (!GROUPED || !a.row) xbase = n0;
-        const int64_t rows = GROUPED && a.row ? a.X : n1 - n0;
-        wp = a.w + ((size_t)e * a.mtiles + t0) * a.nb * kUnit;
-        wbytes = buffer_bytes((int64_t)(a.mtiles - t0) * a.nb * kUnit);
-        xp = a.x + xbase * a.ldx;
-        xbytes = buffer_bytes((rows - 1) * a.ldx + a.nb * kB);
-        sr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.xs + xbase * a.ldxs), (short)0,
-                                               buffer_bytes(((rows - 1) * a.ldxs + ((a.nb + 3) & ~3)) * 4), kQgRawBufferFlags);
-        const int mblock = min((t0 * T + wm * (BM / WM)) / kB, a.mb - 1);
-        vr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.ws + ((size_t)e * a.mb + mblock) * a.nb), (short)0, a.nb * 4,
-                                               kQgRawBufferFlags);
-        auto from = [&](int c) {  // the row, from xbase on, that column c of the tile comes from
-            const int n = min(n0 + c, n1 - 1);
-            return (uint32_t)(GROUPED && a.row ? source_row(a, n) : n - n0);
-        };
-#pragma unroll
-        for (int u = 0; u < G::AU; ++u)
-            woff[u] = (uint32_t)min(unit_of(u) >> 1, a.mtiles - 1 - t0) * (uint32_t)a.nb * kUnit + lane * 16u;
+    }
+    // from(c): the row of x that column c of the tile comes from, counted from the first one of xp.
+    template <class F>
+    QG_DEV void rows(F&& from) {
 #pragma unroll
         for (int u = 0; u < G::XU; ++u)
-            xoff[u] = from((wave * G::XU + u) * 8 + (lane >> 3)) * (uint32_t)a.ldx + chunk * 16u;
+            xoff[u] = from((wave * G::XU + u) * 8 + (lane >> 3)) * (uint32_t)a.ldx + ((lane & 7) ^ (lane >> 3)) * 16u;
         soff = from(wave % (BN / 64) * 64 + lane) * (uint32_t)a.ldxs * 4u;
-        return true;
-    };
-    // Scales of the blocks 8 g .. + 7: the row scales four blocks to a load (wavefronts beyond
-    // the units repeat some), and eight weight scales.
-    auto fetch_scales = [&](int g) {
-        uint8_t* S = sl + (g & 1) * G::SB;
-        const int unit = wave % G::SU, c = min(g * 2 + unit / (BN / 64), (a.nb - 1) >> 2);
-        lds_load(sr, S + unit * 1024, soff, c * 16);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_ptr)(S + G::SU * 1024 + mine * 256), 4, (lane & 7) * 4, g * 32, 0, 0);
-    };
-    // Load u of part `part` of K tile t: its share of the weights, of the first part the
-    // activations too. Beyond the last tile every load is out of its buffer's bounds and reads
-    // nothing, so that the loop needs no branch.
-    constexpr int FIRST = G::AH + G::XU;  // loads of the first part
-    auto fetch = [&](int t, int buf, int part, int u) {
+    }
+    QG_DEV const uint8_t* weights(const TileOf& o) const { return a.w + ((size_t)o.e * a.mtiles + o.t0) * a.nb * kUnit; }
+    QG_DEV int weight_bytes(const TileOf& o) const { return buffer_bytes((int64_t)(a.mtiles - o.t0) * a.nb * kUnit); }
+    // The activations and scales of tile o.
+    QG_DEV void aim(const TileOf& o) {
+        const int64_t base = gathers() ? 0 : o.n0, rows = gathers() ? a.X : o.n1 - o.n0;
+        xp = a.x + base * a.ldx;
+        xbytes = buffer_bytes((rows - 1) * a.ldx + a.nb * kB);
+        sr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.xs + base * a.ldxs), (short)0,
+                                               buffer_bytes(((rows - 1) * a.ldxs + ((a.nb + 3) & ~3)) * 4), kQgRawBufferFlags);
+        const int block = min(o.t0 * T / kB + mine, a.mb - 1);
+        vr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.ws + ((size_t)o.e * a.mb + block) * a.nb), (short)0, a.nb * 4,
+                                               kQgRawBufferFlags);
+    }
+    // Load u of a part of K tile t to the stage in buffer buf: the part's weights first.
+    QG_DEV void fetch(const uint8_t* wp, int wbytes, int xbytes, int t, int buf, int part, int u) const {
         uint8_t* A = lds + buf * G::STAGE;
         if (u < G::AH) {
             const int v = part * G::AH + u;
-            const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wp, (short)0, t < k1 ? wbytes : 0, kQgRawBufferFlags);
+            const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wp, (short)0, wbytes, kQgRawBufferFlags);
             lds_load(wr, A + unit_of(v) * 1024, woff[v], (2 * t + (unit_of(v) & 1)) * 1024);
         } else {
-            const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)xp, (short)0, t < k1 ? xbytes : 0, kQgRawBufferFlags);
+            const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)xp, (short)0, xbytes, kQgRawBufferFlags);
             lds_load(xr, A + G::AB + (wave * G::XU + u - G::AH) * 1024, xoff[u - G::AH], t * kB);
         }
-    };
-    auto fetch_part = [&](int t, int buf, int part) {
+    }
+    // Scales of the blocks GB g .. + GB - 1: the row scales four blocks to a load, and the
+    // weight scales (wavefronts of one block of rows alike).
+    QG_DEV uint8_t* scales(int place) const { return lds + G::P::LDS + place * G::SB; }
+    QG_DEV void fetch_scales(int g, int place) const {
+        uint8_t* S = scales(place);
+        if (wave < G::SU)
+            lds_load(sr, S + wave * 1024, soff, min(g * (G::GB / 4) + wave / (BN / 64), (a.nb - 1) >> 2) * 16);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_ptr)(S + G::SU * 1024 + mine * 256), 4, (lane & (G::GB - 1)) * 4,
+                                                 g * G::GB * 4, 0, 0);
+    }
+};
+
+// A wavefront's reads from LDS, of one of its operands or scales.
+template <class G, int BN>
+struct Reads {
+    const uint8_t* const lds;
+    int arow, x0, x1, srow, wrow;
+    QG_DEV Reads(const uint8_t* l, int lane, int wm, int wn, int mine) : lds(l) {
+        const int r = lane & 15, q = lane >> 4, xrow = G::AB + (wn * G::CT * 16 + r) * 128;
+        arow = wm * G::MT * kUnit + lane * 16;
+        x0 = xrow + ((q ^ (r & 7)) * 16);
+        x1 = xrow + (((4 + q) ^ (r & 7)) * 16);
+        srow = (wn * G::CT * 16 + r) * 16;
+        wrow = G::SU * 1024 + mine * 256;
+    }
+    QG_DEV void row(Op8& o, int buf, int i) const {
+        const uint8_t* A = lds + buf * G::STAGE + arow + i * kUnit;
+        o.h[0] = *reinterpret_cast<const qi4*>(A);
+        o.h[1] = *reinterpret_cast<const qi4*>(A + 1024);
+    }
+    QG_DEV void col(Op8& o, int buf, int j) const {
+        const uint8_t* X = lds + buf * G::STAGE + j * 2048;
+        o.h[0] = *reinterpret_cast<const qi4*>(X + x0);
+        o.h[1] = *reinterpret_cast<const qi4*>(X + x1);
+    }
+    QG_DEV void scales(float (&x)[G::CT], float& w, const uint8_t* S, int t) const {
+        const uint8_t* X = S + ((t >> 2) & (G::GB / 4 - 1)) * (BN * 16) + srow + (t & 3) * 4;
 #pragma unroll
-        for (int u = 0; u < (part ? G::AH : FIRST); ++u) fetch(t, buf, part, u);
+        for (int j = 0; j < G::CT; ++j) x[j] = *reinterpret_cast<const float*>(X + j * 256);
+        w = *reinterpret_cast<const float*>(S + wrow + (t & (G::GB - 1)) * 4);
+    }
+};
+
+// float32 outputs take the exact block sums, 16-bit ones the faster 8-bit matrix cores.
+template <int YT>
+using Operand = typename std::conditional<YT == QG_F32, Op16, Op8>::type;
+template <int YT>
+QG_DEV Operand<YT> operand(const Op8& o) {
+    Operand<YT> v;
+    if constexpr (YT == QG_F32)
+        v.set(o);
+    else
+        v = o;
+    return v;
+}
+
+// Tiles of up to 128, several workgroups to a compute unit, whose starts and ends overlap.
+template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
+    typedef F8Tile<BM, BN, WM, WN, NS, 1, 8, 2> G;
+    constexpr int NP = G::MT / 2;  // pairs of weight operands
+    static_assert(NP % 2 == 0, "the pairs alternate between two sets of registers");
+    extern __shared__ __align__(1024) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM, mine = wm * (BM / WM) / kB;
+    const int k0 = SPLIT ? blockIdx.y * a.kper : 0;
+    const int k1 = SPLIT ? min(a.nb, k0 + a.kper) : a.nb;
+    Experts ex(lds + G::LDS, a.E);
+    if constexpr (GROUPED) {
+        if (wave == 0) ex.fill<BN>(a);
+        __syncthreads();
+    }
+    Loads<G, BM, BN, GROUPED> L(a, lds, lane, wave, mine);
+    const Reads<G, BN> R(lds, lane, wm, wn, mine);
+    TileOf at{};
+    const uint8_t* wp;
+    int wbytes;
+    auto aim = [&](int id) {
+        if (id >= a.total) return false;
+        if constexpr (GROUPED) {
+            if (!ex.tile<BM, BN>(a, id, at)) return false;
+            if (a.row) L.rows([&](int c) { return (uint32_t)source_row(a, min(at.n0 + c, at.n1 - 1)); });
+        } else {
+            const TileAt o = tile_at<BM, BN>(a.mtiles, a.N, id);
+            at = {0, o.t0, o.n0, a.N};
+        }
+        L.aim(at);
+        wp = L.weights(at);
+        wbytes = L.weight_bytes(at);
+        return true;
     };
-    // What the first turns need.
+    // A share of K tile t's loads. Beyond the last one they are out of bounds and read nothing,
+    // so that the loop needs no branch.
+    constexpr int U = G::AU + G::XU;
+    auto fetch = [&](int t, int buf, int part, int parts) {
+#pragma unroll
+        for (int u = part * U / parts; u < (part + 1) * U / parts; ++u)
+            L.fetch(wp, t < k1 ? wbytes : 0, t < k1 ? L.xbytes : 0, t, buf, 0, u);
+    };
     auto start = [&]() {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            if (i == 0 || (((k0 + i) & 7) == 0 && k0 + i < k1)) fetch_scales((k0 + i) >> 3);
-            if (H == 2 || i < NS - 1) fetch_part(k0 + i, i, 0);
-            if (H == 2 && i < NS - 1) fetch_part(k0 + i, i, 1);
+            if (i == 0 || (((k0 + i) & 7) == 0 && k0 + i < k1)) L.fetch_scales((k0 + i) >> 3, (k0 + i) >> 3 & 1);
+            fetch(k0 + i, i, 0, 1);
         }
     };
 
-    const int r = lane & 15, q = lane >> 4;
-    qg_f4 acc[G::MT][G::CT];
-    const int arow = wm * G::MT * kUnit + lane * 16;
-    const int xrow = G::AB + (wn * G::CT * 16 + r) * 128;
-    const int x0 = xrow + ((q ^ (r & 7)) * 16), x1 = xrow + (((4 + q) ^ (r & 7)) * 16);
-    const int srow = (wn * G::CT * 16 + r) * 16;
-    auto get = [](Op8& o, const uint8_t* p0, const uint8_t* p1) {
-        o.h[0] = *reinterpret_cast<const qi4*>(p0);
-        o.h[1] = *reinterpret_cast<const qi4*>(p1);
-    };
-    auto get_row = [&](Op8& o, int buf, int i) {
-        const uint8_t* A = lds + buf * G::STAGE + arow + i * kUnit;
-        get(o, A, A + 1024);
-    };
-    auto get_col = [&](Op8& o, int buf, int j) { get(o, lds + buf * G::STAGE + x0 + j * 2048, lds + buf * G::STAGE + x1 + j * 2048); };
-    auto as = [](const Op8& o) {
-        Op v;
-        if constexpr (YT == QG_F32)
-            v.set(o);
-        else
-            v = o;
-        return v;
-    };
-
-    // The wavefronts work in two groups of four, one of each on every SIMD, that take turns:
-    // while one multiplies a part of a K tile (its operands are in registers, but for the last
-    // few, which are on their way), the other reads the operands of its next part from LDS. A
-    // barrier ends each turn; the second group is a turn behind. So turn 2 H t + 2 h of the
-    // first group reads part h of K tile t, the next one multiplies it, and the second group's
-    // are one later. A part's place in its buffer is free when the second group has multiplied
-    // it. The next loads to it go between the products of the first group one turn later, of
-    // the second two. They have to be there before the first group's turn that reads them: at
-    // the end of a turn before one, the first group has just multiplied and the second read, and each lets only
-    // the loads sent after those be on their way.
-    constexpr int U = G::AU + G::XU;
-    Op fa[G::MH], fx[G::CT];
-    float sx[G::CT], s[G::CT], w;
-    // sums of the last products, not added yet
-    constexpr int LATE = G::MH >= 4 ? 4 : 0;  // reads that may be on their way when a part's products begin
-    constexpr int PRODUCTS = G::MH * G::CT, D = PRODUCTS < 3 ? PRODUCTS : 3;
-    qg_f4 sum[D];
-    auto turn_end = [&](auto reads, auto loads) {
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (decltype(reads)::value >= 0) asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(decltype(reads)::value) : "memory");
-        if constexpr (decltype(loads)::value >= 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(loads)::value) : "memory");
-        asm volatile("s_barrier" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    // Adds the sums of the products that the part h before left over.
-    auto flush = [&](int h) {
+    // A tile's products run pair by pair of weight operands, each pair over the columns, and
+    // the sums of a step are scaled and added during the next one. The operands of a pair are
+    // read during the pair before; before the last pair, whose operands are then in registers,
+    // a barrier: the tile's buffer can be refilled, with the tile NS later, and the next tile
+    // has arrived, whose operands and scales are read as the last pair frees their registers.
+    typedef Operand<YT> Op;
+    Op8 fa[2][2], fx[G::CT];
+    float xs[G::CT], w, sx[G::CT], before;
+    qg_f4 acc[G::MT][G::CT], sum[2];
+    auto tile = [&](auto last, int t, int buf, int nbuf) {
+        constexpr bool LAST = decltype(last)::value;
+        Op cx[G::CT];
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int at = PRODUCTS - D + d;
-            add_scaled(acc[h * G::MH + at / G::CT][at % G::CT], sum[at % D], sx[at % G::CT]);
-        }
-    };
-    auto read = [&](int t, int buf, int h) {
-        Op8 ra[G::MH], rx[G::CT];
-        if (h == 0) {
-#pragma unroll
-            for (int j = 0; j < G::CT; ++j) get_col(rx[j], buf, j);
-            const uint8_t* S = sl + ((t >> 3) & 1) * G::SB;
-            const uint8_t* X = S + ((t >> 2) & 1) * (BN * 16) + srow + (t & 3) * 4;
-#pragma unroll
-            for (int j = 0; j < G::CT; ++j) s[j] = *reinterpret_cast<const float*>(X + j * 256);
-            w = *reinterpret_cast<const float*>(S + G::SU * 1024 + mine * 256 + (t & 7) * 4);
+        for (int j = 0; j < G::CT; ++j) {
+            sx[j] = xs[j] * w;
+            if constexpr (YT == QG_F32) cx[j] = operand<YT>(fx[j]);
         }
 #pragma unroll
-        for (int i = 0; i < G::MH; ++i) {
-            if (2 * (G::MH - i) == LATE) __builtin_amdgcn_sched_barrier(0);
-            get_row(ra[i], buf, h * G::MH + i);
-        }
-        flush(H - 1 - h);
-        if (h == 0) {
-#pragma unroll
-            for (int j = 0; j < G::CT; ++j) fx[j] = as(rx[j]);
-        }
-#pragma unroll
-        for (int i = 0; i < G::MH; ++i) fa[i] = as(ra[i]);
-    };
-    // The products of part h of tile t, and between them the loads that may go now.
-    auto multiply = [&](int t, int buf, int h) {
-        const bool here = H == 2 && h == 1;  // to this tile's first part, or to the last part of the one before
-        const int to = here ? t + NS : t - 1 + NS, at_buf = here ? buf : buf ? buf - 1 : NS - 1;
-        const int part = H == 2 ? 1 - h : 0, count = part ? G::AH : FIRST;
-#pragma unroll
-        for (int at = 0; at < PRODUCTS; ++at) {
-            const qg_f4 now = block_sum(fa[at / G::CT], fx[at % G::CT]);
-            if (at >= D) {
-                const int b = at - D;
-                add_scaled(acc[h * G::MH + b / G::CT][b % G::CT], sum[b % D], sx[b % G::CT]);
+        for (int p = 0; p < NP; ++p) {
+            if (p == NP - 1 && !LAST) {
+                tile_sync<(NS - 2) * U>();
+                __builtin_amdgcn_sched_barrier(0);
             }
-            sum[at % D] = now;
-            if (h == 0 && at == 0) {
+            const Op ca[2] = {operand<YT>(fa[p & 1][0]), operand<YT>(fa[p & 1][1])};
 #pragma unroll
-                for (int j = 0; j < G::CT; ++j) sx[j] = s[j] * w;
+            for (int j = 0; j < G::CT; ++j) {
+                qg_f4 now[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (YT == QG_F32)
+                        now[i] = block_sum(ca[i], cx[j]);
+                    else
+                        now[i] = block_sum(ca[i], fx[j]);
+                }
+                // the step before
+                const int pj = j ? j - 1 : G::CT - 1, pp = j ? p : p ? p - 1 : NP - 1;
+                const float s = j || p ? sx[pj] : before;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    add_scaled(acc[2 * pp + i][pj], sum[i], s);
+                    // (left free, the last tile's additions move behind it and its sums to scratch memory)
+                    if constexpr (LAST) asm volatile("" : "+v"(acc[2 * pp + i][pj]));
+                    sum[i] = now[i];
+                }
+                if (p + 1 < NP) {
+                    if (j == 0)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) R.row(fa[(p + 1) & 1][i], buf, 2 * p + 2 + i);
+                } else if constexpr (!LAST) {
+                    if (j == 0) {
+                        R.scales(xs, w, L.scales((t + 1) >> 3 & 1), t + 1);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) R.row(fa[0][i], nbuf, i);
+                    }
+                    R.col(fx[j], nbuf, j);
+                    fetch(t + NS, buf, j, G::CT);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int u = at * count / PRODUCTS; u < (at + 1) * count / PRODUCTS; ++u)
-                fetch(to, at_buf, part, u);
-            __builtin_amdgcn_sched_barrier(0);
         }
+        before = sx[G::CT - 1];
     };
     int id = blockIdx.x;
     if (!aim(id)) return;
@@ -688,39 +715,25 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         for (int i = 0; i < G::MT; ++i)
 #pragma unroll
             for (int j = 0; j < G::CT; ++j) acc[i][j] = qg_f4{0.f, 0.f, 0.f, 0.f};
+        sum[0] = sum[1] = qg_f4{0.f, 0.f, 0.f, 0.f};
+        before = 0.f;
+        tile_sync<(NS - 1) * U>();
+        R.scales(xs, w, L.scales(k0 >> 3 & 1), k0);
 #pragma unroll
-        for (int d = 0; d < D; ++d) sum[d] = qg_f4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 2; ++i) R.row(fa[0][i], 0, i);
 #pragma unroll
-        for (int j = 0; j < G::CT; ++j) sx[j] = 0.f;
-        tile_sync<H == 2 ? FIRST : (NS - 2) * U>();
-        auto turns = [&](auto behind) {
-            constexpr bool BEHIND = decltype(behind)::value;
-            int buf = 0;
-            for (int t = k0; t < k1; ++t) {
-                if (((t + NS) & 7) == 0 && t + NS < k1) fetch_scales((t + NS) >> 3);
-                auto part = [&](auto which) {
-                    constexpr int h = decltype(which)::value;
-                    // loads sent after those that the next reading turn of the first group needs
-                    constexpr int first = H == 2 ? U : (NS - 2) * U, second = H == 1 ? (NS - 3) * U : h ? G::AH : FIRST;
-                    read(t, buf, h);
-                    turn_end(number<LATE>{}, number<BEHIND ? second : -1>{});
-                    multiply(t, buf, h);
-                    turn_end(number<-1>{}, number<BEHIND ? -1 : first>{});
-                };
-                part(number<0>{});
-                if constexpr (H == 2) part(number<1>{});
-                buf = buf + 1 == NS ? 0 : buf + 1;
-            }
-        };
-        if (wave >= 4) {
-            asm volatile("s_barrier" ::: "memory");
-            turns(std::true_type{});
-        } else {
-            turns(std::false_type{});
-            asm volatile("s_barrier" ::: "memory");
+        for (int j = 0; j < G::CT; ++j) R.col(fx[j], 0, j);
+        int t = k0, buf = 0;
+        for (; t + 1 < k1; ++t) {
+            const int nbuf = buf + 1 == NS ? 0 : buf + 1;
+            if (((t + NS) & 7) == 0 && t + NS < k1) L.fetch_scales((t + NS) >> 3, (t + NS) >> 3 & 1);
+            tile(std::false_type{}, t, buf, nbuf);
+            buf = nbuf;
         }
-        flush(H - 1);
-        const int m0 = (t0 + wm * G::MT) * 16 + q * 8, c0 = n0 + wn * G::CT * 16 + r;
+        tile(std::true_type{}, t, buf, buf);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) add_scaled(acc[G::MT - 2 + i][G::CT - 1], sum[i], before);
+        const int m0 = (at.t0 + wm * G::MT) * 16 + (lane >> 4) * 8, c0 = at.n0 + wn * G::CT * 16 + (lane & 15);
         if constexpr (SPLIT) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (loads beyond the last tile)
             qg_f4* p = a.part + ((((size_t)blockIdx.y * gridDim.x + blockIdx.x) * G::W + wave) * (G::MT * G::CT)) * 64 + lane;
@@ -732,24 +745,245 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
         } else {
             // A workgroup with another tile to do sends that tile's first loads before it
             // stores this one's outputs. (The biases have arrived before: a wait for them in the
-            // next tile's turns would be one for its loads.)
-            float sb[G::MT / 2][8];
+            // next tile would be one for its loads.)
+            float sb[NP][8];
 #pragma unroll
-            for (int c = 0; c < G::MT / 2; ++c) {
-                row_bias(a, e, m0 + 32 * c, sb[c]);
+            for (int c = 0; c < NP; ++c) {
+                row_bias(a, at.e, m0 + 32 * c, sb[c]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sb[c][i]));
             }
-            const int rows = n1;
+            const int rows = at.n1;
             id += gridDim.x;
             tile_sync<0>();  // the last tile's buffer has been read by all (and loads beyond it are done)
-            const bool more = id < a.total && aim(id);
+            const bool more = aim(id);
             if (more) start();
 #pragma unroll
-            for (int c = 0; c < G::MT / 2; ++c)
+            for (int c = 0; c < NP; ++c)
                 store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb[c], m0 + 32 * c, c0, rows);
             if (!more) return;
         }
+    }
+}
+
+// Large tiles, one workgroup of eight wavefronts to a compute unit, for K of some blocks.
+// The wavefronts work in two groups of four, one of each on every SIMD, that take turns: while
+// one multiplies a part of a K tile (its operands are in registers, but for the last few,
+// which are on their way), the other reads the operands of its next part from LDS. A barrier
+// ends each turn; the second group is a turn behind. So turn 2 H t + 2 h of the first group
+// reads part h of K tile t, the next one multiplies it, and the second group's are one later.
+// A part's place in its buffer is free when the second group has multiplied it. The next
+// loads to it go between the products of the first group one turn later, of the second two.
+// They have to be there before the first group's turn that reads them: at the end of a turn
+// before one, the first group has just multiplied and the second read, and each lets only the
+// loads sent after those be on their way.
+// The loads run on into the workgroup's next tile, whose first K tiles are there when this
+// one's outputs are stored; the stores are then waited for with the loads of a later turn.
+constexpr int kTurnsBlocks = 4;     // the least blocks of K: the next tile's rows are known after one
+constexpr int kTurnsExperts = 512;  // the most experts that leave room in LDS
+template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool GROUPED>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
+    typedef F8Tile<BM, BN, WM, WN, NS, H, 4, 3> G;  // (scales: see the places below)
+    static_assert(G::W == 8 && ((H == 1 && NS == 3) || (H == 2 && NS == 2)), "two groups; the waits below");
+    constexpr int AHEAD = 2;  // K tiles from the one that is multiplied to the one whose first part is loaded
+    static_assert(AHEAD == NS - 2 + H && kTurnsBlocks > AHEAD + 1, "");
+    extern __shared__ __align__(1024) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM, mine = wm * (BM / WM) / kB;
+    Experts ex(lds + G::LDS, a.E);
+    int* const next_rows = reinterpret_cast<int*>(lds + G::LDS + Experts::bytes(a.E));
+    if constexpr (GROUPED) {
+        if (wave == 0) ex.fill<BN>(a);
+        __syncthreads();
+    }
+    Loads<G, BM, BN, GROUPED> L(a, lds, lane, wave, mine);
+    const Reads<G, BN> R(lds, lane, wm, wn, mine);
+    int id = blockIdx.x;
+    auto tile_of = [&](TileOf& o) {
+        if (id >= a.total) return false;
+        if constexpr (GROUPED) return ex.tile<BM, BN>(a, id, o);
+        const TileAt d = tile_at<BM, BN>(a.mtiles, a.N, id);
+        o = {0, d.t0, d.n0, a.N};
+        return true;
+    };
+    TileOf at{}, next{};
+    bool more = false;
+    if (!tile_of(at)) return;
+    L.aim(at);
+    if (L.gathers()) L.rows([&](int c) { return (uint32_t)source_row(a, min(at.n0 + c, at.n1 - 1)); });
+    const int nb = a.nb;
+    const uint8_t *wp = L.weights(at), *wnext = wp;
+    int wbytes = L.weight_bytes(at), nbytes = 0;
+    // Load u of a part of K tile t, from nb on of the next tile (without one, nothing is read).
+    auto fetch = [&](int t, int buf, int part, int u) {
+        const bool on = t >= nb;
+        L.fetch(on ? wnext : wp, on ? nbytes : wbytes, L.xbytes, on ? t - nb : t, buf, part, u);
+    };
+    L.fetch_scales(0, 0);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            if (h == 0 || i < NS - 1)
+#pragma unroll
+                for (int u = 0; u < (h ? G::AH : G::FIRST); ++u) fetch(i, i, h, u);
+
+    constexpr int U = G::AU + G::XU;
+    constexpr int LATE = G::MH >= 4 ? 4 : 0;  // reads that may be on their way when a part's products begin
+    constexpr int PRODUCTS = G::MH * G::CT, D = PRODUCTS < 3 ? PRODUCTS : 3;  // D: products whose sums wait to be added
+    typedef Operand<YT> Op;
+    Op fa[G::MH], fx[G::CT];
+    float sx[G::CT], xs[G::CT], w;
+    qg_f4 acc[G::MT][G::CT], sum[D];
+    auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < G::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j) acc[i][j] = qg_f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int d = 0; d < D; ++d) sum[d] = qg_f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < G::CT; ++j) sx[j] = 0.f;
+    };
+    auto turn_end = [&](auto reads, auto loads) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(reads)::value >= 0) asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(decltype(reads)::value) : "memory");
+        if constexpr (decltype(loads)::value >= 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(loads)::value) : "memory");
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Adds the sums that part h has left over.
+    auto flush = [&](int h) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int p = PRODUCTS - D + d;
+            add_scaled(acc[h * G::MH + p / G::CT][p % G::CT], sum[p % D], sx[p % G::CT]);
+        }
+    };
+    auto read = [&](int t, int buf, const uint8_t* S, int h) {
+        Op8 ra[G::MH], rx[G::CT];
+        if (h == 0) {
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j) R.col(rx[j], buf, j);
+            R.scales(xs, w, S, t);
+        }
+#pragma unroll
+        for (int i = 0; i < G::MH; ++i) {
+            if (2 * (G::MH - i) == LATE) __builtin_amdgcn_sched_barrier(0);
+            R.row(ra[i], buf, h * G::MH + i);
+        }
+        flush(H - 1 - h);
+        if (h == 0) {
+#pragma unroll
+            for (int j = 0; j < G::CT; ++j) fx[j] = operand<YT>(rx[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < G::MH; ++i) fa[i] = operand<YT>(ra[i]);
+    };
+    // The products of part h of K tile t, and between them the loads that may go now.
+    auto multiply = [&](int t, int buf, int h) {
+        const bool here = H == 2 && h == 1;  // to this tile's first part, or to the last part of the one before
+        const int to = here ? t + NS : t - 1 + NS, to_buf = here ? buf : buf ? buf - 1 : NS - 1;
+        const int part = H == 2 ? 1 - h : 0, count = part ? G::AH : G::FIRST;
+#pragma unroll
+        for (int p = 0; p < PRODUCTS; ++p) {
+            const qg_f4 now = block_sum(fa[p / G::CT], fx[p % G::CT]);
+            if (p >= D) {
+                const int b = p - D;
+                add_scaled(acc[h * G::MH + b / G::CT][b % G::CT], sum[b % D], sx[b % G::CT]);
+            }
+            sum[p % D] = now;
+            if (h == 0 && p == 0) {
+#pragma unroll
+                for (int j = 0; j < G::CT; ++j) sx[j] = xs[j] * w;
+            }
+#pragma unroll
+            for (int u = p * count / PRODUCTS; u < (p + 1) * count / PRODUCTS; ++u) fetch(to, to_buf, part, u);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto turns = [&](auto behind) {
+        constexpr bool BEHIND = decltype(behind)::value;
+        // Places of the scales that are read, and of those loaded last. A group of four blocks (of
+        // fewer at a tile's end) is loaded when the first of them is two K tiles away, to the
+        // place of the group three before: with four blocks of K or more, two groups
+        // in a row have five, so that one has long been read.
+        int buf = 0, from = 2, to = 0;
+        auto after = [](int place) { return place == 2 ? 0 : place + 1; };
+        // A tile's first waits find what they need: the next ones come behind stores.
+        auto k_tile = [&](auto begin, int t) {
+            if ((t & 3) == 0) from = after(from);
+            auto part = [&](auto which) {
+                constexpr int h = decltype(which)::value;
+                constexpr bool SKIP = decltype(begin)::value && h == 0;
+                // loads sent after those that the next reading turn of the first group needs
+                constexpr int first = U, second = H == 1 ? 0 : h ? G::AH : G::FIRST;
+                read(t, buf, L.scales(from), h);
+                turn_end(number<LATE>{}, number<BEHIND && !SKIP ? second : -1>{});
+                multiply(t, buf, h);
+                turn_end(number<-1>{}, number<BEHIND || SKIP ? -1 : first>{});
+            };
+            part(number<0>{});
+            if constexpr (H == 2) part(number<1>{});
+            buf = buf + 1 == NS ? 0 : buf + 1;
+        };
+        while (true) {
+            // the next tile, and the rows that it gathers
+            id += gridDim.x;
+            more = tile_of(next);
+            if (more && L.gathers()) {
+                const int unit = wave % (BN / 64);
+                const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc((void*)a.row, (short)0, a.N * 4, kQgRawBufferFlags);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, (lds_ptr)(next_rows + unit * 64), 4,
+                                                         min(next.n0 + unit * 64 + lane, next.n1 - 1) * 4, 0, 0, 0);
+            }
+            k_tile(std::true_type{}, 0);
+            for (int t = 1; t < nb; ++t) {
+                const int l = t + AHEAD;
+                if (l == nb) {
+                    wnext = L.weights(next);
+                    nbytes = more ? L.weight_bytes(next) : 0;
+                    L.aim(next);
+                    if (!more) L.xbytes = 0;
+                    if (more && L.gathers()) L.rows([&](int c) { return (uint32_t)min(max(next_rows[c], 0), a.X - 1); });
+                    to = after(to);
+                    if (more) L.fetch_scales(0, to);
+                } else if (l < nb && (l & 3) == 0) {
+                    to = after(to);
+                    L.fetch_scales(l >> 2, to);
+                }
+                k_tile(std::false_type{}, t);
+            }
+            flush(H - 1);
+            const int m0 = (at.t0 + wm * G::MT) * 16 + (lane >> 4) * 8, c0 = at.n0 + wn * G::CT * 16 + (lane & 15);
+            float sb[G::MT / 2][8];
+#pragma unroll
+            for (int c = 0; c < G::MT / 2; ++c) {
+                row_bias(a, at.e, m0 + 32 * c, sb[c]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sb[c][i]));
+            }
+            // what the next tile's first turns read
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(H == 2 ? G::FIRST : 0) : "memory");
+#pragma unroll
+            for (int c = 0; c < G::MT / 2; ++c)
+                store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb[c], m0 + 32 * c, c0, at.n1);
+            if (!more) return;
+            clear();
+            at = next;
+            wp = wnext;
+            wbytes = nbytes;
+        }
+    };
+    clear();
+    tile_sync<H == 2 ? G::FIRST : 0>();
+    if (wave >= 4) {
+        asm volatile("s_barrier" ::: "memory");
+        turns(std::true_type{});
+    } else {
+        turns(std::false_type{});
+        asm volatile("s_barrier" ::: "memory");
     }
 }
 
@@ -802,7 +1036,7 @@ Plan plan(int64_t M, int64_t K, int64_t N, int y_type) {
         return p;
     }
     int side = 64;
-    if (N > 64 && tiles(256) >= 192 && y_type != QG_F32)
+    if (N > 64 && tiles(256) >= 192 && kt >= kTurnsBlocks && y_type != QG_F32)
         side = 256;
     else if (N > 64 && (tiles(128) >= 128 || kt >= 64))
         side = 128;
@@ -817,21 +1051,26 @@ Plan plan(int64_t M, int64_t K, int64_t N, int y_type) {
     return p;
 }
 
-template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool SPLIT, bool GROUPED>
-qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
-    typedef F8Tile<BM, BN, WM, WN, NS, H> G;
-    constexpr int most = G::LDS + (GROUPED ? (QG_EXPERTS_MAX + 64) * 4 : 0);  // (one number, and whole 64s of experts)
-    static_assert(most <= 160 * 1024, "LDS of a compute unit");
-    const int lds = G::LDS + (GROUPED ? (1 + (a.E + 63) / 64 * 64) * 4 : 0);
-    // a workgroup takes tile after tile, as many of them at a time as there is LDS for
-    const int groups = SPLIT ? p.tiles : std::min(p.tiles, qg::device_cus() * (160 * 1024 / lds));
+// A workgroup takes tile after tile, as many of them at a time as there is LDS for.
+template <class K>
+qg_status launch_tiles(K kernel, std::atomic<bool>* done, const GArgs& a, const Plan& p, int threads, int lds, bool split,
+                       hipStream_t s) {
+    if (lds > 65536) {
+        const qg_status st = allow_lds(reinterpret_cast<const void*>(kernel), 160 * 1024, done);
+        if (st) return st;
+    }
+    GArgs b = a;
+    b.total = p.tiles;
+    const int groups = split ? p.tiles : std::min(p.tiles, qg::device_cus() * (160 * 1024 / lds));
+    hipLaunchKernelGGL(kernel, dim3(groups, p.splits), dim3(threads), lds, s, b);
+    return qg::launch_status("qgemm_f8");
+}
+template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
+qg_status launch_small(const GArgs& a, const Plan& p, hipStream_t s) {
+    typedef F8Tile<BM, BN, WM, WN, NS, 1, 8, 2> G;
     static std::atomic<bool> done[64];
-    const qg_status lst =
-        allow_lds(reinterpret_cast<const void*>(&gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, H, SPLIT, GROUPED>), most, done);
-    if (lst) return lst;
-    hipLaunchKernelGGL((gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, H, SPLIT, GROUPED>), dim3(groups, p.splits),
-                       dim3(64 * G::W), lds, s, a);
-    qg_status st = qg::launch_status("qgemm_f8");
+    qg_status st = launch_tiles(gemm_f8_tile_kernel<YT, BM, BN, WM, WN, NS, SPLIT, GROUPED>, done, a, p, 64 * G::W,
+                                G::LDS + (GROUPED ? Experts::bytes(a.E) : 0), SPLIT, s);
     if constexpr (SPLIT) {
         if (st) return st;
         hipLaunchKernelGGL((gemm_f8_join_kernel<YT, BM, BN, WM, WN>), dim3(p.tiles * G::W * (G::MT / 2)), dim3(64), 0, s,
@@ -840,19 +1079,28 @@ qg_status launch_tiles(const GArgs& a, const Plan& p, hipStream_t s) {
     }
     return st;
 }
+template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool GROUPED>
+qg_status launch_turns(const GArgs& a, const Plan& p, hipStream_t s) {
+    typedef F8Tile<BM, BN, WM, WN, NS, H, 4, 3> G;
+    constexpr int rows = GROUPED ? BN * 4 : 0;
+    static_assert(G::LDS + rows + (GROUPED ? (2 + 2 * kTurnsExperts) * 4 : 0) <= 160 * 1024, "LDS of a compute unit");
+    static std::atomic<bool> done[64];
+    return launch_tiles(gemm_f8_turns_kernel<YT, BM, BN, WM, WN, NS, H, GROUPED>, done, a, p, 512,
+                        G::LDS + rows + (GROUPED ? Experts::bytes(a.E) : 0), false, s);
+}
 
 template <int YT>
 qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
     const bool split = p.splits > 1;
     switch (p.form) {
         case FORM_64:
-            return split ? launch_tiles<YT, 64, 64, 2, 4, 4, 1, true, false>(a, p, s)
-                         : launch_tiles<YT, 64, 64, 2, 4, 4, 1, false, false>(a, p, s);
+            return split ? launch_small<YT, 64, 64, 1, 4, 4, true, false>(a, p, s)
+                         : launch_small<YT, 64, 64, 1, 4, 4, false, false>(a, p, s);
         case FORM_128:
-            return split ? launch_tiles<YT, 128, 128, 2, 4, 4, 1, true, false>(a, p, s)
-                         : launch_tiles<YT, 128, 128, 2, 4, 4, 1, false, false>(a, p, s);
+            return split ? launch_small<YT, 128, 128, 2, 2, 2, true, false>(a, p, s)
+                         : launch_small<YT, 128, 128, 2, 2, 2, false, false>(a, p, s);
         case FORM_256:
-            if constexpr (YT != QG_F32) return launch_tiles<YT, 256, 256, 2, 4, 2, 2, false, false>(a, p, s);
+            if constexpr (YT != QG_F32) return launch_turns<YT, 256, 256, 2, 4, 2, 2, false>(a, p, s);
     }
     if (a.N <= 16)
         hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
@@ -871,21 +1119,22 @@ qg_status launch_grouped(const GArgs& a, hipStream_t s) {
     auto tiles = [&](int bm, int bn) {
         return (int)((std::min<int64_t>(a.N, a.N / bn + used)) * qg::ceil_div(a.mtiles * 16, bm));
     };
-    GArgs b = a;
-    if (each <= 32) {
+    if (each <= 4) {
         const dim3 g(a.mtiles, (unsigned)used);
-        if (each <= 12)
-            hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), g, dim3(512), 0, s, a);
-        else
-            hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 2, 8>), g, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), g, dim3(512), 0, s, a);
         return qg::launch_status("qgemm_f8_grouped");
     }
-    if (each <= 96) {
-        b.total = p.tiles = tiles(64, 64);
-        return launch_tiles<YT, 64, 64, 2, 4, 4, 1, false, true>(b, p, s);
+    if (each <= 64) {
+        p.tiles = tiles(128, 64);
+        return launch_small<YT, 128, 64, 2, 2, 3, false, true>(a, p, s);
     }
-    b.total = p.tiles = tiles(128, 128);
-    return launch_tiles<YT, 128, 128, 2, 4, 4, 1, false, true>(b, p, s);
+    if constexpr (YT != QG_F32)
+        if (a.nb >= kTurnsBlocks && a.E <= kTurnsExperts) {
+            p.tiles = tiles(256, 128);
+            return launch_turns<YT, 256, 128, 4, 2, 3, 1, true>(a, p, s);
+        }
+    p.tiles = tiles(128, 128);
+    return launch_small<YT, 128, 128, 2, 2, 2, false, true>(a, p, s);
 }
 
 qg_status check_mk(int64_t M, int64_t K) {
