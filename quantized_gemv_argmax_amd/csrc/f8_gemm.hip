@@ -413,6 +413,26 @@ QG_DEV void store_pair(const GArgs& a, const qg_f4 (&lo)[CT], const qg_f4 (&hi)[
 // The bound of a buffer's loads, whose offsets are 32 bits.
 QG_DEV int buffer_bytes(int64_t n) { return (int)(uint32_t)min(n, (int64_t)0xffffffffll); }
 
+// The same outputs in 16 bits for whole pairs, by as many stores whatever rows there are: a
+// lane's row beyond the last one is out of the bounds of Yr, which begins at column m of row n0.
+template <int YT, int CT>
+QG_DEV void store_pair_counted(const __amdgpu_buffer_rsrc_t Yr, const qg_f4 (&lo)[CT], const qg_f4 (&hi)[CT],
+                               const float (&sb)[8], uint32_t at, uint32_t step, int rows) {
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[e] = lo[j][e] + sb[e];
+            y[4 + e] = hi[j][e] + sb[4 + e];
+        }
+        qg_u4v v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = pack2<YT>(y[2 * e], y[2 * e + 1]);
+        __builtin_amdgcn_raw_buffer_store_b128(v, Yr, 16 * j < rows ? at + j * step : 0xfffffff0u, 0, 0);
+    }
+}
+
 // A tile of Y: the expert, its first 16-row weight tile, first row and end of the expert's rows.
 struct TileOf {
     int e, t0, n0, n1;
@@ -451,8 +471,8 @@ struct Experts {
             *all = sum;
         }
     }
-    // Tile `id`: the experts' tiles in order, each with all of its weight tiles; the XCDs take
-    // contiguous runs. False beyond the last one.
+    // Tile `id`: the experts in order, of each one's the tiles of a weight tile together, so that
+    // they read it from the L2; the XCDs take contiguous runs. False beyond the last one.
     template <int BM, int BN>
     QG_DEV bool tile(const GArgs& a, int id, TileOf& o) const {
         const int lane = threadIdx.x & 63;
@@ -471,9 +491,10 @@ struct Experts {
         }
         const int r0 = __builtin_amdgcn_readfirstlane(from[e]);
         o.e = e;
-        o.t0 = (id - at * mts) * (BM / 16);
-        o.n0 = r0 + (at - __builtin_amdgcn_readfirstlane(first[e])) * BN;
         o.n1 = max(r0, __builtin_amdgcn_readfirstlane(from[e + 1]));
+        const int n = id - __builtin_amdgcn_readfirstlane(first[e]) * mts, nts = (o.n1 - r0 + BN - 1) / BN, m = n / nts;
+        o.t0 = m * (BM / 16);
+        o.n0 = r0 + (n - m * nts) * BN;
         return true;
     }
 };
@@ -777,16 +798,18 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
 // They have to be there before the first group's turn that reads them: at the end of a turn
 // before one, the first group has just multiplied and the second read, and each lets only the
 // loads sent after those be on their way.
-// The loads run on into the workgroup's next tile, whose first K tiles are there when this
-// one's outputs are stored; the stores are then waited for with the loads of a later turn.
-constexpr int kTurnsBlocks = 4;     // the least blocks of K: the next tile's rows are known after one
+// The loads run on into the workgroup's next tile. A tile's outputs are stored between its last
+// turn and the next one's first, in a known number of stores, so that waits for loads sent
+// before them can leave them on their way; where the last columns of Y make that number
+// unknown, the loads come first.
+constexpr int kTurnsBlocks = 4;     // the least blocks of K: the next tile's rows are known after two
 constexpr int kTurnsExperts = 512;  // the most experts that leave room in LDS
 template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool GROUPED>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
     typedef F8Tile<BM, BN, WM, WN, NS, H, 4, 3> G;  // (scales: see the places below)
     static_assert(G::W == 8 && ((H == 1 && NS == 3) || (H == 2 && NS == 2)), "two groups; the waits below");
     constexpr int AHEAD = 2;  // K tiles from the one that is multiplied to the one whose first part is loaded
-    static_assert(AHEAD == NS - 2 + H && kTurnsBlocks > AHEAD + 1, "");
+    static_assert(AHEAD == NS - 2 + H && kTurnsBlocks >= AHEAD + 2, "the next tile's rows are there when its loads begin");
     extern __shared__ __align__(1024) uint8_t lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -829,7 +852,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
 #pragma unroll
                 for (int u = 0; u < (h ? G::AH : G::FIRST); ++u) fetch(i, i, h, u);
 
-    constexpr int U = G::AU + G::XU;
+    constexpr int U = G::AU + G::XU, STORES = G::MT / 2 * G::CT;
     constexpr int LATE = G::MH >= 4 ? 4 : 0;  // reads that may be on their way when a part's products begin
     constexpr int PRODUCTS = G::MH * G::CT, D = PRODUCTS < 3 ? PRODUCTS : 3;  // D: products whose sums wait to be added
     typedef Operand<YT> Op;
@@ -911,24 +934,25 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
         // in a row have five, so that one has long been read.
         int buf = 0, from = 2, to = 0;
         auto after = [](int place) { return place == 2 ? 0 : place + 1; };
-        // A tile's first waits find what they need: the next ones come behind stores.
         auto k_tile = [&](auto begin, int t) {
             if ((t & 3) == 0) from = after(from);
             auto part = [&](auto which) {
                 constexpr int h = decltype(which)::value;
-                constexpr bool SKIP = decltype(begin)::value && h == 0;
-                // loads sent after those that the next reading turn of the first group needs
-                constexpr int first = U, second = H == 1 ? 0 : h ? G::AH : G::FIRST;
+                // loads, and stores of the tile before, sent after those that the next reading turn
+                // of the first group needs
+                constexpr int stores = decltype(begin)::value && h == 0 ? STORES : 0;
+                constexpr int first = U + stores, second = (H == 1 ? 0 : h ? G::AH : G::FIRST) + stores;
                 read(t, buf, L.scales(from), h);
-                turn_end(number<LATE>{}, number<BEHIND && !SKIP ? second : -1>{});
+                turn_end(number<LATE>{}, number<BEHIND ? second : -1>{});
                 multiply(t, buf, h);
-                turn_end(number<-1>{}, number<BEHIND || SKIP ? -1 : first>{});
+                turn_end(number<-1>{}, number<BEHIND ? -1 : first>{});
             };
             part(number<0>{});
             if constexpr (H == 2) part(number<1>{});
             buf = buf + 1 == NS ? 0 : buf + 1;
         };
         while (true) {
+            k_tile(std::true_type{}, 0);
             // the next tile, and the rows that it gathers
             id += gridDim.x;
             more = tile_of(next);
@@ -938,7 +962,6 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, (lds_ptr)(next_rows + unit * 64), 4,
                                                          min(next.n0 + unit * 64 + lane, next.n1 - 1) * 4, 0, 0, 0);
             }
-            k_tile(std::true_type{}, 0);
             for (int t = 1; t < nb; ++t) {
                 const int l = t + AHEAD;
                 if (l == nb) {
@@ -964,11 +987,21 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sb[c][i]));
             }
-            // what the next tile's first turns read
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(H == 2 ? G::FIRST : 0) : "memory");
+            if (at.t0 * T + BM <= a.M && a.ldy < (1 << 22)) {
+                const __amdgpu_buffer_rsrc_t Yr = __builtin_amdgcn_make_buffer_rsrc(
+                    (void*)((uint16_t*)a.Y + at.n0 * a.ldy + at.t0 * T), (short)0,
+                    buffer_bytes(((int64_t)(min(at.n1 - at.n0, BN) - 1) * a.ldy + BM) * 2), kQgRawBufferFlags);
+                const uint32_t ldy = (uint32_t)a.ldy * 2u, o = (uint32_t)(c0 - at.n0) * ldy + (uint32_t)(m0 - at.t0 * T) * 2u;
 #pragma unroll
-            for (int c = 0; c < G::MT / 2; ++c)
-                store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb[c], m0 + 32 * c, c0, at.n1);
+                for (int c = 0; c < G::MT / 2; ++c)
+                    store_pair_counted<YT, G::CT>(Yr, acc[2 * c], acc[2 * c + 1], sb[c], o + c * 64, 16 * ldy, at.n1 - c0);
+            } else {
+                // what the next tile's first turns read
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(H == 2 ? G::FIRST : 0) : "memory");
+#pragma unroll
+                for (int c = 0; c < G::MT / 2; ++c)
+                    store_pair<YT, G::CT>(a, acc[2 * c], acc[2 * c + 1], sb[c], m0 + 32 * c, c0, at.n1);
+            }
             if (!more) return;
             clear();
             at = next;
