@@ -1049,37 +1049,64 @@ __global__ __launch_bounds__(64) void gemm_f8_join_kernel(GArgs a, int tiles, in
 }
 
 // ---------------------------------------------------------------- launches
-enum { FORM_STREAM, FORM_64, FORM_128, FORM_256 };
+int64_t weight_tiles(int64_t M) { return qg::ceil_div(M, kPair) * 2; }
+
+// The forms and the rule that takes one (bf16 outputs, weights from memory, calls in a graph).
+//   STREAM  few rows: 4608 x 3584 by 1 in 6.2 us (64 x 64: 11.0), 152064 x 3584 by 1 in 87 (101);
+//           up to 16 rows of weights of up to 8192 rows (by 16: 8.4 and 11.1; 18944 x 3584 by 16
+//           18.8 and 15.4). From 17 rows on, tiles (4608 x 3584 by 32: 13.5 and 11.0).
+//   S64     tiles of 64 x 64, two workgroups to a unit, until there are over 512 of them.
+//   S128x64 the same with fewer reads of the activations, for one column of many (152064 x
+//           3584 by 32: 105 us, 64 x 64 120).
+//   S128    tiles of 128 in three LDS buffers, one workgroup to a unit, up to 256 of them (4608 x
+//           3584 by 512: 19.2 us, 64 x 64 22.4, 256 x 128 26.7).
+//   M128    tiles of 128 in two buffers, two workgroups to a unit: what is left where turns cannot be
+//           taken (float32, K below four blocks).
+//   T128, T256  256 x 128 and 256 x 256 in turns; a round of tiles on all units costs 27
+//           and 49 us at K = 3584, so the number of rounds decides: 4608 x 3584 by 4096 takes 82
+//           us in 3 of the first, 91 in 2 of the second, 37888 x 3584 by 4096 513 and 495.
+// With fewer tiles than units a long K is split until about 256 workgroups share it, each
+// keeping some K tiles to repay the second launch (3584 x 18944 by 64: 43 us whole, 19 in 4).
+enum { STREAM, S64, S128x64, S128, M128, T128, T256 };
 struct Plan {
     int form, tiles, splits, kper;
     size_t ws;
 };
-
-int64_t weight_tiles(int64_t M) { return qg::ceil_div(M, kPair) * 2; }
 
 Plan plan(int64_t M, int64_t K, int64_t N, int y_type) {
     Plan p{};
     const int kt = (int)qg::ceil_div(K, kB);
     p.splits = 1;
     p.kper = kt;
-    auto tiles = [&](int b) { return qg::ceil_div(M, b) * qg::ceil_div(N, b); };
-    if (N <= 32) {
-        p.form = FORM_STREAM;
+    auto tiles = [&](int bm, int bn) { return qg::ceil_div(M, bm) * qg::ceil_div(N, bn); };
+    auto take = [&](int form, int bm, int bn) {
+        p.form = form;
+        p.tiles = (int)tiles(bm, bn);
+    };
+    if (N <= 4 || (N <= 16 && M <= 8192)) {
+        p.form = STREAM;
         p.tiles = (int)weight_tiles(M);
         return p;
     }
-    int side = 64;
-    if (N > 64 && tiles(256) >= 192 && kt >= kTurnsBlocks && y_type != QG_F32)
-        side = 256;
-    else if (N > 64 && (tiles(128) >= 128 || kt >= 64))
-        side = 128;
-    p.tiles = (int)tiles(side);
-    p.form = side == 256 ? FORM_256 : side == 64 ? FORM_64 : FORM_128;
-    const int s = side == 256 ? 1 : std::min(256 / p.tiles, kt / (side == 128 ? 18 : 28));
-    if (s > 1) {
-        p.kper = (int)qg::ceil_div(kt, s);
-        p.splits = (int)qg::ceil_div(kt, p.kper);
-        p.ws = (size_t)p.splits * p.tiles * side * side * 4;
+    if (N <= 64 && tiles(64, 64) > 1024)
+        take(S128x64, 128, 64);
+    else if (tiles(64, 64) <= 512 && !(N > 64 && kt >= 64))
+        take(S64, 64, 64);
+    else if (tiles(128, 128) <= 256)
+        take(S128, 128, 128);
+    else if (y_type == QG_F32 || kt < kTurnsBlocks)
+        take(M128, 128, 128);
+    else if (qg::ceil_div(tiles(256, 256), 256) * 9 <= qg::ceil_div(tiles(256, 128), 256) * 5)
+        take(T256, 256, 256);
+    else
+        take(T128, 256, 128);
+    if (p.form == S64 || p.form == S128) {
+        const int side = p.form == S64 ? 64 : 128, s = std::min(256 / p.tiles, kt / (side == 128 ? 18 : 28));
+        if (s > 1) {
+            p.kper = (int)qg::ceil_div(kt, s);
+            p.splits = (int)qg::ceil_div(kt, p.kper);
+            p.ws = (size_t)p.splits * p.tiles * side * side * 4;
+        }
     }
     return p;
 }
@@ -1126,36 +1153,45 @@ template <int YT>
 qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
     const bool split = p.splits > 1;
     switch (p.form) {
-        case FORM_64:
+        case S64:
             return split ? launch_small<YT, 64, 64, 1, 4, 4, true, false>(a, p, s)
                          : launch_small<YT, 64, 64, 1, 4, 4, false, false>(a, p, s);
-        case FORM_128:
-            return split ? launch_small<YT, 128, 128, 2, 2, 2, true, false>(a, p, s)
-                         : launch_small<YT, 128, 128, 2, 2, 2, false, false>(a, p, s);
-        case FORM_256:
+        case S128x64: return launch_small<YT, 128, 64, 2, 2, 3, false, false>(a, p, s);
+        case S128:
+            return split ? launch_small<YT, 128, 128, 2, 4, 3, true, false>(a, p, s)
+                         : launch_small<YT, 128, 128, 2, 4, 3, false, false>(a, p, s);
+        case M128: return launch_small<YT, 128, 128, 2, 2, 2, false, false>(a, p, s);
+        case T128:
+            if constexpr (YT != QG_F32) return launch_turns<YT, 256, 128, 4, 2, 3, 1, false>(a, p, s);
+            break;
+        case T256:
             if constexpr (YT != QG_F32) return launch_turns<YT, 256, 256, 2, 4, 2, 2, false>(a, p, s);
+            break;
     }
-    if (a.N <= 16)
-        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
-    else
-        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 2, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
     return qg::launch_status("qgemm_f8");
 }
 
+// The same by the mean of rows to an expert that can have some, as the host does not know the
+// offsets (128 experts of 1536 x 2048, 8 to a token): one token streams (9.8 us, 64 x 64 11.1), as do all
+// with fewer than 256 tiles of 64 weight rows; up to 2 rows 64 x 64 (16 tokens 42.9 us, streamed
+// 60.5); up to 64 rows 128 x 64 (512 tokens 81 us, 256 x 128 90); up to 512 256 x 128 (4096 tokens
+// 166 us, 256 x 256 173), beyond 256 x 256 (8 experts of 4096 x 2048, 2 to each of 4096 tokens: 94 us and 103).
 template <int YT>
 qg_status launch_grouped(const GArgs& a, hipStream_t s) {
-    const int64_t used = std::min(a.E, a.N);  // experts that can have rows
-    const int64_t each = qg::ceil_div(a.N, used);
+    const int64_t used = std::min(a.E, a.N), each = qg::ceil_div(a.N, used);
     Plan p{};
     p.splits = 1;
-    p.kper = a.nb;
     auto tiles = [&](int bm, int bn) {
-        return (int)((std::min<int64_t>(a.N, a.N / bn + used)) * qg::ceil_div(a.mtiles * 16, bm));
+        return (int)(std::min<int64_t>(a.N, a.N / bn + used) * qg::ceil_div(a.mtiles * 16, bm));
     };
-    if (each <= 4) {
-        const dim3 g(a.mtiles, (unsigned)used);
-        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), g, dim3(512), 0, s, a);
+    if (each <= 4 && used * qg::ceil_div(a.mtiles * 16, 64) <= 256) {
+        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), dim3(a.mtiles, (unsigned)used), dim3(512), 0, s, a);
         return qg::launch_status("qgemm_f8_grouped");
+    }
+    if (each <= 2) {
+        p.tiles = tiles(64, 64);
+        return launch_small<YT, 64, 64, 1, 4, 4, false, true>(a, p, s);
     }
     if (each <= 64) {
         p.tiles = tiles(128, 64);
@@ -1163,6 +1199,10 @@ qg_status launch_grouped(const GArgs& a, hipStream_t s) {
     }
     if constexpr (YT != QG_F32)
         if (a.nb >= kTurnsBlocks && a.E <= kTurnsExperts) {
+            if (each >= 512) {
+                p.tiles = tiles(256, 256);
+                return launch_turns<YT, 256, 256, 2, 4, 2, 2, true>(a, p, s);
+            }
             p.tiles = tiles(256, 128);
             return launch_turns<YT, 256, 128, 4, 2, 3, 1, true>(a, p, s);
         }

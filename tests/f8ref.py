@@ -54,15 +54,14 @@ def product(xc, xs, wc, ws, bias=None):
     nb = -(-K // 128)
     X, W = VALUES[xc], VALUES[wc]
     y = np.zeros((xc.shape[0], wc.shape[0]))
-    mag, cut = np.zeros_like(y), np.zeros_like(y)
+    mag = np.zeros_like(y)
     over = np.repeat(ws.astype(np.float64), 128, axis=0)[:wc.shape[0]]  # (M, nb)
     for b in range(nb):
         x, w = X[:, 128 * b:128 * b + 128], W[:, 128 * b:128 * b + 128]
         s = xs[:, b].astype(np.float64)[:, None] * over[:, b][None]
         y += (x @ w.T) * s
         mag += (np.abs(x) @ np.abs(w).T) * np.abs(s)
-        # (largest of each eight at most their sum)
-        cut += (np.abs(x) @ np.abs(w).T) * np.abs(s)
+    cut = mag  # (the largest of each eight is at most their sum)
     if bias is not None:
         y = y + bias.astype(np.float64)
         mag = mag + np.abs(bias.astype(np.float64))

@@ -169,7 +169,7 @@ def check_product(M, K, N, t, bias, seed):
 SHAPES = [(1, 1, 1), (16, 128, 16), (17, 129, 17), (5, 1000, 1), (100, 3, 33), (512, 3584, 1), (1000, 257, 15), (640, 18944, 16),
           (333, 1001, 31), (2000, 640, 65), (257, 191, 129), (1031, 1024, 255), (700, 2048, 256), (519, 130, 513),
           (2050, 320, 1000), (384, 18944, 130), (520, 9000, 100), (2050, 191, 1537), (3300, 200, 4001), (3300, 1000, 3900),
-          (8200, 3584, 16), (8195, 1030, 20), (300, 4000, 70), (3600, 4161, 20), (33, 129, 7), (130, 18944, 64), (64, 18944, 40), (4700, 520, 4200), (4650, 1100, 4250), (6000, 1700, 3000)]
+          (8200, 3584, 16), (8195, 1030, 20), (300, 4000, 70), (3600, 4161, 20), (33, 129, 7), (130, 18944, 64), (64, 18944, 40), (9000, 600, 5), (9000, 600, 40), (70000, 300, 50), (4700, 520, 4200), (5000, 300, 4300), (3000, 1030, 1500), (4000, 520, 900), (4650, 1100, 4250), (6000, 1700, 3000)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -209,7 +209,7 @@ def check_grouped(M, K, counts, t, bias, gather, seed, lead=0, tail=0, X=None):
 
 GROUPS = [(64, 128, [1]), (17, 129, [3, 0, 40]), (517, 1001, [0, 2, 1, 0, 5, 33, 0, 1] * 4), (256, 384, [0, 0, 0, 0]),
           (300, 700, [70, 1, 0, 64, 65, 200]), (140, 260, [130, 300, 128, 0, 1, 500]), (1536, 2048, [8, 30, 17, 0, 16, 1]),
-          (384, 256, [260, 700, 0, 255, 257, 513]), (2100, 640, [300, 70, 129] * 8), (1000, 1100, [257, 0, 1, 400] * 10 + [900]), (600, 512, [100] * 60), (2300, 1537, [200] * 20),
+          (384, 256, [260, 700, 0, 255, 257, 513]), (2100, 640, [300, 70, 129] * 8), (1000, 1100, [257, 0, 1, 400] * 10 + [900]), (600, 512, [100] * 60), (700, 700, [900, 1, 513, 700]), (1100, 520, [700] * 13), (2300, 1537, [200] * 20),
           (96, 640, [1] * 130), (100, 130, [0] * 70 + [45] + [0] * 60 + [2]), (260, 300, [900])]
 
 
