@@ -70,40 +70,67 @@ QG_DEV uint32_t row_max(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));  // row_mirror
 }
 
-// x / d rounded to e4m3's three bits after the leading one (from 2^-6 on; multiples of
-// 2^-9 below), ties to even, decided on the exact quotient: in double precision the
-// quotient of two floats is never rounded onto a border that it does not meet.
-QG_DEV float round_exact(float x, float d) {
-    const double v = (double)x / (double)d, a = fabs(v);
-    const int e = a < 0x1p-6 ? -6 : ilogb(a);
-    return (float)ldexp(rint(ldexp(v, 3 - e)), e - 3);
-}
-
-// Eight values divided by d, as e4m3 bytes. x * inv is off by two units in the last place
-// at most; where it lies within four of a border between two results, the exact quotient
-// decides.
-QG_DEV uint2 quant8(const float (&x)[8], float d, float inv) {
-    float t[8];
-    bool near = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        t[e] = x[e] * inv;
-        float a = fabsf(t[e]);
-        if (a < 0x1p-6f) a += 0x1p-6f;  // (below 2^-6 the borders are those of the next octave, shifted)
-        near |= ((__builtin_bit_cast(uint32_t, a) + 4u - 0x80000u) & 0xfffffu) <= 8u;
-    }
-    if (near) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = round_exact(x[e], d);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = fminf(fmaxf(t[e], -448.f), 448.f);  // (over it where the scale is subnormal)
+QG_DEV uint2 to_f8(const float (&t)[8]) {
     uint2 o;
     o.x = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
     o.x = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], o.x, true);
     o.y = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
     o.y = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], o.y, true);
     return o;
+}
+
+// Eight values divided by a d below 2^-90, as e4m3 bytes: in double precision the quotient of
+// two floats is never rounded onto a border between two results that it does not meet. Three
+// bits after the leading one from 2^-6 on, multiples of 2^-9 below, ties to even.
+QG_DEV uint2 quant8_tiny(const float (&x)[8], float d) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const double v = (double)x[i] / (double)d, a = fabs(v);
+        const int e = a < 0x1p-6 ? -6 : ilogb(a);
+        t[i] = fminf(fmaxf((float)ldexp(rint(ldexp(v, 3 - e)), e - 3), -448.f), 448.f);  // (over it where d is subnormal)
+    }
+    return to_f8(t);
+}
+
+// Eight values divided by d, as e4m3 bytes, by x * inv with inv within a unit in the last place
+// of 1/d. The product is off by three units at most; where it lies within four of a border
+// (as bf16 values often do: in one block of seven the largest value is a multiple of 7, d a power of two
+// times few bits), the remainder of that border, exact in one fused operation, says on which side the quotient lies.
+QG_DEV uint2 quant8(const float (&x)[8], float d, float inv) {
+    float t[8];
+    auto shifted = [](float a) { return a < 0x1p-6f ? a + 0x1p-6f : a; };  // below 2^-6: the next octave's borders, shifted
+    auto off = [](float b) { return (__builtin_bit_cast(uint32_t, b) + (4u - 0x80000u)) << 12; };  // from 4 below a border on
+    uint32_t least = ~0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        t[e] = x[e] * inv;
+        least = min(least, off(shifted(fabsf(t[e]))));
+    }
+    if (__ballot(least <= 8u << 12)) {
+        asm volatile("");  // (a branch: without it both sides are computed and one is taken)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = fabsf(t[e]), b = shifted(a);
+            const float at = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, b) & 0xfff00000u) | 0x80000u);
+            const float border = a < 0x1p-6f ? at - 0x1p-6f : at;
+            const float rest = __builtin_fmaf(-border, d, fabsf(x[e]));
+            const float side = rest > 0.f ? 0x1p-22f : rest < 0.f ? -0x1p-22f : 0.f;
+            if (off(b) <= 8u << 12) t[e] = copysignf(__builtin_fmaf(border, side, border), t[e]);
+        }
+    }
+    return to_f8(t);
+}
+
+// z / (1 + exp(-z)): the exponential by a power of two, whose argument's rounding error is
+// added back; within a few units in the last place.
+QG_DEV float silu(float z) {
+    const float p = z * -1.44269504f;
+    const float e = __builtin_amdgcn_exp2f(p);
+    // (where e is infinite or zero, its correction would not be a number)
+    const float low = __builtin_fmaf(z, -1.44269504f, -p) + z * -1.925963033e-8f;
+    const float c = p < 126.f && p > -126.f ? __builtin_fmaf(e * 0.693147181f, low, e) : e;
+    return z * __builtin_amdgcn_rcpf(1.f + c);
 }
 
 struct QArgs {
@@ -153,28 +180,40 @@ __global__ __launch_bounds__(256) void quantize_f8_kernel(QArgs a) {
         const int b = (int)(at - n * a.quads) * 4 + (lane >> 4);
         float x[8];
         uint32_t mx = 0;  // the largest |x| by its bits: above every finite value an infinity, above it a NaN
+        if constexpr (!GATED && VN == 8) {
+            // 16-bit values in pairs
+            typedef uint16_t h2 __attribute__((ext_vector_type(2)));
+            h2 m = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                m = __builtin_elementwise_max(m, __builtin_bit_cast(h2, (&v[u][0].x)[e] & 0x7fff7fffu));
+            const uint4 one = make_uint4(max(m[0], m[1]), 0, 0, 0);
+            mx = __builtin_bit_cast(uint32_t, XVec<XT>::get(one, 0));
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[e] = XVec<XT>::get(v[u][e / VN], e % VN);
-            if constexpr (GATED) {
-                const float z = XVec<XT>::get(g[u][e / VN], e % VN);
-                x[e] *= z / (1.f + expf(-z));
-            }
-            mx = max(mx, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
+            if constexpr (GATED) x[e] *= silu(XVec<XT>::get(g[u][e / VN], e % VN));
+            if constexpr (GATED || VN == 4) mx = max(mx, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
         }
         mx = row_max(mx);
         const bool finite = mx < 0x7f800000u;
-        const float d0 = finite ? __builtin_bit_cast(float, mx) / 448.f : __builtin_nanf("");
-        const bool ok = d0 > 0.f;
-        // tiny scales: x and d scaled alike (exactly), so that 1/d stays finite
-        const float s = d0 < 0x1p-90f ? 0x1p60f : 1.f;
-        const float d = ok ? d0 * s : 1.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = ok ? x[e] * s : 0.f;
-        const uint2 o = quant8(x, d, 1.f / d);
+        const float top = __builtin_bit_cast(float, mx);
+        // top / 448 rounded to nearest: the product with 1/448 and its exact remainder's correction
+        const float q0 = top * (1.f / 448.f);
+        float d = __builtin_fmaf(__builtin_fmaf(-448.f, q0, top), 1.f / 448.f, q0);
+        const bool tiny = d < 0x1p-90f;  // (the remainder could be subnormal, and 1/d infinite)
+        if (tiny) d = top / 448.f;
+        if (!finite) d = __builtin_nanf("");
+        uint2 o = quant8(x, d, tiny ? 0.f : __builtin_amdgcn_rcpf(d));
+        if (__ballot(tiny && d > 0.f)) {
+            asm volatile("");
+            if (tiny && d > 0.f) o = quant8_tiny(x, d);
+        }
+        if (!(d > 0.f)) o = make_uint2(0, 0);
         const bool in = b * kB < a.K;
         if (in) *reinterpret_cast<uint2*>(a.q + n * a.ldq + b * kB + (lane & 15) * 8) = o;
-        if ((lane & 15) == 0) a.scale[n * a.lds + b] = in ? d0 : 0.f;
+        if ((lane & 15) == 0) a.scale[n * a.lds + b] = in ? d : 0.f;
     }
     }
 }
