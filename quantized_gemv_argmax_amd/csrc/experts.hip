@@ -6,6 +6,7 @@
 // bit map per expert, so a row's place among an expert's rows is a count of bits.
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include "qg_device.h"
@@ -28,26 +29,36 @@ struct SArgs {
 
 QG_DEV float neg_inf() { return -__builtin_inff(); }
 
-// One step of a reduction over a wavefront: lanes whose DPP source is out of range keep v.
-template <int CTRL, int ROWS>
-QG_DEV float dpp_step(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, v), __builtin_bit_cast(int, v), CTRL,
-                                                                 ROWS, 0xf, false));
+// Reductions over groups of 16 or 64 lanes, the result in all of them.
+template <int CTRL>
+QG_DEV int lane_swap(int v) {
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
 }
-// The largest of a value's 64 lanes (row shifts, then row 0 to 1 and 2 to 3, then 1 to the rest).
-QG_DEV float wave_max(float v) {
-    v = fmaxf(v, dpp_step<0x111, 0xf>(v));
-    v = fmaxf(v, dpp_step<0x112, 0xf>(v));
-    v = fmaxf(v, dpp_step<0x114, 0xf>(v));
-    v = fmaxf(v, dpp_step<0x118, 0xf>(v));
-    v = fmaxf(v, dpp_step<0x142, 0xa>(v));
-    v = fmaxf(v, dpp_step<0x143, 0xc>(v));
-    return qg_readlane(v, 63);
-}
-QG_DEV float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+template <int L, class F>
+QG_DEV int reduce(int v, F&& op) {
+    v = op(v, lane_swap<0xb1>(v));   // quad_perm [1, 0, 3, 2]
+    v = op(v, lane_swap<0x4e>(v));   // quad_perm [2, 3, 0, 1]
+    v = op(v, lane_swap<0x141>(v));  // row_half_mirror
+    v = op(v, lane_swap<0x140>(v));  // row_mirror
+    if constexpr (L == 64) {
+        v = op(v, __shfl_xor(v, 16));
+        v = op(v, __shfl_xor(v, 32));
+    }
     return v;
+}
+QG_DEV float as_float(int v) { return __builtin_bit_cast(float, v); }
+QG_DEV int as_int(float v) { return __builtin_bit_cast(int, v); }
+template <int L>
+QG_DEV float group_max(float v) {
+    return as_float(reduce<L>(as_int(v), [](int a, int b) { return as_int(fmaxf(as_float(a), as_float(b))); }));
+}
+template <int L>
+QG_DEV float group_sum(float v) {
+    return as_float(reduce<L>(as_int(v), [](int a, int b) { return as_int(as_float(a) + as_float(b)); }));
+}
+template <int L>
+QG_DEV int group_min(int v) {
+    return reduce<L>(v, [](int a, int b) { return min(a, b); });
 }
 QG_DEV int wave_scan(int v, int lane) {  // inclusive
 #pragma unroll
@@ -58,105 +69,131 @@ QG_DEV int wave_scan(int v, int lane) {  // inclusive
     return v;
 }
 
-// The k best of a row, in a wavefront: the maximum and its first place, k times. Lane j
-// gets the j-th (expert -1 where there are fewer) and its weight.
-template <int XT, int V>
-QG_DEV void select_row(const SArgs& a, int64_t n, int lane, int& expert, float& weight) {
-    typedef typename XVec<XT>::E E;
-    const E* p = reinterpret_cast<const E*>(a.z) + n * a.ld;
-    float z[V], top = neg_inf();
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        z[v] = neg_inf();
-        if (v * 64 + lane < a.E) z[v] = XVec<XT>::one(p[v * 64 + lane]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        z[v] = z[v] == z[v] ? fminf(z[v], FLT_MAX) : neg_inf();
-        top = fmaxf(top, z[v]);
-    }
-    expert = -1;
-    float mine = neg_inf(), first = neg_inf(), sum = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-        const float m = wave_max(top);
-        if (m == neg_inf()) break;
-        if (j == 0) {
-            first = m;
-            if (!a.normalize) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) sum += expf(z[v] - m);
-                sum = wave_sum(sum);
-            }
-        }
-        bool found = false;
-        top = neg_inf();
+// The k best of a row of logits, in L lanes of V each (logit v L + lane): the maximum and
+// its first place, k times. Lane j of the group gets the j-th and, beyond 16 lanes' worth, the
+// (j + 16)-th (expert -1 where there are fewer), with their weights.
+constexpr int kPer16 = QG_EXPERTS_MAX_K / 16;
+template <int XT, int L, int V>
+struct Row {
+    static constexpr int R = L == 64 ? 1 : kPer16;  // results of a lane
+    float z[V];
+    int expert[R];
+    float weight[R];
+    QG_DEV void load(const SArgs& a, int64_t n, int lane) {
+        typedef typename XVec<XT>::E E;
+        const E* p = reinterpret_cast<const E*>(a.z) + n * a.ld;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const uint64_t hit = found ? 0 : __ballot(z[v] == m);
-            if (hit) {
-                const int l = __builtin_ctzll(hit);
-                found = true;
-                if (lane == l) z[v] = neg_inf();
-                if (lane == j) {
-                    expert = v * 64 + l;
-                    mine = m;
-                }
-            }
-            top = fmaxf(top, z[v]);
+            z[v] = neg_inf();
+            if (v * L + lane < a.E) z[v] = XVec<XT>::one(p[v * L + lane]);
         }
     }
-    weight = expert >= 0 ? expf(mine - first) : 0.f;
-    if (a.normalize) sum = wave_sum(weight);
-    if (expert >= 0) weight = a.scale * (weight / sum);
-}
+    QG_DEV void select(const SArgs& a, int lane) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) z[v] = z[v] == z[v] ? fminf(z[v], FLT_MAX) : neg_inf();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            expert[r] = -1;
+            weight[r] = neg_inf();
+        }
+        float first = neg_inf(), sum = 0.f;
+        for (int j = 0; j < a.k; ++j) {
+            float m = z[0];
+#pragma unroll
+            for (int v = 1; v < V; ++v) m = fmaxf(m, z[v]);
+            m = group_max<L>(m);
+            if (j == 0) {
+                first = m;
+                if (!a.normalize) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) sum += z[v] > neg_inf() ? expf(z[v] - m) : 0.f;
+                    sum = group_sum<L>(sum);
+                }
+            }
+            int at = INT_MAX;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) at = z[v] == m ? v * L + lane : at;
+            at = group_min<L>(at);
+            const bool there = m > neg_inf();
+#pragma unroll
+            for (int v = 0; v < V; ++v) z[v] = v * L + lane == at ? neg_inf() : z[v];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (there && lane + 16 * r == j) {
+                    expert[r] = at;
+                    weight[r] = m;
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) weight[r] = expert[r] >= 0 ? expf(weight[r] - first) : 0.f;
+        if (a.normalize) {
+            float s = weight[0];
+#pragma unroll
+            for (int r = 1; r < R; ++r) s += weight[r];
+            sum = group_sum<L>(s);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (expert[r] >= 0) weight[r] = a.scale * (weight[r] / sum);
+    }
+};
 
-// 32 rows per workgroup, four at a time to a wavefront's turn. ONE: these are all rows,
-// and the order follows in the same launch; otherwise their words go to the bit map.
-constexpr int kRows = 32, kWaves = 8;
-template <int XT, int V, bool ONE>
-__global__ __launch_bounds__(64 * kWaves) void select_kernel(SArgs a) {
-    __shared__ uint32_t word[V * 64];
-    __shared__ int base[ONE ? V * 64 : 1], chosen[ONE ? kRows * QG_EXPERTS_MAX_K : 1], asked;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    for (int e = tid; e < V * 64; e += 64 * kWaves) word[e] = 0;
+// Rows of a workgroup: 32, their words to the bit map; or (ONE) all rows, up to 64, and
+// their order too. Four rows to a wavefront at a time, up to 256 experts, else one.
+constexpr int kOneRows = 64;
+template <int XT, int L, int V, bool ONE>
+__global__ __launch_bounds__(ONE ? 1024 : 512) void select_kernel(SArgs a) {
+    constexpr int W = ONE ? 2 : 1, ROWS = 32 * W, NT = ONE ? 1024 : 512, P = 64 / L, EP = V * L < 64 ? 64 : V * L;
+    __shared__ uint32_t word[EP * W];
+    __shared__ int base[ONE ? EP : 1], chosen[ONE ? ROWS * QG_EXPERTS_MAX_K : 1], asked;
+    const int tid = threadIdx.x, lane = tid & (L - 1), group = tid / L;
+    const int64_t n0 = (int64_t)blockIdx.x * ROWS;
+    const int rows = (int)min((int64_t)ROWS, a.N - n0);
+    Row<XT, L, V> row;
+    if (group < rows) row.load(a, n0 + group, lane);
+    for (int e = tid; e < EP * W; e += NT) word[e] = 0;
     __syncthreads();
-    const int64_t n0 = (int64_t)blockIdx.x * kRows;
-    for (int i = wave; i < kRows && n0 + i < a.N; i += kWaves) {
-        int expert;
-        float weight;
-        select_row<XT, V>(a, n0 + i, lane, expert, weight);
-        if (lane < a.k) {
-            const int64_t at = (n0 + i) * a.k + lane;
-            a.o.expert[at] = expert;
-            a.o.weight[at] = weight;
-            if constexpr (ONE) chosen[i * a.k + lane] = expert;
-            if (expert >= 0)
-                atomicOr(&word[expert], 1u << i);
-            else if constexpr (!ONE)
-                a.o.position[at] = -1;  // (the others' come with the order)
+    for (int i = group; i < rows; i += NT / L) {
+        if (i != group) row.load(a, n0 + i, lane);
+        row.select(a, lane);
+#pragma unroll
+        for (int r = 0; r < row.R; ++r) {
+            const int j = lane + 16 * r;
+            if (j < a.k && (L == 64 || lane < 16)) {
+                const int64_t at = (n0 + i) * a.k + j;
+                const int e = row.expert[r];
+                a.o.expert[at] = e;
+                a.o.weight[at] = row.weight[r];
+                if constexpr (ONE) chosen[i * a.k + j] = e;
+                if (e >= 0)
+                    atomicOr(&word[e * W + (i >> 5)], 1u << (i & 31));
+                else if constexpr (!ONE)
+                    a.o.position[at] = -1;  // (the others' come with the order)
+            }
         }
     }
     __syncthreads();
     if constexpr (!ONE) {
-        for (int e = tid; e < a.E; e += 64 * kWaves) a.bits[(int64_t)e * a.words + blockIdx.x] = word[e];
+        for (int e = tid; e < a.E; e += NT) a.bits[(int64_t)e * a.words + blockIdx.x] = word[e];
     } else {
-        if (wave == 0) {
+        if (tid < 64) {
             int carry = 0;
             for (int e0 = 0; e0 < a.E; e0 += 64) {
-                const int c = __popc(word[e0 + lane]), upto = wave_scan(c, lane) + carry;
-                base[e0 + lane] = upto - c;
-                if (e0 + lane < a.E) a.o.offsets[e0 + lane] = upto - c;
+                const int e = e0 + tid, c = __popc(word[e * W]) + __popc(word[e * W + 1]), upto = wave_scan(c, tid) + carry;
+                base[e] = upto - c;
+                if (e < a.E) a.o.offsets[e] = upto - c;
                 carry = __builtin_amdgcn_readlane(upto, 63);
             }
-            if (lane == 0) a.o.offsets[a.E] = asked = carry;
+            if (tid == 0) a.o.offsets[a.E] = asked = carry;
         }
         __syncthreads();
         const int all = a.N * a.k;
-        for (int i = tid; i < all; i += 64 * kWaves) {
+        for (int i = tid; i < all; i += NT) {
             const int e = chosen[i], n = i / a.k;
             int at = -1;
             if (e >= 0) {
-                at = base[e] + __popc(word[e] & ((1u << n) - 1));
+                at = base[e] + __popc(word[e * W + (n >> 5)] & ((1u << (n & 31)) - 1));
+                if (n >= 32) at += __popc(word[e * W]);
                 a.o.row[at] = n;
             }
             a.o.position[i] = at;
@@ -169,27 +206,29 @@ __global__ __launch_bounds__(64 * kWaves) void select_kernel(SArgs a) {
 // experts before it end; its own bits become a list of rows, a chunk of words at a time.
 template <int NT>
 __global__ __launch_bounds__(NT) void order_kernel(SArgs a) {
+    constexpr int C = 256;  // words of a chunk
     __shared__ int red[NT / 64];
-    __shared__ int list[NT * 32];
+    __shared__ int list[C * 32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, e = blockIdx.x;
     const int64_t before = (int64_t)e * a.words;
+    uint32_t bits = tid < C && tid < a.words ? a.bits[before + tid] : 0;  // (on their way while the others are counted)
     int sum = 0;
     const uint4* b4 = reinterpret_cast<const uint4*>(a.bits);
+#pragma unroll 4
     for (int64_t i = tid; i < before / 4; i += NT) {
         const uint4 v = b4[i];
         sum += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
     }
     if (tid < (int)(before & 3)) sum += __popc(a.bits[before - 1 - tid]);
-#pragma unroll
-    for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
+    sum = reduce<64>(sum, [](int x, int y) { return x + y; });
     if (lane == 0) red[wave] = sum;
     __syncthreads();
     int at = 0;
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w) at += red[w];
     if (tid == 0) a.o.offsets[e] = at;
-    for (int w0 = 0; w0 < a.words; w0 += NT) {
-        uint32_t bits = w0 + tid < a.words ? a.bits[before + w0 + tid] : 0;
+    for (int w0 = 0; w0 < a.words; w0 += C) {
+        if (w0) bits = tid < C && w0 + tid < a.words ? a.bits[before + w0 + tid] : 0;
         const int c = __popc(bits);
         int upto = wave_scan(c, lane);
         __syncthreads();  // (red and list of the step before have been read)
@@ -197,7 +236,7 @@ __global__ __launch_bounds__(NT) void order_kernel(SArgs a) {
         __syncthreads();
         int all = 0;
 #pragma unroll
-        for (int w = 0; w < NT / 64; ++w) {
+        for (int w = 0; w < C / 64; ++w) {
             if (w < wave) upto += red[w];
             all += red[w];
         }
@@ -211,6 +250,7 @@ __global__ __launch_bounds__(NT) void order_kernel(SArgs a) {
             const int n = list[i];
             a.o.row[at + i] = n;
             const int64_t p = (int64_t)n * a.k;
+#pragma unroll 8
             for (int j = 0; j < a.k; ++j)
                 if (a.o.expert[p + j] == e) a.o.position[p + j] = at + i;
         }
@@ -222,23 +262,23 @@ __global__ __launch_bounds__(NT) void order_kernel(SArgs a) {
     }
 }
 
-template <int XT, int V>
+template <int XT, int L, int V>
 void launch_select(const SArgs& a, hipStream_t s) {
-    if (a.N <= kRows)
-        hipLaunchKernelGGL((select_kernel<XT, V, true>), dim3(1), dim3(64 * kWaves), 0, s, a);
+    if (a.N <= kOneRows)
+        hipLaunchKernelGGL((select_kernel<XT, L, V, true>), dim3(1), dim3(1024), 0, s, a);
     else
-        hipLaunchKernelGGL((select_kernel<XT, V, false>), dim3((unsigned)qg::ceil_div(a.N, kRows)), dim3(64 * kWaves), 0, s, a);
+        hipLaunchKernelGGL((select_kernel<XT, L, V, false>), dim3((unsigned)a.words), dim3(512), 0, s, a);
 }
 template <int XT>
 void launch_select(const SArgs& a, hipStream_t s) {
     if (a.E <= 64)
-        launch_select<XT, 1>(a, s);
+        launch_select<XT, 16, 4>(a, s);
     else if (a.E <= 128)
-        launch_select<XT, 2>(a, s);
+        launch_select<XT, 16, 8>(a, s);
     else if (a.E <= 256)
-        launch_select<XT, 4>(a, s);
+        launch_select<XT, 16, 16>(a, s);
     else
-        launch_select<XT, QG_EXPERTS_MAX / 64>(a, s);
+        launch_select<XT, 64, QG_EXPERTS_MAX / 64>(a, s);
 }
 
 // ---------------------------------------------------------------- combination
@@ -345,7 +385,7 @@ bool select_shape(int64_t N, int E, int k) {
     return E >= 1 && E <= QG_EXPERTS_MAX && k >= 1 && k <= E && k <= QG_EXPERTS_MAX_K && N >= 1 && N <= QG_F8_MAX_ROWS / k;
 }
 size_t select_ws(int64_t N, int E) {
-    return N <= kRows ? 0 : qg::align_up((size_t)E * (size_t)qg::ceil_div(N, 32) * 4, 16);
+    return N <= kOneRows ? 0 : qg::align_up((size_t)E * (size_t)qg::ceil_div(N, 32) * 4, 16);
 }
 
 }  // namespace
@@ -403,7 +443,7 @@ qg_status logits_expert_select(const void* logits, int logits_type, int64_t ld, 
         launch_select<QG_BF16>(a, s);
     st = qg::launch_status("logits_expert_select");
     if (st || !need) return st;
-    hipLaunchKernelGGL((order_kernel<256>), dim3(E), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((order_kernel<512>), dim3(E), dim3(512), 0, s, a);
     return qg::launch_status("logits_expert_select (order)");
 }
 
