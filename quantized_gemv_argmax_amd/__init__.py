@@ -1113,11 +1113,10 @@ class ExpertSelection:
     (int32), (N, k) each, row (int32, N * k) and offsets (int32, experts + 1)."""
 
     def __init__(self, N: int, E: int, k: int, device):
-        whole = torch.empty_strided((4 * N * k + E + 1,), (1,), dtype=torch.int32, device=device)
-        n = N * k
-        self.expert, self.position = whole[:n].view(N, k), whole[n:2 * n].view(N, k)
-        self.weight = whole[2 * n:3 * n].view(torch.float32).view(N, k)
-        self.row, self.offsets = whole[3 * n:4 * n], whole[4 * n:]
+        self.expert, self.position = torch.empty_strided((2, N, k), (N * k, k, 1), dtype=torch.int32, device=device).unbind()
+        self.weight = torch.empty_strided((N, k), (k, 1), dtype=torch.float32, device=device)
+        self.row = torch.empty_strided((N * k,), (1,), dtype=torch.int32, device=device)
+        self.offsets = torch.empty_strided((E + 1,), (1,), dtype=torch.int32, device=device)
 
 
 def logits_expert_select(logits: torch.Tensor, k: int, normalize: bool = False, scale: float = 1.0,
