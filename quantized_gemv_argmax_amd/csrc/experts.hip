@@ -21,44 +21,38 @@ using namespace qg;
 struct SArgs {
     const void* z;
     int64_t ld;
-    int32_t N, E, k, normalize, words;  // words of an expert's bit map
+    int32_t N, E, k, normalize;
+    int32_t words, parts, per;  // words of an expert's bit map, its parts (1: not counted), words of one
     float scale;
     uint32_t* bits;  // [E][words]
+    int32_t* counts;  // [E][parts]
     qg_experts_out o;
 };
 
 QG_DEV float neg_inf() { return -__builtin_inff(); }
 
-// Reductions over groups of 16 or 64 lanes, the result in all of them.
+// Reductions over groups of 16 lanes, the result in all of them.
 template <int CTRL>
 QG_DEV int lane_swap(int v) {
     return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
 }
-template <int L, class F>
+template <class F>
 QG_DEV int reduce(int v, F&& op) {
     v = op(v, lane_swap<0xb1>(v));   // quad_perm [1, 0, 3, 2]
     v = op(v, lane_swap<0x4e>(v));   // quad_perm [2, 3, 0, 1]
     v = op(v, lane_swap<0x141>(v));  // row_half_mirror
-    v = op(v, lane_swap<0x140>(v));  // row_mirror
-    if constexpr (L == 64) {
-        v = op(v, __shfl_xor(v, 16));
-        v = op(v, __shfl_xor(v, 32));
-    }
-    return v;
+    return op(v, lane_swap<0x140>(v));  // row_mirror
 }
 QG_DEV float as_float(int v) { return __builtin_bit_cast(float, v); }
 QG_DEV int as_int(float v) { return __builtin_bit_cast(int, v); }
-template <int L>
 QG_DEV float group_max(float v) {
-    return as_float(reduce<L>(as_int(v), [](int a, int b) { return as_int(fmaxf(as_float(a), as_float(b))); }));
+    return as_float(reduce(as_int(v), [](int a, int b) { return as_int(fmaxf(as_float(a), as_float(b))); }));
 }
-template <int L>
 QG_DEV float group_sum(float v) {
-    return as_float(reduce<L>(as_int(v), [](int a, int b) { return as_int(as_float(a) + as_float(b)); }));
+    return as_float(reduce(as_int(v), [](int a, int b) { return as_int(as_float(a) + as_float(b)); }));
 }
-template <int L>
 QG_DEV int group_min(int v) {
-    return reduce<L>(v, [](int a, int b) { return min(a, b); });
+    return reduce(v, [](int a, int b) { return min(a, b); });
 }
 QG_DEV int wave_scan(int v, int lane) {  // inclusive
 #pragma unroll
@@ -69,13 +63,15 @@ QG_DEV int wave_scan(int v, int lane) {  // inclusive
     return v;
 }
 
-// The k best of a row of logits, in L lanes of V each (logit v L + lane): the maximum and
-// its first place, k times. Lane j of the group gets the j-th and, beyond 16 lanes' worth, the
-// (j + 16)-th (expert -1 where there are fewer), with their weights.
-constexpr int kPer16 = QG_EXPERTS_MAX_K / 16;
-template <int XT, int L, int V>
+// The k best of a row of logits z, in 16 lanes of V each (logit 16 v + lane): the maximum and
+// its first place, k times, each a reduction within 16 lanes, which costs less than one over 64 (E = 512,
+// 4096 rows: the row in 16 lanes 20 us in all, in 64 lanes 35). Lane j gets the j-th and the (j + 16)-th
+// (expert -1 where there are fewer) with their weights exp(z - max) / sum, the sum over
+// the chosen ones or over all.
+constexpr int L = 16;
+template <int XT, int V>
 struct Row {
-    static constexpr int R = L == 64 ? 1 : kPer16;  // results of a lane
+    static constexpr int R = QG_EXPERTS_MAX_K / L;  // results of a lane
     float z[V];
     int expert[R];
     float weight[R];
@@ -101,25 +97,26 @@ struct Row {
             float m = z[0];
 #pragma unroll
             for (int v = 1; v < V; ++v) m = fmaxf(m, z[v]);
-            m = group_max<L>(m);
+            m = group_max(m);
             if (j == 0) {
                 first = m;
                 if (!a.normalize) {
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int v = 0; v < V; ++v) sum += z[v] > neg_inf() ? expf(z[v] - m) : 0.f;
-                    sum = group_sum<L>(sum);
+                    for (int v = 0; v < V; ++v) part[v & 3] += z[v] > neg_inf() ? expf(z[v] - m) : 0.f;
+                    sum = group_sum((part[0] + part[1]) + (part[2] + part[3]));
                 }
             }
             int at = INT_MAX;
 #pragma unroll
             for (int v = V - 1; v >= 0; --v) at = z[v] == m ? v * L + lane : at;
-            at = group_min<L>(at);
+            at = group_min(at);
             const bool there = m > neg_inf();
 #pragma unroll
             for (int v = 0; v < V; ++v) z[v] = v * L + lane == at ? neg_inf() : z[v];
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if (there && lane + 16 * r == j) {
+                if (there && lane + L * r == j) {
                     expert[r] = at;
                     weight[r] = m;
                 }
@@ -130,7 +127,7 @@ struct Row {
             float s = weight[0];
 #pragma unroll
             for (int r = 1; r < R; ++r) s += weight[r];
-            sum = group_sum<L>(s);
+            sum = group_sum(s);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -139,17 +136,19 @@ struct Row {
 };
 
 // Rows of a workgroup: 32, their words to the bit map; or (ONE) all rows, up to 64, and
-// their order too. Four rows to a wavefront at a time, up to 256 experts, else one.
+// their order too, which saves a launch (45 x 37, 3 of them: 4.7 us, in two launches 10).
+// Bounded by the chain of k maxima: 4096 x 128, 8 of them, takes 11.4 us in all, 0.4
+// of them to read the logits.
 constexpr int kOneRows = 64;
-template <int XT, int L, int V, bool ONE>
+template <int XT, int V, bool ONE>
 __global__ __launch_bounds__(ONE ? 1024 : 512) void select_kernel(SArgs a) {
-    constexpr int W = ONE ? 2 : 1, ROWS = 32 * W, NT = ONE ? 1024 : 512, P = 64 / L, EP = V * L < 64 ? 64 : V * L;
+    constexpr int W = ONE ? 2 : 1, ROWS = 32 * W, NT = ONE ? 1024 : 512, EP = V * L;
     __shared__ uint32_t word[EP * W];
     __shared__ int base[ONE ? EP : 1], chosen[ONE ? ROWS * QG_EXPERTS_MAX_K : 1], asked;
     const int tid = threadIdx.x, lane = tid & (L - 1), group = tid / L;
     const int64_t n0 = (int64_t)blockIdx.x * ROWS;
     const int rows = (int)min((int64_t)ROWS, a.N - n0);
-    Row<XT, L, V> row;
+    Row<XT, V> row;
     if (group < rows) row.load(a, n0 + group, lane);
     for (int e = tid; e < EP * W; e += NT) word[e] = 0;
     __syncthreads();
@@ -158,8 +157,8 @@ __global__ __launch_bounds__(ONE ? 1024 : 512) void select_kernel(SArgs a) {
         row.select(a, lane);
 #pragma unroll
         for (int r = 0; r < row.R; ++r) {
-            const int j = lane + 16 * r;
-            if (j < a.k && (L == 64 || lane < 16)) {
+            const int j = lane + L * r;
+            if (j < a.k) {
                 const int64_t at = (n0 + i) * a.k + j;
                 const int e = row.expert[r];
                 a.o.expert[at] = e;
@@ -202,33 +201,64 @@ __global__ __launch_bounds__(ONE ? 1024 : 512) void select_kernel(SArgs a) {
     }
 }
 
+// Sums over a workgroup, the result in all threads. (A barrier first: `red` may be in use.)
+template <int NT>
+QG_DEV int group_total(int v, int* red) {
+    v = reduce(v, [](int x, int y) { return x + y; });
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) v += red[w];
+    return v;
+}
+
+// Rows of expert blockIdx.x in part blockIdx.y of its words.
+constexpr int kOrder = 512, kChunk = 256;  // threads, words of a chunk
+__global__ __launch_bounds__(256) void count_kernel(SArgs a) {
+    __shared__ int red[4];
+    const int e = blockIdx.x, part = blockIdx.y, w0 = part * a.per;
+    int sum = 0;
+    for (int w = w0 + threadIdx.x; w < min(w0 + a.per, a.words); w += 256) sum += __popc(a.bits[(int64_t)e * a.words + w]);
+    sum = group_total<256>(sum, red);
+    if (threadIdx.x == 0) a.counts[e * a.parts + part] = sum;
+}
+
 // The order by expert, a workgroup per expert: its rows begin where the bits of all
 // experts before it end; its own bits become a list of rows, a chunk of words at a time.
-template <int NT>
-__global__ __launch_bounds__(NT) void order_kernel(SArgs a) {
-    constexpr int C = 256;  // words of a chunk
+// With more than a chunk to an expert, a workgroup per part of its words, whose rows begin where the
+// counts of the parts before end: a launch more, but no reading that grows with the square of the experts
+// (16384 x 256: 22.8 us, without counts 26.7; 131072 x 512: 171 and 377; 524288 x 64: 121 and 296).
+template <bool PARTS>
+__global__ __launch_bounds__(kOrder) void order_kernel(SArgs a) {
+    constexpr int C = kChunk, NT = kOrder;
     __shared__ int red[NT / 64];
     __shared__ int list[C * 32];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, e = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, e = blockIdx.x, part = PARTS ? blockIdx.y : 0;
+    const int begin = PARTS ? part * a.per : 0, end = PARTS ? min(begin + a.per, a.words) : a.words;
     const int64_t before = (int64_t)e * a.words;
-    uint32_t bits = tid < C && tid < a.words ? a.bits[before + tid] : 0;  // (on their way while the others are counted)
-    int sum = 0;
-    const uint4* b4 = reinterpret_cast<const uint4*>(a.bits);
+    uint32_t bits = tid < C && begin + tid < end ? a.bits[before + begin + tid] : 0;  // (on their way while the others are counted)
+    int sum = 0, rest = 0;
+    if constexpr (PARTS) {
+        const int mine = e * a.parts + part;
+        for (int i = tid; i < a.E * a.parts; i += NT) (i < mine ? sum : rest) += a.counts[i];
+    } else {
+        const uint4* b4 = reinterpret_cast<const uint4*>(a.bits);
 #pragma unroll 4
-    for (int64_t i = tid; i < before / 4; i += NT) {
-        const uint4 v = b4[i];
-        sum += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+        for (int64_t i = tid; i < before / 4; i += NT) {
+            const uint4 v = b4[i];
+            sum += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+        }
+        if (tid < (int)(before & 3)) sum += __popc(a.bits[before - 1 - tid]);
     }
-    if (tid < (int)(before & 3)) sum += __popc(a.bits[before - 1 - tid]);
-    sum = reduce<64>(sum, [](int x, int y) { return x + y; });
-    if (lane == 0) red[wave] = sum;
-    __syncthreads();
-    int at = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 64; ++w) at += red[w];
-    if (tid == 0) a.o.offsets[e] = at;
-    for (int w0 = 0; w0 < a.words; w0 += C) {
-        if (w0) bits = tid < C && w0 + tid < a.words ? a.bits[before + w0 + tid] : 0;
+    int at = group_total<NT>(sum, red);
+    const int asked = PARTS ? at + group_total<NT>(rest, red) : 0;  // rows of all experts
+    if (tid == 0 && part == 0) a.o.offsets[e] = at;
+    for (int w0 = begin; w0 < end; w0 += C) {
+        if (w0 > begin) bits = tid < C && w0 + tid < end ? a.bits[before + w0 + tid] : 0;
         const int c = __popc(bits);
         int upto = wave_scan(c, lane);
         __syncthreads();  // (red and list of the step before have been read)
@@ -256,29 +286,35 @@ __global__ __launch_bounds__(NT) void order_kernel(SArgs a) {
         }
         at += all;
     }
-    if (e == a.E - 1) {
+    // nothing behind the last expert's rows
+    if constexpr (PARTS) {
+        if (tid == 0 && e == 0 && part == 0) a.o.offsets[a.E] = asked;
+        for (int i = asked + (e * a.parts + part) * NT + tid; i < a.N * a.k; i += a.E * a.parts * NT) a.o.row[i] = -1;
+    } else if (e == a.E - 1) {
         if (tid == 0) a.o.offsets[a.E] = at;
         for (int i = at + tid; i < a.N * a.k; i += NT) a.o.row[i] = -1;
     }
 }
 
-template <int XT, int L, int V>
+template <int XT, int V>
 void launch_select(const SArgs& a, hipStream_t s) {
     if (a.N <= kOneRows)
-        hipLaunchKernelGGL((select_kernel<XT, L, V, true>), dim3(1), dim3(1024), 0, s, a);
+        hipLaunchKernelGGL((select_kernel<XT, V, true>), dim3(1), dim3(1024), 0, s, a);
     else
-        hipLaunchKernelGGL((select_kernel<XT, L, V, false>), dim3((unsigned)a.words), dim3(512), 0, s, a);
+        hipLaunchKernelGGL((select_kernel<XT, V, false>), dim3((unsigned)a.words), dim3(512), 0, s, a);
 }
 template <int XT>
 void launch_select(const SArgs& a, hipStream_t s) {
     if (a.E <= 64)
-        launch_select<XT, 16, 4>(a, s);
+        launch_select<XT, 4>(a, s);
     else if (a.E <= 128)
-        launch_select<XT, 16, 8>(a, s);
+        launch_select<XT, 8>(a, s);
     else if (a.E <= 256)
-        launch_select<XT, 16, 16>(a, s);
+        launch_select<XT, 16>(a, s);
+    else if (a.E <= 512)
+        launch_select<XT, 32>(a, s);
     else
-        launch_select<XT, 64, QG_EXPERTS_MAX / 64>(a, s);
+        launch_select<XT, QG_EXPERTS_MAX / L>(a, s);
 }
 
 // ---------------------------------------------------------------- combination
@@ -384,8 +420,11 @@ void launch_combine(const CArgs& a, int out_type, hipStream_t s) {
 bool select_shape(int64_t N, int E, int k) {
     return E >= 1 && E <= QG_EXPERTS_MAX && k >= 1 && k <= E && k <= QG_EXPERTS_MAX_K && N >= 1 && N <= QG_F8_MAX_ROWS / k;
 }
+// Parts of an expert's words: whole chunks, and counts that every workgroup can sum.
+int select_parts(int64_t words, int E) { return (int)std::min<int64_t>(qg::ceil_div(words, kChunk), std::max(1, 4096 / E)); }
+size_t select_bits(int64_t N, int E) { return qg::align_up((size_t)E * (size_t)qg::ceil_div(N, 32) * 4, 16); }
 size_t select_ws(int64_t N, int E) {
-    return N <= kOneRows ? 0 : qg::align_up((size_t)E * (size_t)qg::ceil_div(N, 32) * 4, 16);
+    return N <= kOneRows ? 0 : select_bits(N, E) + qg::align_up((size_t)E * select_parts(qg::ceil_div(N, 32), E) * 4, 16);
 }
 
 }  // namespace
@@ -433,7 +472,11 @@ qg_status logits_expert_select(const void* logits, int logits_type, int64_t ld, 
     }
     qg_status st = qg::check_device();
     if (st) return st;
-    const SArgs a{logits, ld, (int32_t)N, E, k, normalize, (int32_t)qg::ceil_div(N, 32), scale, (uint32_t*)workspace, *out};
+    const int64_t words = qg::ceil_div(N, 32);
+    const int parts = select_parts(words, E);
+    const int per = (int)qg::align_up((size_t)qg::ceil_div(words, parts), kChunk);
+    const SArgs a{logits, ld, (int32_t)N, E, k, normalize, (int32_t)words, parts, per, scale, (uint32_t*)workspace,
+                  (int32_t*)((char*)workspace + select_bits(N, E)), *out};
     hipStream_t s = (hipStream_t)stream;
     if (logits_type == QG_F32)
         launch_select<QG_F32>(a, s);
@@ -443,7 +486,14 @@ qg_status logits_expert_select(const void* logits, int logits_type, int64_t ld, 
         launch_select<QG_BF16>(a, s);
     st = qg::launch_status("logits_expert_select");
     if (st || !need) return st;
-    hipLaunchKernelGGL((order_kernel<512>), dim3(E), dim3(512), 0, s, a);
+    if (parts == 1) {
+        hipLaunchKernelGGL((order_kernel<false>), dim3(E), dim3(kOrder), 0, s, a);
+    } else {
+        hipLaunchKernelGGL(count_kernel, dim3(E, parts), dim3(256), 0, s, a);
+        st = qg::launch_status("logits_expert_select (count)");
+        if (st) return st;
+        hipLaunchKernelGGL((order_kernel<true>), dim3(E, parts), dim3(kOrder), 0, s, a);
+    }
     return qg::launch_status("logits_expert_select (order)");
 }
 

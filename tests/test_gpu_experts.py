@@ -69,6 +69,17 @@ def test_select_masks_and_ties(N):
     check_select(one, 4, True, 1.0, f"logits_expert_select one expert N={N}")
 
 
+@pytest.mark.parametrize("N,E,k", [(8193, 512, 3), (20011, 300, 4), (16385, 1024, 2), (70001, 37, 5)])
+def test_select_long(N, E, k):
+    """Rows whose expert's words are counted and ordered in parts, the last ones ragged, some rows masked."""
+    g = torch.Generator(device=DEV).manual_seed(N)
+    z = torch.randn(N, E, generator=g, device=DEV).half()
+    z[:, 1] += 3                                 # one expert with most rows
+    z[:, E - 1] = -float("inf")                  # and one with none
+    z[N // 3: N // 2] = -float("inf")            # padding: the rows behind the last are told by -1
+    check_select(z, k, N % 2 == 0, 1.0, f"logits_expert_select long N={N} E={E} k={k}")
+
+
 def test_select_strided_rows_and_own_outputs():
     base = torch.randn(50, 203, device=DEV).bfloat16()
     check_select(base[:, 3:163], 6, True, 1.0, "logits_expert_select strided")
