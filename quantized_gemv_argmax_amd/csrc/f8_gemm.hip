@@ -154,67 +154,67 @@ __global__ __launch_bounds__(256) void quantize_f8_kernel(QArgs a) {
     const uint32_t rows = a.count ? min(max(*a.count, 0), a.N) : a.N;
     const uint32_t total = rows * a.quads;  // below 2^31
     for (uint32_t first = (blockIdx.x * 4 + wave) * U; first < total; first += gridDim.x * 4 * U) {
-    uint4 v[U][V], g[GATED ? U : 1][V];
+        uint4 v[U][V], g[GATED ? U : 1][V];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t at = first + u;
-        if (at < total) {
-            const uint32_t n = at / a.quads;
-            const int k = (int)(at - n * a.quads) * 4 * kB + lane * 8;
-            const E* p = reinterpret_cast<const E*>(a.x) + n * a.ldx;
+        for (int u = 0; u < U; ++u) {
+            const uint32_t at = first + u;
+            if (at < total) {
+                const uint32_t n = at / a.quads;
+                const int k = (int)(at - n * a.quads) * 4 * kB + lane * 8;
+                const E* p = reinterpret_cast<const E*>(a.x) + n * a.ldx;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                v[u][i] = row_vec<XT>(p, a.K, k / VN + i);
-                if constexpr (GATED) {
-                    g[u][i] = v[u][i];
-                    v[u][i] = row_vec<XT>(p + a.K, a.K, k / VN + i);
+                for (int i = 0; i < V; ++i) {
+                    v[u][i] = row_vec<XT>(p, a.K, k / VN + i);
+                    if constexpr (GATED) {
+                        g[u][i] = v[u][i];
+                        v[u][i] = row_vec<XT>(p + a.K, a.K, k / VN + i);
+                    }
                 }
             }
         }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t at = first + u;
-        if (at >= total) return;
-        const uint32_t n = at / a.quads;
-        const int b = (int)(at - n * a.quads) * 4 + (lane >> 4);
-        float x[8];
-        uint32_t mx = 0;  // the largest |x| by its bits: above every finite value an infinity, above it a NaN
-        if constexpr (!GATED && VN == 8) {
-            // 16-bit values in pairs
-            typedef uint16_t h2 __attribute__((ext_vector_type(2)));
-            h2 m = {0, 0};
+        for (int u = 0; u < U; ++u) {
+            const uint32_t at = first + u;
+            if (at >= total) return;
+            const uint32_t n = at / a.quads;
+            const int b = (int)(at - n * a.quads) * 4 + (lane >> 4);
+            float x[8];
+            uint32_t mx = 0;  // the largest |x| by its bits: above every finite value an infinity, above it a NaN
+            if constexpr (!GATED && VN == 8) {
+                // 16-bit values in pairs
+                typedef uint16_t h2 __attribute__((ext_vector_type(2)));
+                h2 m = {0, 0};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                m = __builtin_elementwise_max(m, __builtin_bit_cast(h2, (&v[u][0].x)[e] & 0x7fff7fffu));
-            const uint4 one = make_uint4(max(m[0], m[1]), 0, 0, 0);
-            mx = __builtin_bit_cast(uint32_t, XVec<XT>::get(one, 0));
-        }
+                for (int e = 0; e < 4; ++e)
+                    m = __builtin_elementwise_max(m, __builtin_bit_cast(h2, (&v[u][0].x)[e] & 0x7fff7fffu));
+                const uint4 one = make_uint4(max(m[0], m[1]), 0, 0, 0);
+                mx = __builtin_bit_cast(uint32_t, XVec<XT>::get(one, 0));
+            }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = XVec<XT>::get(v[u][e / VN], e % VN);
-            if constexpr (GATED) x[e] *= silu(XVec<XT>::get(g[u][e / VN], e % VN));
-            if constexpr (GATED || VN == 4) mx = max(mx, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
+            for (int e = 0; e < 8; ++e) {
+                x[e] = XVec<XT>::get(v[u][e / VN], e % VN);
+                if constexpr (GATED) x[e] *= silu(XVec<XT>::get(g[u][e / VN], e % VN));
+                if constexpr (GATED || VN == 4) mx = max(mx, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
+            }
+            mx = row_max(mx);
+            const bool finite = mx < 0x7f800000u;
+            const float top = __builtin_bit_cast(float, mx);
+            // top / 448 rounded to nearest: the product with 1/448 and its exact remainder's correction
+            const float q0 = top * (1.f / 448.f);
+            float d = __builtin_fmaf(__builtin_fmaf(-448.f, q0, top), 1.f / 448.f, q0);
+            const bool tiny = d < 0x1p-90f;  // (the remainder could be subnormal, and 1/d infinite)
+            if (tiny) d = top / 448.f;
+            if (!finite) d = __builtin_nanf("");
+            uint2 o = quant8(x, d, tiny ? 0.f : __builtin_amdgcn_rcpf(d));
+            if (__ballot(tiny && d > 0.f)) {
+                asm volatile("");
+                if (tiny && d > 0.f) o = quant8_tiny(x, d);
+            }
+            if (!(d > 0.f)) o = make_uint2(0, 0);
+            const bool in = b * kB < a.K;
+            if (in) *reinterpret_cast<uint2*>(a.q + n * a.ldq + b * kB + (lane & 15) * 8) = o;
+            if ((lane & 15) == 0) a.scale[n * a.lds + b] = in ? d : 0.f;
         }
-        mx = row_max(mx);
-        const bool finite = mx < 0x7f800000u;
-        const float top = __builtin_bit_cast(float, mx);
-        // top / 448 rounded to nearest: the product with 1/448 and its exact remainder's correction
-        const float q0 = top * (1.f / 448.f);
-        float d = __builtin_fmaf(__builtin_fmaf(-448.f, q0, top), 1.f / 448.f, q0);
-        const bool tiny = d < 0x1p-90f;  // (the remainder could be subnormal, and 1/d infinite)
-        if (tiny) d = top / 448.f;
-        if (!finite) d = __builtin_nanf("");
-        uint2 o = quant8(x, d, tiny ? 0.f : __builtin_amdgcn_rcpf(d));
-        if (__ballot(tiny && d > 0.f)) {
-            asm volatile("");
-            if (tiny && d > 0.f) o = quant8_tiny(x, d);
-        }
-        if (!(d > 0.f)) o = make_uint2(0, 0);
-        const bool in = b * kB < a.K;
-        if (in) *reinterpret_cast<uint2*>(a.q + n * a.ldq + b * kB + (lane & 15) * 8) = o;
-        if ((lane & 15) == 0) a.scale[n * a.lds + b] = in ? d : 0.f;
-    }
     }
 }
 
@@ -327,56 +327,47 @@ QG_DEV void row_bias(const GArgs& a, int e, int m, float (&sb)[C]) {
 }
 
 // ---------------------------------------------------------------- few rows
-// One 16-row tile of an expert's weights and NB blocks of 16 rows of Y per workgroup; its
-// KW wavefronts take blocks of K in turn, and their sums meet in LDS, in order. The
-// weights go from memory straight to registers, in the packed order.
-template <int YT, int NB, int KW>
-__global__ __launch_bounds__(64 * KW) void gemm_f8_stream_kernel(GArgs a) {
-    __shared__ qg_f4 part[KW][NB][64];
+// One 16-row tile of an expert's weights and 16 rows of Y after the other per workgroup; its
+// wavefronts take blocks of K in turn, and their sums meet in LDS, in order. The weights go
+// from memory straight to registers, in the packed order, and are what bounds it.
+constexpr int kStreamWaves = 8;
+template <int YT>
+__global__ __launch_bounds__(64 * kStreamWaves) void gemm_f8_stream_kernel(GArgs a) {
+    constexpr int W = kStreamWaves;
+    __shared__ qg_f4 part[W][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = blockIdx.x, slot = blockIdx.y;
     Group g = {0, 0, a.N};
     if (a.offsets && !used_group(a, slot, g)) return;
     const uint8_t* w = a.w + ((size_t)g.e * a.mtiles + t) * a.nb * kUnit + lane * 16;
     const float* ws = a.ws + ((size_t)g.e * a.mb + t * T / kB) * a.nb;
-    for (int c0 = g.r0; c0 < g.r1; c0 += 16 * NB) {
-        const uint8_t* xr[NB];
-        const float* sr[NB];
-#pragma unroll
-        for (int c = 0; c < NB; ++c) {  // rows beyond the last repeat it; their sums are not stored
-            const int64_t r = source_row(a, min(c0 + 16 * c + (lane & 15), g.r1 - 1));
-            xr[c] = a.x + r * a.ldx + (lane >> 4) * 16;
-            sr[c] = a.xs + r * a.ldxs;
-        }
-        qg_f4 acc[NB];
-#pragma unroll
-        for (int c = 0; c < NB; ++c) acc[c] = qg_f4{0.f, 0.f, 0.f, 0.f};
-        Op8 wv[2], xv[2][NB];
-        float sv[2][NB];
+    for (int c0 = g.r0; c0 < g.r1; c0 += 16) {
+        // (rows beyond the last repeat it; their sums are not stored)
+        const int n = c0 + (lane & 15);
+        const int64_t r = source_row(a, min(n, g.r1 - 1));
+        const uint8_t* const xr = a.x + r * a.ldx + (lane >> 4) * 16;
+        const float* const sr = a.xs + r * a.ldxs;
+        qg_f4 acc = {0.f, 0.f, 0.f, 0.f};
+        Op8 wv[2], xv[2];
+        float sv[2];
         auto load = [&](int p, int b) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
                 wv[p].h[h] = __builtin_nontemporal_load(reinterpret_cast<const qi4*>(w + (size_t)b * kUnit + h * 1024));
-#pragma unroll
-            for (int c = 0; c < NB; ++c) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) xv[p][c].h[h] = *reinterpret_cast<const qi4*>(xr[c] + b * kB + h * 64);
-                sv[p][c] = sr[c][b] * ws[b];
+                xv[p].h[h] = *reinterpret_cast<const qi4*>(xr + b * kB + h * 64);
             }
+            sv[p] = sr[b] * ws[b];
         };
         auto mma = [&](int p) {
             Op16 wh, xh;
             wh.set(wv[p]);
-#pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                xh.set(xv[p][c]);
-                add_scaled(acc[c], block_sum(wh, xh), sv[p][c]);
-            }
+            xh.set(xv[p]);
+            add_scaled(acc, block_sum(wh, xh), sv[p]);
         };
         int b = wave;
-        for (; b + KW < a.nb; b += 2 * KW) {
+        for (; b + W < a.nb; b += 2 * W) {
             load(0, b);
-            load(1, b + KW);
+            load(1, b + W);
             mma(0);
             mma(1);
         }
@@ -384,14 +375,13 @@ __global__ __launch_bounds__(64 * KW) void gemm_f8_stream_kernel(GArgs a) {
             load(0, b);
             mma(0);
         }
-#pragma unroll
-        for (int c = 0; c < NB; ++c) part[wave][c][lane] = acc[c];
+        part[wave][lane] = acc;
         __syncthreads();
-        if (wave < NB) {
-            const int c = wave, n = c0 + 16 * c + (lane & 15), m = (t >> 1) * kPair + (lane >> 4) * 8 + (t & 1) * 4;
-            qg_f4 s = part[0][c][lane];
+        if (wave == 0) {
+            const int m = (t >> 1) * kPair + (lane >> 4) * 8 + (t & 1) * 4;
+            qg_f4 s = part[0][lane];
 #pragma unroll
-            for (int k = 1; k < KW; ++k) s += part[k][c][lane];
+            for (int k = 1; k < W; ++k) s += part[k][lane];
             if (n < g.r1 && m < a.M) {
                 float sb[4], y[4];
                 row_bias(a, g.e, m, sb);
@@ -1207,7 +1197,7 @@ qg_status launch_gemm(const GArgs& a, const Plan& p, hipStream_t s) {
             if constexpr (YT != QG_F32) return launch_turns<YT, 256, 256, 2, 4, 2, 2, false>(a, p, s);
             break;
     }
-    hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), dim3(a.mtiles), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((gemm_f8_stream_kernel<YT>), dim3(a.mtiles), dim3(64 * kStreamWaves), 0, s, a);
     return qg::launch_status("qgemm_f8");
 }
 
@@ -1225,7 +1215,7 @@ qg_status launch_grouped(const GArgs& a, hipStream_t s) {
         return (int)(std::min<int64_t>(a.N, a.N / bn + used) * qg::ceil_div(a.mtiles * 16, bm));
     };
     if (each <= 4 && used * qg::ceil_div(a.mtiles * 16, 64) <= 256) {
-        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT, 1, 8>), dim3(a.mtiles, (unsigned)used), dim3(512), 0, s, a);
+        hipLaunchKernelGGL((gemm_f8_stream_kernel<YT>), dim3(a.mtiles, (unsigned)used), dim3(64 * kStreamWaves), 0, s, a);
         return qg::launch_status("qgemm_f8_grouped");
     }
     if (each <= 2) {
