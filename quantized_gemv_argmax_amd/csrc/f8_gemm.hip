@@ -191,13 +191,15 @@ __global__ __launch_bounds__(256) void quantize_f8_kernel(QArgs a) {
         // top / 448 rounded to nearest: the product with 1/448 and its exact remainder's correction
         const float q0 = top * (1.f / 448.f);
         float d = __builtin_fmaf(__builtin_fmaf(-448.f, q0, top), 1.f / 448.f, q0);
-        const bool tiny = d < 0x1p-90f;  // (the remainder could be subnormal, and 1/d infinite)
-        if (tiny) d = top / 448.f;
         if (!finite) d = __builtin_nanf("");
-        uint2 o = quant8(x, d, tiny ? 0.f : __builtin_amdgcn_rcpf(d));
-        if (__ballot(tiny && d > 0.f)) {
+        uint2 o = quant8(x, d, __builtin_amdgcn_rcpf(d));
+        const bool tiny = d < 0x1p-90f && top > 0.f;  // (the remainders could be subnormal, and 1/d infinite)
+        if (__ballot(tiny)) {
             asm volatile("");
-            if (tiny && d > 0.f) o = quant8_tiny(x, d);
+            if (tiny) {
+                d = top / 448.f;
+                o = quant8_tiny(x, d);
+            }
         }
         if (!(d > 0.f)) o = make_uint2(0, 0);
         const bool in = b * kB < a.K;
