@@ -1,7 +1,7 @@
 // Selection of experts and the weighted sum of their outputs, for gfx950: what a
 // mixture-of-experts layer runs before and after its grouped products.
 //
-// The selection ranks each row of E logits in one wavefront and orders the rows by
+// The selection ranks each row of E logits within sixteen lanes and orders the rows by
 // expert without atomics whose order could change the result: 32 rows are a word of a
 // bit map per expert, so a row's place among an expert's rows is a count of bits.
 #include <algorithm>
@@ -342,8 +342,9 @@ QG_DEV float get8(const uint4 (&v)[8 / XVec<XT>::N], int e) {
     return XVec<XT>::get(v[e / XVec<XT>::N], e % XVec<XT>::N);
 }
 
-// Eight columns of a row per thread; the rows it adds are all on their way at once, eight
-// at a time.
+// out = (add +) sum_j weight_j Y[position_j], in float32, in the order of j. Eight columns of a
+// row per thread; the rows it adds are all on their way at once, eight at a time. Bound by
+// memory: 4096 rows of 8 by 2048 bf16 onto a residual take 34 us, 168 MB at 4.9 TB/s.
 template <int YT, int OT>
 __global__ __launch_bounds__(256) void combine_kernel(CArgs a) {
     typedef typename XVec<YT>::E E;

@@ -29,7 +29,8 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 // ---------------------------------------------------------------- weight layout
 // Operands in pairs of 32 weight rows: row r of operand i of a pair is the weight row 8 (r /
 // 4) + 4 i + r % 4, so that a lane, which gets four rows of a product, gets eight
-// consecutive ones of a pair's.
+// consecutive ones of a pair's. Once per model; bound by memory (37888 x 3584: 43 us, 6.3 TB/s read and
+// written; 128 x 1536 x 2048: 146 us, 5.5).
 __global__ __launch_bounds__(256) void pack_f8_kernel(const uint8_t* __restrict__ src, int64_t ldw, int64_t w_expert,
                                                       uint4* __restrict__ dst, int64_t M, int K, int nb,
                                                       int64_t mtiles, int64_t units) {
@@ -147,10 +148,10 @@ struct QArgs {
 
 // A block's scale is d = max |x| / 448, its values are x / d rounded to e4m3, ties to even.
 // Sixteen lanes per block, a wavefront per four blocks of a row: one pass, every value read
-// once and in flight at once on the card (four groups to a wavefront at a time, with their loads ahead, took
-// 89 us for 4096 x 18944 gated bf16 and 4.9 for 64 x 3584, where this takes 83.5 and 3.0). Bound
-// by memory and, gated, nearly as much by its instructions: 86 us and 4.5 TB/s in a row of
-// calls, plain 61 us.
+// once (four groups to a wavefront at a time, with their loads ahead, took 90 us for 4096 x
+// 18944 gated bf16 and 4.9 for 64 x 3584, where this takes 84 and 3.0). Bound by memory (gated
+// 388 MB, 4.6 to 5.0 TB/s) and by nearly as many cycles of instructions, which is what the plain
+// form's 59 us (233 MB, 3.9 TB/s) are bound by.
 template <int XT, bool GATED>
 __global__ __launch_bounds__(256) void quantize_f8_kernel(QArgs a) {
     typedef typename XVec<XT>::E E;
@@ -319,7 +320,11 @@ QG_DEV void row_bias(const GArgs& a, int e, int m, float (&sb)[C]) {
 // ---------------------------------------------------------------- few rows
 // One 16-row tile of an expert's weights and 16 rows of Y after the other per workgroup; its
 // wavefronts take blocks of K in turn, and their sums meet in LDS, in order. The weights go
-// from memory straight to registers, in the packed order, and are what bounds it.
+// from memory straight to registers, in the packed order, and are what bounds it: latency
+// where they are few (4608 x 3584 by 1: 6.2 us, 16.5 MB in 3.5 at the copy's rate; 8 of 128 experts of
+// 1536 x 2048, one token: 9.4 us, of which the offsets, the weights and the joining of sums are one
+// round trip after the other), memory where they are many (152064 x 3584 by 1: 87 us, 6.3 TB/s).
+// Products are exact on the fp16 cores, whose rate does not matter here.
 constexpr int kStreamWaves = 8;
 template <int YT>
 __global__ __launch_bounds__(64 * kStreamWaves) void gemm_f8_stream_kernel(GArgs a) {
@@ -633,7 +638,11 @@ QG_DEV Operand<YT> operand(const Op8& o) {
     return v;
 }
 
-// Tiles of up to 128, several workgroups to a compute unit, whose starts and ends overlap.
+// Tiles of up to 128, several workgroups to a compute unit, whose starts and ends overlap. A K
+// tile's products run between the loads of the one NS - 1 ahead; a pair of weight operands is
+// read from LDS while the one before is multiplied. Few rows to an expert are bound by
+// memory (128 experts of 2048 x 768, 8 to each of 256 tokens: 44 us, 201 MB of weights at 4.6
+// TB/s), few tiles by the latency of their K tiles (4608 x 3584 by 32: 11.0 us).
 template <int YT, int BM, int BN, int WM, int WN, int NS, bool SPLIT, bool GROUPED>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
     typedef F8Tile<BM, BN, WM, WN, NS, 1, 8, 2> G;
@@ -821,6 +830,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
 // turn and the next one's first, in a known number of stores, so that waits for loads sent
 // before them can leave them on their way; where the last columns of Y make that number
 // unknown, the loads come first.
+// Bound by the reads that the L1 has on their way, about 64 lines at a time: 9 TB/s over the card
+// at the L2's latency. So tiles of 256 beat 256 x 128 where they fit (37888 x 3584 by 4096: 495 to 510 us,
+// 2200 TFLOP/s, matrix cores busy 58% of the cycles), and groups of 256 rows +- 16, which take two
+// and a half tiles of 128, are where this costs most (128 experts of 1536 x 2048: 166 us, busy
+// 40%; 512 MB, 108 us at the copy's rate).
 constexpr int kTurnsBlocks = 4;     // the least blocks of K: the next tile's rows are known after two
 constexpr int kTurnsExperts = 512;  // the most experts that leave room in LDS
 template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool GROUPED>
@@ -890,8 +904,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
     };
     auto turn_end = [&](auto reads, auto loads) {
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (decltype(reads)::value >= 0) asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(decltype(reads)::value) : "memory");
-        if constexpr (decltype(loads)::value >= 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(decltype(loads)::value) : "memory");
+        constexpr int R = decltype(reads)::value, V = decltype(loads)::value;
+        if constexpr (R >= 0) asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(R) : "memory");
+        if constexpr (V >= 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(V) : "memory");
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -977,7 +992,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
             more = tile_of(next);
             if (more && L.gathers()) {
                 const int unit = wave % (BN / 64);
-                const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc((void*)a.row, (short)0, a.N * 4, kQgRawBufferFlags);
+                const __amdgpu_buffer_rsrc_t rr =
+                    __builtin_amdgcn_make_buffer_rsrc((void*)a.row, (short)0, a.N * 4, kQgRawBufferFlags);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, (lds_ptr)(next_rows + unit * 64), 4,
                                                          min(next.n0 + unit * 64 + lane, next.n1 - 1) * 4, 0, 0, 0);
             }
@@ -1040,7 +1056,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_turns_kernel(GArgs a) {
 }
 
 // The partial sums of a split product added in order and stored: one wavefront per pair
-// of a tile wavefront's products.
+// of a tile wavefront's products. A launch of its own (4 to 5 us in a trace), so that a
+// workspace needs no preparation and no sum depends on who arrives last.
 template <int YT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64) void gemm_f8_join_kernel(GArgs a, int tiles, int splits) {
     typedef Tile<BM, BN, WM, WN, 2> G;
