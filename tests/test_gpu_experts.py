@@ -228,3 +228,25 @@ def test_layer_on_another_stream():
                 outs.append(layer(x, z, *args))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_one_workspace_of_any_contents():
+    """Selections that count, that do not and that need none, and products split along K, in turn on one workspace
+    that holds garbage before every call."""
+    ws = qg.Workspace(DEV, 1 << 24)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    w = (torch.randn(300, 9000, generator=g, device=DEV) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    wp, wsc = qg.pack_f8(w), torch.rand(3, 71, generator=g, device=DEV) + 0.5
+    case("one workspace of any contents")
+    for N, E, k, cols in [(9000, 40, 3, 100), (300, 200, 8, 20), (40, 64, 2, 300), (20000, 16, 1, 70)]:
+        z = torch.randn(N, E, generator=g, device=DEV)
+        xq, xs = qg.quantize_f8_rows(torch.randn(cols, 9000, generator=g, device=DEV))
+        want, y = qg.logits_expert_select(z, k), qg.qgemm_f8(wp, wsc, xq, xs, 300, 9000)[:, :300].clone()
+        for fill in (0xff, 0x01, 0x80):
+            ws.buf.fill_(fill)
+            r = qg.logits_expert_select(z, k, ws=ws)
+            for name in ("expert", "weight", "position", "row", "offsets"):
+                assert torch.equal(getattr(r, name), getattr(want, name)), (N, E, k, name)
+            ws.buf.fill_(fill)
+            assert torch.equal(qg.qgemm_f8(wp, wsc, xq, xs, 300, 9000, ws=ws)[:, :300], y), cols
+    assert not ws.outgrown
