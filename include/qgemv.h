@@ -605,7 +605,9 @@ qg_status qg_beam_reorder_check(const qg_beam_state* states /* host */, int coun
  *
  * qg_quantize_f8_rows quantizes rows of fp32, fp16 or bf16 (row n at x + n * ldx
  * elements): of K values x, or with gated = 1 of 2 K values g and u that enter as
- * g / (1 + exp(-g)) * u in float32. scale[n, b] = max |.| / 448 over block b, rounded to
+ * g / (1 + exp(-g)) * u in float32: the quotient to a few units in the last place, or to a
+ * step of 2^-149 below the normal floats (also where exp(-g) alone passes float32; NaN for g = -infinity),
+ * then its product with u, rounded. scale[n, b] = max |.| / 448 over block b, rounded to
  * float32; q = x / scale rounded to the nearest e4m3 value, ties to even, decided on the
  * exact quotient and clamped to +-448 (0 where the scale is 0). Bytes K .. round_up(K,
  * 128) - 1 of each row of q and the scales up to a multiple of 4 blocks are set to 0;

@@ -124,14 +124,27 @@ QG_DEV uint2 quant8(const float (&x)[8], float d, float inv) {
 }
 
 // z / (1 + exp(-z)): the exponential by a power of two, whose argument's rounding error is
-// added back; within a few units in the last place.
+// added back; within a few units in the last place. For |z| below kFarGate: the exponential and
+// 1 + it stay normal and the sum's reciprocal too (the hardware's is zero below 2^-126).
+constexpr float kFarGate = 87.f;
 QG_DEV float silu(float z) {
     const float p = z * -1.44269504f;
     const float e = __builtin_amdgcn_exp2f(p);
-    // (where e is infinite or zero, its correction would not be a number)
     const float low = __builtin_fmaf(z, -1.44269504f, -p) + z * -1.925963033e-8f;
-    const float c = p < 126.f && p > -126.f ? __builtin_fmaf(e * 0.693147181f, low, e) : e;
-    return z * __builtin_amdgcn_rcpf(1.f + c);
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_fmaf(e * 0.693147181f, low, e));
+}
+// The same for any z: from exponentials of 2^64 on with numerator and denominator times 2^-64,
+// so that they last until the quotient itself is below the floats (z = -190 / log2(e)); below the normal
+// floats it is rounded to their step. As the formula has it, zero beyond and NaN for -infinity.
+QG_DEV float silu_far(float z) {
+#pragma clang fp contract(off)  // (p - 64 is exact for the rounded p, whose error is what `low` adds)
+    const float p = z * -1.44269504f;
+    const float one = p > 64.f ? 0x1p-64f : 1.f, q = p > 64.f ? p - 64.f : p;
+    const float e = __builtin_amdgcn_exp2f(q);
+    // (where e is infinite or zero, its correction would not be a number)
+    const float low = __builtin_fmaf(z, -1.925963033e-8f, __builtin_fmaf(z, -1.44269504f, -p));
+    const float c = q < 128.f && q > -126.f ? __builtin_fmaf(e * 0.693147181f, low, e) : e;
+    return z * __builtin_amdgcn_rcpf(one + c) * one;
 }
 
 struct QArgs {
@@ -169,7 +182,23 @@ __global__ __launch_bounds__(256) void quantize_f8_kernel(QArgs a) {
             v[i] = row_vec<XT>(GATED ? p + a.K : p, a.K, k / VN + i);
             if constexpr (GATED) g[i] = row_vec<XT>(p, a.K, k / VN + i);
         }
-        float x[8];
+        float x[8], z[8];
+        if constexpr (GATED) {
+            float far = 0.f;  // (a NaN among the gates needs no care)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                z[e] = XVec<XT>::get(g[e / VN], e % VN);
+                far = fmaxf(far, fabsf(z[e]));
+            }
+            if (__ballot(far >= kFarGate)) {
+                asm volatile("");
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = silu_far(z[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = silu(z[e]);
+            }
+        }
         uint32_t mx = 0;  // the largest |x| by its bits: above every finite value an infinity, above it a NaN
         if constexpr (!GATED && VN == 8) {
             // 16-bit values in pairs
@@ -183,7 +212,7 @@ __global__ __launch_bounds__(256) void quantize_f8_kernel(QArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[e] = XVec<XT>::get(v[e / VN], e % VN);
-            if constexpr (GATED) x[e] *= silu(XVec<XT>::get(g[e / VN], e % VN));
+            if constexpr (GATED) x[e] *= z[e];
             if constexpr (GATED || VN == 4) mx = max(mx, __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu);
         }
         mx = row_max(mx);
