@@ -590,8 +590,9 @@ qg_status qg_beam_reorder_check(const qg_beam_state* states /* host */, int coun
  * keep 13 bits below its leading one: its error is below 2^-10 * sum |xq * wq| (measured:
  * 1.5e-5 of the result for normally distributed values, 2^-12 of the sum of magnitudes at
  * worst for random bytes), under the rounding of the output where the sum does
- * not cancel. Results are deterministic; they may differ in the last bits between
- * numbers of rows, which run in different forms.
+ * not cancel; where it does, take float32. Results are deterministic. Different numbers of
+ * rows run in different forms, whose results differ within these bounds: with float32 Y
+ * in the order of additions, with fp16 or bf16 Y by that error too, as few rows have exact products.
  *
  * qg_pack_f8 lays the weights out once, at load time: `experts` matrices (1 for a dense
  * product) of M rows of K bytes, rows ldw >= K bytes apart, matrices w_expert bytes apart

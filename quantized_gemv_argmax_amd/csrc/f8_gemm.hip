@@ -162,9 +162,9 @@ struct QArgs {
 // A block's scale is d = max |x| / 448, its values are x / d rounded to e4m3, ties to even.
 // Sixteen lanes per block, a wavefront per four blocks of a row: one pass, every value read
 // once (four groups to a wavefront at a time, with their loads ahead, took 90 us for 4096 x
-// 18944 gated bf16 and 4.9 for 64 x 3584, where this takes 84 and 3.0). Bound by memory (gated
-// 388 MB, 4.6 to 5.0 TB/s) and by nearly as many cycles of instructions, which is what the plain
-// form's 59 us (233 MB, 3.9 TB/s) are bound by.
+// 18944 gated bf16 where one took 84, and 4.9 for 64 x 3584 where it took 3.0). Bound by memory and by
+// as many cycles of instructions: that gated case 71 to 73 us in a trace, up to 87 in a row of calls
+// (390 MB, 4.5 to 5.5 TB/s), the plain one 59 us (235 MB, 4.0 TB/s) by the instructions.
 template <int XT, bool GATED>
 __global__ __launch_bounds__(256) void quantize_f8_kernel(QArgs a) {
     typedef typename XVec<XT>::E E;
@@ -865,10 +865,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f8_tile_kernel(GArgs a) {
 // before them can leave them on their way; where the last columns of Y make that number
 // unknown, the loads come first.
 // Bound by the reads that the L1 has on their way, about 64 lines at a time: 9 TB/s over the card
-// at the L2's latency. So tiles of 256 beat 256 x 128 where they fit (37888 x 3584 by 4096: 495 to 510 us,
-// 2200 TFLOP/s, matrix cores busy 58% of the cycles), and groups of 256 rows +- 16, which take two
-// and a half tiles of 128, are where this costs most (128 experts of 1536 x 2048: 166 us, busy
-// 40%; 512 MB, 108 us at the copy's rate).
+// at the L2's latency. So tiles of 256 beat 256 x 128 where they fit (37888 x 3584 by 4096: 492 to 529 us
+// on several cards, 2100 to 2260 TFLOP/s, matrix cores busy 58% of the cycles). Experts whose rows are
+// few and uneven are where this costs most: 32768 rows over 128 experts of 1536 x 2048, 256 in the
+// mean and from 2 to 1400, are 1920 tiles of 256 x 128, a quarter of their rows padding, and 1.5 GB
+// (163 to 171 us, busy 40%; memory alone 82 us). In tiles of 256 they are 1.25 GB but 55% more rows than there are.
 constexpr int kTurnsBlocks = 4;     // the least blocks of K: the next tile's rows are known after two
 constexpr int kTurnsExperts = 512;  // the most experts that leave room in LDS
 template <int YT, int BM, int BN, int WM, int WN, int NS, int H, bool GROUPED>
